@@ -43,6 +43,8 @@ EXPORTS = (
     "lora_debug_gather", "lora_debug_decode", "lora_debug_block_timeline", "lora_last_error",
     "lora_store_create",
     "lora_store_destroy", "lora_store_add", "lora_store_ensure", "lora_store_get_stats",
+    "lora_kv_layout", "lora_kv_write", "lora_kv_read", "lora_kv_attend_workspace_size",
+    "lora_kv_attend", "lora_spec_verify_workspace_size", "lora_spec_verify",
 )
 
 
@@ -79,6 +81,29 @@ class PlanStats(ctypes.Structure):
                 ("mfma_tokens", ctypes.c_int32), ("l_long", ctypes.c_int32)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scales_dev", ctypes.c_void_p)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("q_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
+                ("table_dev", ctypes.c_void_p)]
+
+
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("n_drafts", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("target_ld", ctypes.c_int64), ("draft_ld", ctypes.c_int64),
+                ("q_start_dev", ctypes.c_void_p), ("drafted_dev", ctypes.c_void_p),
+                ("target_dev", ctypes.c_void_p), ("draft_dev", ctypes.c_void_p),
+                ("u_accept_dev", ctypes.c_void_p), ("u_sample_dev", ctypes.c_void_p),
+                ("tokens_dev", ctypes.c_void_p), ("n_out_dev", ctypes.c_void_p)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError("%s is not built: run `python gather_lora_matmul_amd/build.py`" % LIB_PATH)
@@ -92,6 +117,7 @@ def _load() -> ctypes.CDLL:
         pass
     lib = ctypes.CDLL(LIB_PATH)
     V, I32, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    SZ, KV, KB = ctypes.c_size_t, ctypes.POINTER(KvDesc), ctypes.POINTER(KvBatchDesc)
     sig = {
         "lora_pool_create": [ctypes.POINTER(PoolDesc), ctypes.POINTER(V)],
         "lora_pool_destroy": [V],
@@ -135,6 +161,13 @@ def _load() -> ctypes.CDLL:
         "lora_apply_noalloc": [V, V, I32, ctypes.POINTER(Io), I32, V],
         "lora_debug_resolve": [V, I32, V, I32, V, V, V],
         "lora_debug_gather": [V, I32, I32, V, V, V],
+        "lora_kv_layout": [V, KV, ctypes.POINTER(I32), ctypes.POINTER(I32), ctypes.POINTER(SZ)],
+        "lora_kv_write": [V, KV, KB, V, V, I64, V],
+        "lora_kv_read": [V, KV, KB, V, V, I64, V],
+        "lora_kv_attend_workspace_size": [V, KV, KB, I32, ctypes.POINTER(SZ)],
+        "lora_kv_attend": [V, KV, KB, V, I64, I32, F, I32, V, I64, V, V, SZ, V],
+        "lora_spec_verify_workspace_size": [I32, I32, ctypes.POINTER(SZ)],
+        "lora_spec_verify": [ctypes.POINTER(VerifyDesc), V, SZ, V],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -595,6 +628,128 @@ def lora_apply_noalloc(pool: int, plan: int, ios: Sequence[Tuple[int, object, ob
 
 
 # ----------------------------------------------------------------------------
+# KV cache in the unified pool, attention, verification of drafted tokens
+# ----------------------------------------------------------------------------
+def lora_kv_layout(pool: int, n_kv_heads: int, head_dim: int, dtype: int) -> Tuple[int, int, int]:
+    """-> (tokens per page, pages per block of that many tokens, bytes of the
+    FP8 scales) of a cache in this pool."""
+    d = KvDesc(int(n_kv_heads), int(head_dim), int(dtype), None)
+    t, p, b = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
+    _check(_lib.lora_kv_layout(pool, ctypes.byref(d), ctypes.byref(t), ctypes.byref(p), ctypes.byref(b)),
+           "lora_kv_layout")
+    return t.value, p.value, int(b.value)
+
+
+class KvCache:
+    """A KV cache in a pool's pages: lora_kv_desc with the geometry that follows
+    from it.  scales: for FP8 caches, a uint8 device tensor of scale_bytes
+    elements ([n_pages][tokens_per_page]), kept alive here."""
+
+    def __init__(self, pool: int, n_kv_heads: int, head_dim: int, dtype: int, scales=None):
+        import torch
+        self.pool, self.scales = pool, scales
+        self.tokens_per_page, self.pages_per_block, self.scale_bytes = lora_kv_layout(
+            pool, n_kv_heads, head_dim, dtype)
+        if self.scale_bytes:
+            _check_tensor(scales, "scales", None, self.scale_bytes)
+            if scales.dtype != torch.uint8:
+                raise TypeError("scales: dtype %s, expected uint8" % scales.dtype)
+        self.desc = KvDesc(int(n_kv_heads), int(head_dim), int(dtype),
+                           _dev_ptr(scales) if self.scale_bytes else None)
+        info = _POOLS.get(pool)
+        self.act = info[0] if info else None
+
+
+class KvBatch:
+    """The sequences of one call (lora_kv_batch): int32 device tensors q_start
+    [n_seqs + 1], kv_len [n_seqs] and table [n_seqs][2][n_kv_heads][max_blocks],
+    read by the calls that use it (kept alive here).  Their contents may change
+    between calls; n_tokens and max_q_len are bounds."""
+
+    def __init__(self, q_start, kv_len, table, n_tokens: int, max_q_len: int):
+        import torch
+        for t, what in ((q_start, "q_start"), (kv_len, "kv_len"), (table, "table")):
+            if t.dtype != torch.int32:
+                raise TypeError("%s: dtype %s, expected int32" % (what, t.dtype))
+        n = int(kv_len.numel())
+        if q_start.numel() < n + 1:
+            raise ValueError("q_start: %d entries for %d sequences" % (q_start.numel(), n))
+        if table.dim() != 4 or table.shape[0] != n or table.shape[1] != 2:
+            raise ValueError("table: shape %s, expected [%d][2][n_kv_heads][max_blocks]" % (tuple(table.shape), n))
+        self.q_start, self.kv_len, self.table = q_start, kv_len, table
+        self.desc = KvBatchDesc(n, int(n_tokens), int(max_q_len), int(table.shape[3]), _dev_ptr(q_start),
+                                _dev_ptr(kv_len), _dev_ptr(table))
+
+
+def _kv_rows(cache: KvCache, batch: KvBatch, t, what: str, heads: Optional[int] = None):
+    """(pointer, elements between tokens) of a [n_tokens][heads][head_dim] tensor."""
+    d = cache.desc
+    if cache.act is not None:
+        _check_tensor(t, what, cache.act, 0)
+    if t.dim() != 3 or t.shape[2] != d.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s: shape %s, expected [n_tokens][%s][%d]" % (
+            what, tuple(t.shape), "heads" if heads is None else heads, d.head_dim))
+    if t.shape[0] < batch.desc.n_tokens:
+        raise ValueError("%s: %d rows for %d tokens" % (what, t.shape[0], batch.desc.n_tokens))
+    if not t.is_cuda:
+        raise ValueError("expected a device tensor")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d.head_dim):
+        raise ValueError("%s: a token's heads must be contiguous" % what)
+    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), t.shape[1] * d.head_dim)
+
+
+def _kv_copy_args(cache: KvCache, batch: KvBatch, k, v):
+    if batch.table.shape[2] != cache.desc.n_kv_heads:
+        raise ValueError("table: %d heads, the cache has %d" % (batch.table.shape[2], cache.desc.n_kv_heads))
+    kp, ld = _kv_rows(cache, batch, k, "k", cache.desc.n_kv_heads)
+    vp, vld = _kv_rows(cache, batch, v, "v", cache.desc.n_kv_heads)
+    if ld != vld:
+        raise ValueError("k and v rows must have one stride")
+    return (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), kp, vp, ld)
+
+
+def lora_kv_write(cache: KvCache, batch: KvBatch, k, v, stream=None):
+    """k, v [n_tokens][n_kv_heads][head_dim] to their places in the pages."""
+    prepare_kv_write(cache, batch, k, v)(stream)
+
+
+def lora_kv_read(cache: KvCache, batch: KvBatch, k, v, stream=None):
+    """The cached rows of the batch's tokens into k, v."""
+    prepare_kv_read(cache, batch, k, v)(stream)
+
+
+def lora_kv_attend_workspace_size(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_kv_attend_workspace_size(cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc),
+                                              int(n_q_heads), ctypes.byref(out)),
+           "lora_kv_attend_workspace_size")
+    return int(out.value)
+
+
+def lora_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window: int = 0, lse=None,
+                   workspace=None, stream=None):
+    """out = attention of q [n_tokens][n_q_heads][head_dim] over the cache; lse
+    (optional): float32 [n_tokens][n_q_heads]; workspace: a device tensor of
+    lora_kv_attend_workspace_size bytes."""
+    prepare_kv_attend(cache, batch, q, out, scale, window, lse, workspace)(stream)
+
+
+def lora_spec_verify_workspace_size(n_seqs: int, vocab: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_spec_verify_workspace_size(int(n_seqs), int(vocab), ctypes.byref(out)),
+           "lora_spec_verify_workspace_size")
+    return int(out.value)
+
+
+def lora_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out, workspace,
+                     stream=None):
+    """Verify drafted tokens: q_start [n_seqs + 1], drafted [n_drafts], target
+    [n_tokens][vocab], draft [n_drafts][vocab] or None, u_accept [n_drafts],
+    u_sample [n_seqs]; writes tokens [n_tokens] and n_out [n_seqs]."""
+    prepare_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out, workspace)(stream)
+
+
+# ----------------------------------------------------------------------------
 # prepared calls: arguments checked and marshalled once
 # ----------------------------------------------------------------------------
 class PreparedCall:
@@ -650,6 +805,65 @@ def prepare_apply(pool: int, plan: int, ios: Sequence[Tuple[int, object, object]
     wp, wb = _ws(workspace)
     return PreparedCall(_lib.lora_apply, (pool, plan, len(ios), arr, y_dtype, wp, wb),
                         "lora_apply", (ios, workspace, arr))
+
+
+def prepare_kv_write(cache: KvCache, batch: KvBatch, k, v) -> PreparedCall:
+    return PreparedCall(_lib.lora_kv_write, _kv_copy_args(cache, batch, k, v), "lora_kv_write",
+                        (cache, batch, k, v))
+
+
+def prepare_kv_read(cache: KvCache, batch: KvBatch, k, v) -> PreparedCall:
+    return PreparedCall(_lib.lora_kv_read, _kv_copy_args(cache, batch, k, v), "lora_kv_read",
+                        (cache, batch, k, v))
+
+
+def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window: int = 0, lse=None,
+                      workspace=None) -> PreparedCall:
+    if batch.table.shape[2] != cache.desc.n_kv_heads:
+        raise ValueError("table: %d heads, the cache has %d" % (batch.table.shape[2], cache.desc.n_kv_heads))
+    qp, q_ld = _kv_rows(cache, batch, q, "q")
+    heads = int(q.shape[1])
+    op, out_ld = _kv_rows(cache, batch, out, "out", heads)
+    if lse is not None:
+        _check_tensor(lse, "lse", 0, batch.desc.n_tokens * heads)
+    wp, wb = _ws(workspace)
+    return PreparedCall(_lib.lora_kv_attend,
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, q_ld, heads,
+                         float(scale), int(window), op, out_ld, _dev_ptr(lse), wp, wb),
+                        "lora_kv_attend", (cache, batch, q, out, lse, workspace))
+
+
+def prepare_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out,
+                        workspace) -> PreparedCall:
+    import torch
+    code = {torch.float32: LORA_F32, torch.float16: LORA_F16, torch.bfloat16: LORA_BF16}
+    if target.dtype not in code:
+        raise TypeError("target: dtype %s" % target.dtype)
+    if target.dim() != 2 or target.stride(1) != 1 or not target.is_cuda:
+        raise ValueError("target: expected a device tensor [n_tokens][vocab] with contiguous rows")
+    n_tokens, vocab = (int(x) for x in target.shape)
+    n_drafts, n_seqs = int(drafted.numel()), int(u_sample.numel())
+    if draft is not None:
+        if draft.dtype != target.dtype:
+            raise TypeError("draft: dtype %s, target has %s" % (draft.dtype, target.dtype))
+        if draft.dim() != 2 or tuple(draft.shape) != (n_drafts, vocab) or (n_drafts and draft.stride(1) != 1) \
+                or not draft.is_cuda:
+            raise ValueError("draft: expected a device tensor [%d][%d] with contiguous rows" % (n_drafts, vocab))
+    for t, what, need in ((q_start, "q_start", n_seqs + 1), (drafted, "drafted", n_drafts),
+                          (tokens, "tokens", n_tokens), (n_out, "n_out", n_seqs)):
+        if t.dtype != torch.int32:
+            raise TypeError("%s: dtype %s, expected int32" % (what, t.dtype))
+        _check_tensor(t, what, None, need)
+    _check_tensor(u_accept, "u_accept", 0, n_drafts)
+    _check_tensor(u_sample, "u_sample", 0, n_seqs)
+    ld = [max(int(t.stride(0)), vocab) if t is not None else 0 for t in (target, draft)]
+    d = VerifyDesc(n_seqs, n_tokens, n_drafts, vocab, code[target.dtype], 0, ld[0], ld[1], _dev_ptr(q_start),
+                   _dev_ptr(drafted), target.data_ptr(),
+                   draft.data_ptr() if draft is not None and n_drafts else None, _dev_ptr(u_accept),
+                   _dev_ptr(u_sample), _dev_ptr(tokens), _dev_ptr(n_out))
+    wp, wb = _ws(workspace)
+    return PreparedCall(_lib.lora_spec_verify, (ctypes.byref(d), wp, wb), "lora_spec_verify",
+                        (d, q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out, workspace))
 
 
 # ----------------------------------------------------------------------------

@@ -405,6 +405,135 @@ lora_status lora_dplan_apply(lora_pool* pool, const lora_dplan* dplan, int32_t n
                              const lora_io* io_host, int32_t y_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * KV cache in the unified pool (S-LoRA explainer, "Unified Paging"; serving
+ * article, unified paged pool section: adapters and KV blocks in one pool) and
+ * the decoding step around it: new keys and values are written to pages, the
+ * new tokens attend to the cache, drafted tokens are verified.
+ * ------------------------------------------------------------------------- */
+/* A cache of n_kv_heads heads of head_dim (64 or 128) elements in pages of this
+ * pool (taken with lora_pool_alloc_pages).  dtype: the pool's act_dtype
+ * (LORA_F16 or LORA_BF16), or LORA_FP8_E4M3 codes with a power-of-two scale per
+ * token and head.  A page holds T tokens' K or V rows of one head: with elt
+ * bytes an element and E = 16 / elt, T = floor(page bytes / (head_dim * elt))
+ * rounded down to a multiple of E.  Element d of token slot t lies
+ *   in a K page at ((d / E) * T + t) * E + d % E,
+ *   in a V page at ((t / E) * head_dim + d) * E + t % E
+ * (elements; a page's tail stays unused). */
+typedef struct {
+  int32_t n_kv_heads;      /* 1..256                                             */
+  int32_t head_dim;        /* 64 or 128                                          */
+  int32_t dtype;           /* lora_dtype of the cached elements                  */
+  uint8_t* scales_dev;     /* FP8: [n_pages][T] exponent bytes by page id and
+                              token slot (16-byte aligned, caller-owned); a
+                              code c of slot t stands for c * 2^(byte - 127).
+                              NULL otherwise                                     */
+} lora_kv_desc;
+
+/* The sequences of one call.  Sequence s has q_start[s + 1] - q_start[s] new
+ * tokens, rows q_start[s].. of the call's token-major tensors, and kv_len[s]
+ * cached tokens, its new ones included and last: new token t is at position
+ * kv_len[s] - q_len + t.  table [n_seqs][2][n_kv_heads][max_blocks]: page ids of
+ * the sequence's K (0) and V (1) blocks of T tokens.  All three are read on the
+ * device and never trusted: rows outside [0, n_tokens] and positions past the
+ * table's max_blocks * T are cut off, and tokens whose K or V page id lies
+ * outside [0, n_pages) (e.g. -1: given back, or never there) are absent.
+ * max_q_len: the longest q_len (a bound for workspaces and the choice of
+ * kernels; results do not depend on it). */
+typedef struct {
+  int32_t n_seqs;          /* 0..1024                                            */
+  int32_t n_tokens;        /* rows of the new tensors, 0..2^24                   */
+  int32_t max_q_len;       /* 0..n_tokens                                        */
+  int32_t max_blocks;      /* >= 1, max_blocks * T <= 2^28                       */
+  const int32_t* q_start_dev;  /* [n_seqs + 1], ascending                        */
+  const int32_t* kv_len_dev;   /* [n_seqs]                                       */
+  const int32_t* table_dev;
+} lora_kv_batch;
+
+/* Tokens of a page (T), pages of one block of T tokens (2 n_kv_heads) and bytes
+ * of scales_dev (0 unless FP8); any of the outputs may be NULL.  Works on
+ * host-only pools.  LORA_E_UNSUPPORTED: other head_dim, pools of fp32. */
+lora_status lora_kv_layout(const lora_pool* pool, const lora_kv_desc* kv, int32_t* tokens_per_page,
+                           int32_t* pages_per_block, size_t* scale_bytes);
+/* Write the new tokens' rows k, v [n_tokens][n_kv_heads][head_dim] (act_dtype,
+ * ld elements between tokens, ld % 8 == 0, 16-byte aligned) to their places.
+ * FP8: a row x of one token and head gets the smallest exponent e in [-126,
+ * 127] with 448 * 2^e >= max |x| over its finite elements, and the codes
+ * e4m3(x * 2^-e), nearest even; elements that are not finite become NaN codes.
+ * Tokens at negative positions and in absent pages are dropped.  No page may
+ * be named twice by the tokens written. */
+lora_status lora_kv_write(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                          const void* k_dev, const void* v_dev, int64_t ld, void* stream);
+/* The reverse: the cached rows of the batch's tokens (the last q_len of each
+ * sequence) into k, v, act_dtype; FP8 values c * 2^e are rounded once.  Rows of
+ * absent pages become zero, rows of tokens at negative positions are left. */
+lora_status lora_kv_read(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                         void* k_dev, void* v_dev, int64_t ld, void* stream);
+/* Bytes of caller-owned workspace of lora_kv_attend for this batch's max_q_len:
+ * the partial results of tiles that several blocks share. */
+lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
+                                          const lora_kv_batch* batch, int32_t n_q_heads,
+                                          size_t* bytes);
+/* Attention of the batch's new tokens over their sequences' cached ones (which
+ * include them: write first).  q, out [n_tokens][n_q_heads][head_dim] in
+ * act_dtype, q_ld / out_ld elements between tokens (multiples of 8, 16-byte
+ * aligned rows; out may not overlap q); query head h reads kv head
+ * h / (n_q_heads / n_kv_heads).  The token at position i sees the present tokens
+ * j with j <= i and, if window > 0, j > i - window:
+ *   out_i = sum_j p_ij v_j,  p_i. = softmax of scale * q_i . k_j over those j
+ * in fp32, with p rounded to 16 bits (FP8 caches: bf16) for the products with v,
+ * and one rounding at the store.  A token that sees none gets zeros.  What is
+ * not seen has no influence, whatever it holds.  lse (optional, NULL)
+ * [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j), -inf for none.  Rows
+ * of q that belong to no sequence are not written.  Stream-ordered, no host
+ * wait, no allocation (graph-capturable); workspace_dev: 256-byte aligned, at
+ * least lora_kv_attend_workspace_size bytes, no initial contents; calls that
+ * share one must not overlap.  Runs of one batch give the same bits. */
+lora_status lora_kv_attend(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                           const void* q_dev, int64_t q_ld, int32_t n_q_heads, float scale,
+                           int32_t window, void* out_dev, int64_t out_ld, float* lse_dev,
+                           void* workspace_dev, size_t ws_bytes, void* stream);
+
+/* Verification of drafted tokens (speculative decoding, serving article, FAQ).
+ * Sequence s has the rows q_start[s] .. q_start[s + 1] - 1 of the target's
+ * probabilities: one per drafted token and one after the last (k + 1 rows for k
+ * drafted tokens; none: the sequence is idle).  The drafted tokens and their
+ * rows are dense, without that last one: those of s begin at q_start[s] less the
+ * number of sequences before s that are not idle. */
+typedef struct {
+  int32_t n_seqs;              /* 0..65535                                        */
+  int32_t n_tokens;            /* rows of target, = drafts + active sequences     */
+  int32_t n_drafts;            /* rows of drafted, draft and u_accept             */
+  int32_t vocab;               /* 1..2^18                                         */
+  int32_t dtype;               /* of target and draft: LORA_F32, F16 or BF16      */
+  int32_t reserved;
+  int64_t target_ld;           /* elements between rows, >= vocab                 */
+  int64_t draft_ld;
+  const int32_t* q_start_dev;  /* [n_seqs + 1]                                    */
+  const int32_t* drafted_dev;  /* [n_drafts] token ids                            */
+  const void* target_dev;      /* [n_tokens][target_ld] probabilities             */
+  const void* draft_dev;       /* [n_drafts][draft_ld], or NULL: each drafted token
+                                  was proposed with probability 1                 */
+  const float* u_accept_dev;   /* [n_drafts] uniform numbers in [0, 1)            */
+  const float* u_sample_dev;   /* [n_seqs]                                        */
+  int32_t* tokens_dev;         /* [n_tokens] out: the accepted tokens, then the new
+                                  one, then -1                                    */
+  int32_t* n_out_dev;          /* [n_seqs] out: accepted tokens + 1 (idle: 0)     */
+} lora_verify_desc;
+
+lora_status lora_spec_verify_workspace_size(int32_t n_seqs, int32_t vocab, size_t* bytes);
+/* Drafted token i of a sequence is accepted while u_i * q_i < p_i (its draft and
+ * target probabilities, the product in fp32).  The token after the accepted ones
+ * is drawn with the weights w_v = floor(2^44 max(p_v - q_v, 0)) of the refused
+ * token's rows (the difference in fp32, clamped to [0, 1], NaN: 0), or
+ * floor(2^44 p_v) after the last one or when all of those are 0: the smallest v
+ * with w_0 + .. + w_v > floor(total * floor(2^31 u) / 2^31).  All weights 0: -1.
+ * Whole-number sums: the token depends on no order or split.  An id outside
+ * [0, vocab) is refused.  Stream-ordered, no wait, no allocation; workspace_dev
+ * 16-byte aligned, no initial contents, not shared by calls that overlap. */
+lora_status lora_spec_verify(const lora_verify_desc* desc, void* workspace_dev, size_t ws_bytes,
+                             void* stream);
+
+/* ---------------------------------------------------------------------------
  * Debug / verification of the page-table resolution done inside the kernels.
  * ------------------------------------------------------------------------- */
 /* For token i: a_off[i][k*npa + c] = byte offset (from the pool base) of page
