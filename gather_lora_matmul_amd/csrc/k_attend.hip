@@ -24,6 +24,7 @@
 // wait).  A tile that several blocks share leaves unnormalised partial results in
 // the workspace, and a second launch joins them in block order (run to run the
 // same bits; the cut, and with it the rounding, depends on the batch).
+#include <algorithm>
 #include <type_traits>
 
 #include "kcommon.h"
@@ -33,16 +34,19 @@ namespace lora {
 
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
+__device__ __forceinline__ u32x4 ldv(const void* p) { return *reinterpret_cast<const u32x4*>(p); }
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <typename T>
-__device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, f32x4 c) {
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, f32x4 c) {
   if constexpr (std::is_same<T, bf16_t>::value)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -51,7 +55,7 @@ __device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, f32x4 c)
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 template <typename T>
-__device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 c) {
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, f32x16 c) {
   if constexpr (std::is_same<T, bf16_t>::value)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -62,8 +66,8 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 
 
 // Eight FP8 codes (two words) -> eight 16-bit values, exact.
 template <typename T>
-__device__ __forceinline__ uint4 fp8_to16(uint32_t w0, uint32_t w1) {
-  uint4 r;
+__device__ __forceinline__ u32x4 fp8_to16(uint32_t w0, uint32_t w1) {
+  u32x4 r;
   if constexpr (std::is_same<T, bf16_t>::value) {
     r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false));
     r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true));
@@ -78,8 +82,13 @@ __device__ __forceinline__ uint4 fp8_to16(uint32_t w0, uint32_t w1) {
   return r;
 }
 
+// 2^(byte - 127), less `down` (0 or 1) in the exponent.
+__device__ __forceinline__ float scale_of(uint32_t byte, int down) {
+  return __uint_as_float((byte > (uint32_t)down ? byte - (uint32_t)down : 0u) << 23);
+}
+
 // Element e of eight 16-bit values kept where bit e is set, else zero.
-__device__ __forceinline__ uint4 keep8(uint4 u, uint32_t bits) {
+__device__ __forceinline__ u32x4 keep8(u32x4 u, uint32_t bits) {
   auto m = [](uint32_t b) { return ((b & 1) ? 0xffffu : 0u) | ((b & 2) ? 0xffff0000u : 0u); };
   u.x &= m(bits);
   u.y &= m(bits >> 2);
@@ -93,7 +102,7 @@ __device__ __forceinline__ uint4 keep8(uint4 u, uint32_t bits) {
 // second operand (together 2^-16 of bf16, 2^-22 of f16).  The sums take P
 // unrounded: lse is an fp32 result.
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void p_operand(const float* p, uint4& hi, uint4& lo) {
+__device__ __forceinline__ void p_operand(const float* p, u32x4& hi, u32x4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -101,8 +110,8 @@ __device__ __forceinline__ void p_operand(const float* p, uint4& hi, uint4& lo) 
     if (SPLIT)
       l[i] = pack2<T>(p[2 * i] - bits_to_f<T>(h[i] & 0xffffu), p[2 * i + 1] - bits_to_f<T>(h[i] >> 16));
   }
-  hi = uint4{h[0], h[1], h[2], h[3]};
-  if (SPLIT) lo = uint4{l[0], l[1], l[2], l[3]};
+  hi = u32x4{h[0], h[1], h[2], h[3]};
+  if (SPLIT) lo = u32x4{l[0], l[1], l[2], l[3]};
 }
 
 // Values without a finite number in V must reach the rows that see their token
@@ -111,7 +120,7 @@ __device__ __forceinline__ void p_operand(const float* p, uint4& hi, uint4& lo) 
 // indicator takes their place in a product with the visibility of the tokens,
 // whose result says which rows get that value.
 template <typename T>
-__device__ __forceinline__ uint32_t class_bits(const uint4& u, int cls) {
+__device__ __forceinline__ uint32_t class_bits(const u32x4& u, int cls) {
   constexpr uint32_t kInf = std::is_same<T, bf16_t>::value ? 0x7f80u : 0x7c00u;
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t bits = 0;
@@ -126,10 +135,19 @@ __device__ __forceinline__ uint32_t class_bits(const uint4& u, int cls) {
   }
   return bits;
 }
+// Not zero if one of eight values is not finite: adding one to an exponent of all
+// ones carries into the sign's place.
 template <typename T>
-__device__ __forceinline__ uint4 ones8(uint32_t bits) {
+__device__ __forceinline__ uint32_t not_finite(const u32x4& u) {
+  constexpr uint32_t kExp = std::is_same<T, bf16_t>::value ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = std::is_same<T, bf16_t>::value ? 0x00800080u : 0x04000400u;
+  return (((u.x & kExp) + kOne) | ((u.y & kExp) + kOne) | ((u.z & kExp) + kOne) | ((u.w & kExp) + kOne)) &
+         0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 ones8(uint32_t bits) {
   constexpr uint32_t kOne = std::is_same<T, bf16_t>::value ? 0x3f803f80u : 0x3c003c00u;
-  return keep8(uint4{kOne, kOne, kOne, kOne}, bits);
+  return keep8(u32x4{kOne, kOne, kOne, kOne}, bits);
 }
 __device__ __forceinline__ float class_value(int cls) {
   return __uint_as_float(cls == 0 ? 0x7f800000u : (cls == 1 ? 0xff800000u : 0x7fc00000u));
@@ -154,61 +172,107 @@ struct PartDesc {        // a tile whose last of several parts a block has
   int32_t head, row0, rows, q0, pad;
 };
 
+__device__ __forceinline__ int token_of(const AttendArgs& a, int row) {  // row / group
+  return a.group == 1 ? row : (int)(__umulhi((uint32_t)row, a.group_m) >> a.group_s);
+}
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni(int64_t x) {
+  return (int64_t)(((uint64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x));
+}
+__device__ __forceinline__ int64_t quot(int64_t x, int64_t y) {  // of numbers >= 0
+  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
+
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
 // row's window, down to a multiple of KU, to the last row's own position.
 template <int KU>
 __device__ __forceinline__ void tile_keys(const AttendArgs& a, const KvSeq& q, int row0, int rows,
                                           int& lo, int& hi) {
-  const int t0 = row0 / a.group, t1 = (row0 + rows - 1) / a.group;
+  const int t0 = token_of(a, row0), t1 = token_of(a, row0 + rows - 1);
   const int base = q.kv_len - q.q_len;
   hi = base + t1 + 1;
   lo = 0;
   if (a.window > 0 && base + t0 + 1 - a.window > 0) lo = (base + t0 + 1 - a.window) / KU * KU;
   if (hi <= lo) hi = lo + 1;  // nothing is seen: one unit, all of it masked
 }
-
-// Units of one head of a sequence whose rows are cut into tiles of TR.
 template <int KU, int TR>
-__device__ __forceinline__ int head_units(const AttendArgs& a, const KvSeq& q, int row_lo, int row_hi) {
-  const int64_t rows64 = (int64_t)q.q_len * a.group;
-  if (rows64 < row_lo || rows64 > row_hi || rows64 == 0) return 0;
-  const int rows = (int)rows64;
-  int u = 0;
-  for (int r = 0; r < rows; r += TR) {
-    int lo, hi;
-    tile_keys<KU>(a, q, r, min(TR, rows - r), lo, hi);
-    u += (hi - lo + KU - 1) / KU;
-  }
-  return u;
+__device__ __forceinline__ int tile_units(const AttendArgs& a, const KvSeq& q, int tile) {
+  const int row0 = tile * TR, rows = min(TR, q.q_len * a.group - row0);
+  if (rows <= 0) return 0;
+  int lo, hi;
+  tile_keys<KU>(a, q, row0, rows, lo, hi);
+  return (hi - lo + KU - 1) / KU;
+}
+// Units of the tiles before `tile`, by the whole wave (q and tile uniform).
+__device__ __forceinline__ int wave_add(int x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  return x;
 }
 
 struct Cut {
-  int64_t pos, end, total;   // this block's range of units
+  int64_t pos, end;          // this block's range of units
+  int64_t total, each;       // all units; block L's range begins at L each + min(L, over)
+  int over;
   int block, blocks;         // its number in the order of the ranges, and the blocks that have one
   int seq;
+  __device__ int64_t begin_of(int L) const { return L * each + min(L, over); }
+  __device__ int block_of(int64_t x) const {
+    const int64_t big = (each + 1) * over;
+    return (int)(x < big ? quot(x, each + 1) : over + quot(x - big, each));
+  }
 };
 
 // Prefix sums of the sequences' units in LDS, and this block's range.  Every
-// block computes them itself: the lengths are a few KB that stay in L2.
+// block computes them itself: the lengths are a few KB that stay in L2.  A lane
+// adds up the tiles of its sequence if they are few, all lanes together those of
+// each other one.
 template <int KU, int TR, int THREADS>
-__device__ __forceinline__ void cut_work(const AttendArgs& a, int row_lo, int row_hi, int64_t* pre,
-                                         Cut& c) {
+__device__ __forceinline__ void cut_work(const AttendArgs& a, int64_t* pre, Cut& c) {
   const int n = a.kv.n_seqs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int W = THREADS / 64;
+  constexpr int W = THREADS / 64, FEW = 2;
   int64_t* wsum = pre + kKvMaxSeqs + 1;
   int64_t run = 0;
-  for (int s0 = 0; s0 < n; s0 += THREADS) {
-    const int s = s0 + tid;
-    int64_t x = 0;
-    if (s < n) x = (int64_t)head_units<KU, TR>(a, kv_seq(a.kv, s), row_lo, row_hi) * a.kv.H;
-    int64_t sum = x;
+  const bool small = n <= 64;   // every wave for itself
+  for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
+    const int s = s0 + (small ? lane : tid);
+    int units = 0;
+    KvSeq q{0, 0, 0};
+    if (s < n) q = kv_seq(a.kv, s);
+    const int tiles = (q.q_len * a.group + TR - 1) / TR;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t y = __shfl_up(sum, d);
-      if (lane >= d) sum += y;
+    for (int t = 0; t < FEW; ++t)
+      if (t < tiles) units += tile_units<KU, TR>(a, q, t);
+    for (unsigned long long more = __ballot(tiles > FEW); more; more &= more - 1) {
+      const int src = __builtin_ctzll(more);
+      const KvSeq u{__shfl(q.q0, src), __shfl(q.q_len, src), __shfl(q.kv_len, src)};
+      const int tu = __shfl(tiles, src);
+      int part = 0;
+      for (int t = FEW + lane; t < tu; t += 64) part += tile_units<KU, TR>(a, u, t);
+      part = wave_add(part);
+      if (lane == src) units += part;
     }
-    if (n > 64) {
+    const int64_t x = (int64_t)units * a.kv.H;
+    int64_t sum = x;
+    if (!__ballot(x >> 25)) {
+      int y = (int)x;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int z = __shfl_up(y, d);
+        if (lane >= d) y += z;
+      }
+      sum = y;
+    } else {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int64_t y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+      }
+    }
+    if (!small) {
       if (lane == 63) wsum[wave] = sum;
       __syncthreads();
       int64_t before = run, all = 0;
@@ -220,67 +284,91 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int row_lo, int ro
       run += all;
       __syncthreads();
     } else if (s < n) {
-      pre[s + 1] = sum;
+      pre[s + 1] = sum;   // the same from every wave
     }
   }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
-  c.total = pre[n];
+  if (small ? lane == 0 : tid == 0) pre[0] = 0;
+  if (!small) __syncthreads();
+  c.total = uni(pre[n]);
   // blocks b, b + 8, ... run on one XCD: give each XCD one contiguous eighth of
   // the ranges, so that the tiles that read the same keys share an L2
   const int G = (int)gridDim.x;
   const int b = (int)blockIdx.x;
   c.blocks = c.total < G ? (int)c.total : G;
-  const int each = (c.blocks + 7) >> 3;
-  const int L = (b & 7) * each + (b >> 3);
+  const int per = (c.blocks + 7) >> 3;
+  const int L = (b & 7) * per + (b >> 3);
   c.block = L;
-  if ((b >> 3) >= each || L >= c.blocks) {
-    c.pos = c.end = 0;
-    return;
-  }
-  c.pos = c.total * L / c.blocks;
-  c.end = c.total * (L + 1) / c.blocks;
+  c.pos = c.end = 0;
+  if ((b >> 3) >= per || L >= c.blocks) return;
+  c.each = quot(c.total, c.blocks);
+  c.over = (int)(c.total - c.each * c.blocks);
+  c.pos = c.begin_of(L);
+  c.end = c.begin_of(L + 1);
   // the sequence of the first unit
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= c.pos) lo = mid;
-    else hi = mid;
+  if (small) {
+    c.seq = __popcll(__ballot(lane < n && pre[min(lane, n - 1) + 1] <= c.pos));
+  } else {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= c.pos) lo = mid;
+      else hi = mid;
+    }
+    c.seq = uni(lo);
   }
-  c.seq = lo;
 }
 
 // The next piece of the range; advances c.  Sequences without units are passed.
+// Every wave computes it for itself, with all its lanes.
 template <int KU, int TR>
-__device__ __forceinline__ bool next_piece(const AttendArgs& a, int row_lo, int row_hi,
-                                           const int64_t* pre, Cut& c, Piece& p) {
+__device__ __forceinline__ bool next_piece(const AttendArgs& a, const int64_t* pre, Cut& c, Piece& p) {
   if (c.pos >= c.end) return false;
-  while (pre[c.seq + 1] <= c.pos) ++c.seq;
+  while (uni(pre[c.seq + 1]) <= c.pos) ++c.seq;
   p.seq = c.seq;
   p.q = kv_seq(a.kv, c.seq);
-  const int64_t seq_units = pre[c.seq + 1] - pre[c.seq];
-  const int64_t off = c.pos - pre[c.seq];
-  const int hu = (int)(seq_units / a.kv.H);
-  p.head = (int)(off / hu);
+  p.q.q0 = uni(p.q.q0);
+  p.q.q_len = uni(p.q.q_len);
+  p.q.kv_len = uni(p.q.kv_len);
+  const int64_t before = uni(pre[c.seq]), off = c.pos - before;
+  const int hu = (int)quot(uni(pre[c.seq + 1]) - before, a.kv.H);
+  p.head = (int)quot(off, hu);
   int rem = (int)(off - (int64_t)p.head * hu);
   const int rows = p.q.q_len * a.group;
-  int lo = 0, hi = 0, units = 0;
-  for (p.row0 = 0;; p.row0 += TR) {
-    p.rows = min(TR, rows - p.row0);
-    tile_keys<KU>(a, p.q, p.row0, p.rows, lo, hi);
-    units = (hi - lo + KU - 1) / KU;
-    if (rem < units) break;
-    rem -= units;
+  int tile = 0;
+  if (rows > TR) {
+    const int lane = threadIdx.x & 63;
+    for (;; tile += 64) {
+      int sum = tile_units<KU, TR>(a, p.q, tile + lane);
+      const int own = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int z = __shfl_up(sum, d);
+        if (lane >= d) sum += z;
+      }
+      const unsigned long long past = __ballot(sum > rem);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        rem -= __shfl(sum - own, at);
+        tile += at;
+        break;
+      }
+      rem -= __shfl(sum, 63);
+    }
   }
+  p.row0 = uni(tile) * TR;
+  rem = uni(rem);
+  p.rows = min(TR, rows - p.row0);
+  int lo = 0, hi = 0;
+  tile_keys<KU>(a, p.q, p.row0, p.rows, lo, hi);
+  const int units = (hi - lo + KU - 1) / KU;
   const int64_t left = c.end - c.pos;
   const int take = left < units - rem ? (int)left : units - rem;
   p.begins = rem == 0;
   p.ends = rem + take == units;
   p.key0 = lo + rem * KU;
   p.key1 = p.ends ? hi : p.key0 + take * KU;
-  // the block of the tile's first unit: L with L total / B <= first < (L + 1) total / B
   p.start = c.pos - rem;
-  p.first = (int)(((p.start + 1) * c.blocks - 1) / c.total);
+  p.first = p.begins ? c.block : c.block_of(p.start);
   c.pos += take;
   return true;
 }
@@ -313,7 +401,7 @@ __device__ __forceinline__ void describe(const Parts<TR, D>& parts, const Cut& c
     d.last = c.block;
     d.first = p->first;
     // the first part is its block's first piece iff that block's range begins with the tile
-    d.first_slot = c.total * p->first / c.blocks == p->start ? 0 : 1;
+    d.first_slot = c.begin_of(p->first) == p->start ? 0 : 1;
     d.head = p->head;
     d.row0 = p->row0;
     d.rows = p->rows;
@@ -325,7 +413,7 @@ __device__ __forceinline__ void describe(const Parts<TR, D>& parts, const Cut& c
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- the joining launch ----------------------------------------------------------
-// One wave a row: weights of the parts by their maxima, then a weighted sum.
+// D / 4 lanes a row: weights of the parts by their maxima, then a weighted sum.
 // Bound by the reads of the parts; each is a contiguous D * 4 bytes.
 template <typename A, int D, int TR>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
@@ -333,36 +421,32 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
   const PartDesc d = parts.desc[blockIdx.x];
   const int L = d.last;
   if (L < 0) return;
-  const int lane = threadIdx.x & 63;
-  constexpr int V = D / 64;
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 6); r < d.rows; r += gridDim.y * 4) {
+  constexpr int LR = D / 4, RB = 256 / LR;   // lanes of a row, rows of a block
+  const int li = threadIdx.x % LR;
+  auto slot = [&](int j) { return (int64_t)(2 * j + (j == d.first ? d.first_slot : 0)) * TR; };
+  for (int r = blockIdx.y * RB + threadIdx.x / LR; r < d.rows; r += gridDim.y * RB) {
     float M = -INFINITY;
-    auto slot = [&](int j) { return 2 * j + (j == d.first ? d.first_slot : 0); };
-    for (int j = d.first + lane; j <= L; j += 64)
-      M = fmaxf(M, parts.ml[(int64_t)slot(j) * TR + r].x);
+    for (int j = d.first + li; j <= L; j += LR) M = fmaxf(M, parts.ml[slot(j) + r].x);
 #pragma unroll
-    for (int x = 32; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
+    for (int x = LR / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
     const float Mu = safe_max(M);
-    float acc[V], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 8
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
+#pragma unroll 4
     for (int j = d.first; j <= L; ++j) {
-      const int64_t at = (int64_t)slot(j) * TR + r;
+      const int64_t at = slot(j) + r;
       const float2 ml = parts.ml[at];
       const float w = exp2f(ml.x - Mu);  // an empty part: exp2(-inf) = 0
       sum += w * ml.y;
-      const float* o = parts.o + at * D + lane * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += w * o[i];
+      acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
     }
     const int row = d.row0 + r;
-    const int t = row / a.group, head = d.head * a.group + row % a.group;
+    const int t = token_of(a, row), head = d.head * a.group + row - t * a.group;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(d.q0 + t) * a.out_ld + (int64_t)head * D + lane * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = (uint16_t)f_to_bits<A>(sum == 0.f ? 0.f : acc[i] * inv);
-    if (a.lse && lane == 0)
+    if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(d.q0 + t) * a.out_ld + (int64_t)head * D + li * 4;
+    *reinterpret_cast<uint2*>(out) = uint2{pack2<A>(acc[0] * inv, acc[1] * inv), pack2<A>(acc[2] * inv, acc[3] * inv)};
+    if (a.lse && li == 0)
       a.lse[(int64_t)(d.q0 + t) * a.n_q_heads + head] = sum == 0.f ? -INFINITY : (Mu + log2f(sum)) * kLn2;
   }
 }
@@ -387,7 +471,7 @@ struct Skinny {
 };
 
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo, int row_hi) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_rows(AttendArgs a) {
   using S = Skinny<A, KV, D>;
   using PT = typename S::PT;
   constexpr int E = S::E, KT = S::KT, KU = S::KU, TR = S::TR, NT = S::NT, NC = S::NC, ND = S::ND;
@@ -399,28 +483,28 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
   const int col = lane & 15, g = lane >> 4;   // query column, lane group
   const KvView& kv = a.kv;
   Cut c;
-  cut_work<KU, TR, 256>(a, row_lo, row_hi, pre, c);
+  cut_work<KU, TR, 256>(a, pre, c);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
   Piece p;
   int n_piece = 0;
   if (c.pos >= c.end) describe<TR, D>(parts, c, nullptr);
-  while (next_piece<KU, TR>(a, row_lo, row_hi, pre, c, p)) {
+  while (next_piece<KU, TR>(a, pre, c, p)) {
     // ---- queries: operand B of the first product, column = row of the tile
     const int row = p.row0 + min(col, p.rows - 1);
-    const int tq = row / a.group;
+    const int tq = token_of(a, row);
     const int pos = p.q.kv_len - p.q.q_len + tq;
-    const int posmin = p.q.kv_len - p.q.q_len + p.row0 / a.group;
-    const int posmax = p.q.kv_len - p.q.q_len + (p.row0 + p.rows - 1) / a.group;
+    const int posmin = p.q.kv_len - p.q.q_len + token_of(a, p.row0);
+    const int posmax = p.q.kv_len - p.q.q_len + token_of(a, p.row0 + p.rows - 1);
     const int vislo = a.window > 0 ? pos - a.window + 1 : 0;
-    uint4 qf[S::NQ];
+    u32x4 qf[S::NQ];
     {
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(p.q.q0 + tq) * a.q_ld +
-                           (int64_t)(p.head * a.group + row % a.group) * D;
+                           (int64_t)(p.head * a.group + row - tq * a.group) * D;
 #pragma unroll
       for (int i = 0; i < S::NQ; ++i) {
         // 16 bits: piece c = 4 i + g of 8 elements; FP8: half i & 1 of piece 4 (i / 2) + g of 16
         const int d = Q8 ? (4 * (i >> 1) + g) * 16 + (i & 1) * 8 : (4 * i + g) * 8;
-        qf[i] = ld16(qp + d);
+        qf[i] = ldv(qp + d);
       }
     }
     const int32_t* ktab = kv.table + ((int64_t)p.seq * 2 * kv.H + p.head) * kv.nb;
@@ -448,23 +532,23 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
       r.vp = vb < nblk ? vtab[vb] : -1;
       return r;
     };
-    uint4 kf[NT][NC], vf[ND];
-    uint4 kscale, vscale;
+    u32x4 kf[NT][NC], vf[ND];
+    u32x4 kscale, vscale;
     auto load_k = [&](const Ids& id) {
       const bool ok = (unsigned)id.kp < (unsigned)kv.n_pages;
       const char* base = kv.pages + (int64_t)(ok ? id.kp : 0) * kv.page_bytes + (g * kv.T + id.slot) * 16;
 #pragma unroll
       for (int n = 0; n < NC; ++n)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) kf[t][n] = ld16(base + (n * 4 * kv.T + 4 * t) * 16);
+        for (int t = 0; t < NT; ++t) kf[t][n] = ldv(base + (n * 4 * kv.T + 4 * t) * 16);
     };
     auto load_v = [&](const Ids& id) {
       const bool ok = (unsigned)id.vp < (unsigned)kv.n_pages;
       const char* base = kv.pages + (int64_t)(ok ? id.vp : 0) * kv.page_bytes +
                          ((int64_t)(id.vslot / E) * D + col) * 16;
 #pragma unroll
-      for (int n = 0; n < ND; ++n) vf[n] = ld16(base + n * 256);
-      if (Q8) vscale = ld16(kv.scales + (int64_t)(ok ? id.vp : 0) * kv.T + id.vslot);
+      for (int n = 0; n < ND; ++n) vf[n] = ldv(base + n * 256);
+      if (Q8) vscale = ldv(kv.scales + (int64_t)(ok ? id.vp : 0) * kv.T + id.vslot);
     };
     // scale bytes of the lane's score tokens: group g, which is the V group's token range
     auto load_ks = [&](int tile) {
@@ -473,7 +557,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
       const int vb = (int)kv_div(kv, (uint32_t)vt);
       const int kp = vb < nblk ? ktab[vb] : -1;
       const bool ok = (unsigned)kp < (unsigned)kv.n_pages;
-      kscale = ld16(kv.scales + (int64_t)(ok ? kp : 0) * kv.T + (vt - vb * kv.T));
+      kscale = ldv(kv.scales + (int64_t)(ok ? kp : 0) * kv.T + (vt - vb * kv.T));
     };
 
     int tile = p.key0 + wave * KT;
@@ -575,7 +659,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
           if (edge && !((seen >> e) & 1)) pr[e] = 0.f;
         }
       }
-      uint4 pf[E / 8], pl[E / 8];
+      u32x4 pf[E / 8], pl[E / 8];
 #pragma unroll
       for (int q = 0; q < E / 8; ++q) p_operand<PT, true>(pr + 8 * q, pf[q], pl[q]);
       // ---- O^T += V^T P^T
@@ -583,7 +667,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
 #pragma unroll
         for (int n = 0; n < ND; ++n) {
           if constexpr (Q8) {
-            const uint4 v0 = fp8_to16<PT>(vf[n].x, vf[n].y), v1 = fp8_to16<PT>(vf[n].z, vf[n].w);
+            const u32x4 v0 = fp8_to16<PT>(vf[n].x, vf[n].y), v1 = fp8_to16<PT>(vf[n].z, vf[n].w);
             o[n] = mfma16<PT>(v0, pf[0], o[n]);
             o[n] = mfma16<PT>(v1, pf[E / 8 - 1], o[n]);
             o[n] = mfma16<PT>(v0, pl[0], o[n]);
@@ -598,12 +682,12 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
         for (int n = 0; n < ND; ++n)
 #pragma unroll
           for (int q = 0; q < E / 8; ++q) {
-            uint4 v = vf[n];
+            u32x4 v = vf[n];
             if constexpr (Q8) v = q ? fp8_to16<PT>(vf[n].z, vf[n].w) : fp8_to16<PT>(vf[n].x, vf[n].y);
             v = keep8(v, live >> (8 * q));
             const uint32_t odd = class_bits<PT>(v, 3);
             if (__ballot(odd != 0)) {
-              const uint4 vis = ones8<PT>(seen >> (8 * q));
+              const u32x4 vis = ones8<PT>(seen >> (8 * q));
               for (int cls = 0; cls < 3; ++cls) {
                 const f32x4 hit = mfma16<PT>(ones8<PT>(class_bits<PT>(v, cls)), vis, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
@@ -649,7 +733,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
         acc += f * *reinterpret_cast<const f32x4*>(&sh_o[w][r][d]);
       }
       if (whole) {
-        const int rr = p.row0 + r, t = rr / a.group, head = p.head * a.group + rr % a.group;
+        const int rr = p.row0 + r, t = token_of(a, rr), head = p.head * a.group + rr - t * a.group;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f};
         uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + t) * a.out_ld + (int64_t)head * D + d;
@@ -669,181 +753,250 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(AttendArgs a, int row_lo
 }
 
 // ---- more rows -------------------------------------------------------------------
-// Tiles of 128 rows: four waves of 32, which share every tile of 64 keys through
-// LDS (loaded there directly, two buffers, one barrier a tile).  The LDS image is
-// the pages' own order, [piece][token] and [token group][element] of 16 bytes, so
-// that all reads of operands are contiguous over lanes and free of bank conflicts.
-template <typename KV>
-__device__ __forceinline__ int key_of(int r, int hi) {  // token of score register r in a tile of 32
-  return is_quant<KV>() ? hi * 16 + r : (r >> 3) * 16 + hi * 8 + (r & 7);
-}
-
+// Tiles of 128 rows: four waves of 32, which share tiles of 64 keys through LDS
+// (two slots, one barrier a tile).  The LDS image is the 16-bit pages' own order,
+// [piece][token] and [token group][element] of 16 bytes, so that operand reads are
+// contiguous over lanes and free of bank conflicts; 16-bit pages are loaded there
+// directly, FP8 ones through registers, where the codes get their scales (2 scales
+// a pair of V codes, one a K row: the products and the softmax then know nothing
+// of FP8).
+//
+// The matrix cores and the vector ALUs are about equally long busy with a tile (2 x
+// 512 cycles for the products of 32 rows with 64 keys of 128 elements, 32
+// exponentials of 16 cycles and about 100 other instructions a lane), so only what
+// overlaps is fast: two blocks share a CU, whose waves drift apart because no
+// barrier ties them.
 __device__ __forceinline__ void load_lds16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
+// Eight FP8 codes times a power of two -> eight 16-bit values.
+template <typename T>
+__device__ __forceinline__ u32x4 fp8_to16s(uint32_t w0, uint32_t w1, float sc) {
+  u32x4 r;
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, sc, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, sc, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, sc, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, sc, true));
+  } else {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, sc, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, sc, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, sc, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, sc, true));
+  }
+  return r;
+}
+// Eight codes of eight tokens, each times its token's power of two (scale bytes
+// s0, s1), less `down` (0 or 1) in the exponent.
+template <typename T>
+__device__ __forceinline__ u32x4 fp8_to16v(uint32_t w0, uint32_t w1, uint32_t s0, uint32_t s1, int down) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? w0 : w1, sb = i < 2 ? s0 : s1;
+    const float fa = scale_of((sb >> (16 * (i & 1))) & 0xffu, down);
+    const float fb = scale_of((sb >> (16 * (i & 1) + 8)) & 0xffu, down);
+    uint32_t a, b;
+    if constexpr (std::is_same<T, bf16_t>::value) {
+      a = __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, fa, true)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, fa, false));
+      b = __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, fb, true)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, fb, false));
+    } else {
+      a = __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, fa, true)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, fa, false));
+      b = __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, fb, true)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, fb, false));
+    }
+    o[i] = __builtin_amdgcn_perm(b, a, 0x07060100u);  // token 2 i of a, token 2 i + 1 of b
+  }
+  return u32x4{o[0], o[1], o[2], o[3]};
+}
+
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a, int row_lo, int row_hi) {
+struct Tiles {
+  static constexpr int NW = 4, TR = 32 * NW, KU = 64, NS = 2;
+  static constexpr int NIDS = 512;   // blocks of the page-id window in LDS
+  struct Shared {
+    u32x4 k[NS][D / 8][KU];
+    u32x4 v[NS][KU / 8][D];
+    int64_t pre[kKvMaxSeqs + 1 + NW];
+    int ids[2][NIDS];
+  };
+};
+
+template <typename A, typename KV, int D>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_tiles(AttendArgs a) {
+  using TT = Tiles<A, KV, D>;
   constexpr bool Q8 = is_quant<KV>();
-  using PT = typename std::conditional<Q8, bf16_t, A>::type;
-  // f16 rows over an FP8 cache: bf16 holds the scaled P's range, two terms of it f16's precision
-  constexpr bool SPLIT = !std::is_same<A, PT>::value;
-  constexpr int E = ET<KV>::E, KU = 64, TR = 128;
-  constexpr int NCK = D / E;          // 16-byte pieces of a K row
-  constexpr int NGV = KU / E;         // token groups of a tile
-  constexpr int ND = D / 32;
-  constexpr int NQ = D / 16;
-  constexpr int KLOADS = NCK / 4, VLOADS = NGV * D / 256;  // 1 KB loads of a wave
-  __shared__ __align__(16) uint4 sk[2][NCK][KU];
-  __shared__ __align__(16) uint4 sv[2][NGV][D];
-  __shared__ float ss[2][2][KU];      // FP8: scales of K and V
-  __shared__ int64_t pre[kKvMaxSeqs + 1 + 4];
+  constexpr int NW = TT::NW, TR = TT::TR, KU = TT::KU, NIDS = TT::NIDS;
+  constexpr int E = ET<KV>::E;
+  constexpr int ND = D / 32, NQ = D / 16;
+  constexpr int KL = D / E;                 // wave loads of K (and of V) of a tile
+  constexpr int LPW = KL / NW;              // ... of a wave
+  static_assert(KL % NW == 0, "loads divide over the waves");
+  // f16 over FP8: values at half their size, so that 448 * 2^8 fits; made good in
+  // the score's scale and in the output
+  constexpr int DOWN = Q8 && std::is_same<A, f16_t>::value ? 1 : 0;
+  extern __shared__ __align__(16) char smem[];
+  typename TT::Shared& sh = *reinterpret_cast<typename TT::Shared*>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hi = lane >> 5;
   const KvView& kv = a.kv;
   Cut c;
-  cut_work<KU, TR, 256>(a, row_lo, row_hi, pre, c);
+  cut_work<KU, TR, NW * 64>(a, sh.pre, c);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
   Piece p;
   int n_piece = 0;
   if (c.pos >= c.end) describe<TR, D>(parts, c, nullptr);
-  // row col of the K operand is this token of a tile of 32, so that a lane's
-  // scores are runs of E tokens
-  const int ktok = Q8 ? ((col >> 2) & 1) * 16 + (col >> 3) * 4 + (col & 3)
-                      : (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
-  while (next_piece<KU, TR>(a, row_lo, row_hi, pre, c, p)) {
+  // row col of a K operand is this token of a tile of 32: a lane's 16 scores are
+  // those of tokens hi * 8 .. + 7 and 16 + hi * 8 .. + 7
+  const int ktok = (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
+  const float sl = DOWN ? a.scale_log2 * 2.f : a.scale_log2;
+  while (next_piece<KU, TR>(a, sh.pre, c, p)) {
     const int wrow0 = p.row0 + wave * 32;
     const int wrows = min(32, p.rows - wave * 32);   // <= 0: no rows of its own
     const int base = p.q.kv_len - p.q.q_len;
     const int row = min(wrow0 + col, p.row0 + p.rows - 1);
-    const int tq = row / a.group;
+    const int tq = token_of(a, row);
     const int pos = base + tq;
-    const int posmin = base + wrow0 / a.group;
-    const int posmax = base + (wrow0 + max(wrows, 1) - 1) / a.group;
-    const int vislo = a.window > 0 ? pos - a.window + 1 : 0;
-    uint4 qf[NQ];
+    const int posmin = base + token_of(a, wrow0);
+    const int posmax = base + token_of(a, wrow0 + max(wrows, 1) - 1);
+    u32x4 qf[NQ];
     {
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(p.q.q0 + tq) * a.q_ld +
-                           (int64_t)(p.head * a.group + row % a.group) * D;
+                           (int64_t)(p.head * a.group + row - tq * a.group) * D + hi * 8;
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int d = Q8 ? (2 * (i >> 1) + hi) * 16 + (i & 1) * 8 : (2 * i + hi) * 8;
-        qf[i] = ld16(qp + d);
-      }
+      for (int i = 0; i < NQ; ++i) qf[i] = ldv(qp + 16 * i);
     }
     const int32_t* ktab = kv.table + ((int64_t)p.seq * 2 * kv.H + p.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-    // pages of the tile's tokens, lane = token; every wave looks up all of them
-    struct Ids {
-      int kp, vp, slot;
+    // ---- page ids of the blocks from b0 on, in LDS (absent ones as they are)
+    const int b_last = min((int)kv_div(kv, (uint32_t)max(p.key1 - 1, 0)), kv.nb - 1);
+    int b0 = 0;
+    bool any_bad = false;
+    auto load_ids = [&](int tile) {
+      b0 = (int)kv_div(kv, (uint32_t)tile);
+      bool bad = false;
+      for (int i = tid; i < 2 * NIDS; i += NW * 64) {
+        const int w = i / NIDS, b = b0 + i % NIDS;
+        int id = -1;
+        if (b <= b_last) {
+          id = (w ? vtab : ktab)[b];
+          bad |= (unsigned)id >= (unsigned)kv.n_pages;
+        }
+        sh.ids[w][i % NIDS] = id;
+      }
+      any_bad = __syncthreads_or(bad);
     };
-    auto find = [&](int tile) {
-      Ids r;
-      const int t = tile + lane;
-      const int b = (int)kv_div(kv, (uint32_t)t);
-      r.slot = t - b * kv.T;
-      r.kp = r.vp = -1;
-      if (b < kv.nb) {
-        r.kp = ktab[b];
-        r.vp = vtab[b];
+    // ---- loads of one tile; lane = token for the page lookups
+    u32x4 stk[Q8 ? LPW : 1], stv[Q8 ? LPW : 1], vsc[Q8 ? LPW : 1];
+    float ksc = 0.f;
+    auto issue = [&](int tile, int slot) {
+      const int t = tile + lane, b = (int)kv_div(kv, (uint32_t)t), sl_ = t - b * kv.T;
+      int kp = sh.ids[0][b - b0], vp = sh.ids[1][b - b0];
+      kp = (unsigned)kp < (unsigned)kv.n_pages ? kp : 0;
+      vp = (unsigned)vp < (unsigned)kv.n_pages ? vp : 0;
+      const char* kb = kv.pages + (int64_t)kp * kv.page_bytes + (wave * kv.T + sl_) * 16;
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) {
+        const char* src = kb + i * NW * kv.T * 16;
+        if constexpr (!Q8) load_lds16(src, &sh.k[slot][wave + NW * i][0]);
+        else stk[i] = ldv(src);
       }
-      return r;
+      if constexpr (Q8) ksc = scale_of(kv.scales[(int64_t)kp * kv.T + sl_], DOWN);
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) {
+        const int j = wave * LPW + i, gr = j * 64 / D, d0 = j * 64 % D;
+        const int pg = __builtin_amdgcn_readlane(vp, gr * E), s0 = __builtin_amdgcn_readlane(sl_, gr * E);
+        const char* src = kv.pages + (int64_t)pg * kv.page_bytes + ((s0 / E) * D + d0 + lane) * 16;
+        if constexpr (!Q8) {
+          load_lds16(src, &sh.v[slot][gr][d0]);
+        } else {
+          stv[i] = ldv(src);
+          vsc[i] = ldv(kv.scales + (int64_t)pg * kv.T + s0);
+        }
+      }
     };
-    float sc_next = 0.f;
-    auto stage = [&](const Ids& id, int buf) {
-      const int kp = (unsigned)id.kp < (unsigned)kv.n_pages ? id.kp : 0;
-      const int vp = (unsigned)id.vp < (unsigned)kv.n_pages ? id.vp : 0;
-      const char* kb = kv.pages + (int64_t)kp * kv.page_bytes + (int64_t)id.slot * 16;
+    auto commit = [&](int slot) {   // FP8: what was loaded goes to LDS
+      if constexpr (Q8) {
 #pragma unroll
-      for (int i = 0; i < KLOADS; ++i) {
-        const int ch = wave + 4 * i;
-        load_lds16(kb + (int64_t)ch * kv.T * 16, &sk[buf][ch][0]);
+        for (int i = 0; i < LPW; ++i) {
+          const int ch = wave + NW * i;
+          sh.k[slot][2 * ch][lane] = fp8_to16s<A>(stk[i].x, stk[i].y, ksc);
+          sh.k[slot][2 * ch + 1][lane] = fp8_to16s<A>(stk[i].z, stk[i].w, ksc);
+          const int j = wave * LPW + i, gr = j * 64 / D, d = j * 64 % D + lane;
+          sh.v[slot][2 * gr][d] = fp8_to16v<A>(stv[i].x, stv[i].y, vsc[i].x, vsc[i].y, DOWN);
+          sh.v[slot][2 * gr + 1][d] = fp8_to16v<A>(stv[i].z, stv[i].w, vsc[i].z, vsc[i].w, DOWN);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < VLOADS; ++i) {
-        const int j = wave * VLOADS + i;
-        const int gr = j * 64 / D, d0 = j * 64 % D;
-        const int pg = __builtin_amdgcn_readlane(vp, gr * E), sl = __builtin_amdgcn_readlane(id.slot, gr * E);
-        const char* vb = kv.pages + (int64_t)pg * kv.page_bytes + ((int64_t)(sl / E) * D + d0) * 16;
-        load_lds16(vb + lane * 16, &sv[buf][gr][d0]);
-      }
-      if (Q8 && wave < 2)
-        sc_next = __uint_as_float((uint32_t)kv.scales[(int64_t)(wave ? vp : kp) * kv.T + id.slot] << 23);
     };
     f32x16 o[ND];
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+    for (int i = 0; i < ND; ++i) o[i] = f32x16{};
     float m = -INFINITY, l = 0.f;
-    auto bad_of = [&](const Ids& id) {
-      return (unsigned long long)__ballot((unsigned)id.kp >= (unsigned)kv.n_pages ||
-                                          (unsigned)id.vp >= (unsigned)kv.n_pages);
+    // bits of the lane's 16 tokens of half kt (register r: bit r) that lie in [lo, up] of the tile
+    auto range_bits = [&](int kt, int lo, int up) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k0 = kt * 32 + q * 16 + hi * 8;
+        const int x = min(max(lo - k0, 0), 8), y = min(max(up - k0 + 1, 0), 8);
+        bits |= (((1u << y) - 1u) & ~((1u << x) - 1u)) << (8 * q);
+      }
+      return bits;
     };
-    Ids idn = find(p.key0);
-    unsigned long long bad = bad_of(idn), badn = 0;
-    stage(idn, 0);
-    idn = find(p.key0 + KU);
-    int buf = 0;
-    for (int tile = p.key0; tile < p.key1; tile += KU, buf ^= 1) {
+    load_ids(p.key0);
+    issue(p.key0, 0);
+    commit(0);
+    int slot = 0;
+    for (int tile = p.key0; tile < p.key1; tile += KU, slot ^= 1) {
       const bool more = tile + KU < p.key1;
-      if (Q8 && wave < 2) ss[buf][wave][lane] = sc_next;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
+      __syncthreads();   // this tile has arrived (the compiler waits for all loads), the last one is read
       if (more) {
-        badn = bad_of(idn);
-        stage(idn, buf ^ 1);
-        idn = find(tile + 2 * KU);
+        if ((int)kv_div(kv, (uint32_t)(tile + 2 * KU - 1)) - b0 >= NIDS) load_ids(tile);
+        issue(tile + KU, slot ^ 1);
       }
       const bool mine = wrows > 0 && tile <= posmax && (a.window <= 0 || tile + KU - 1 > posmin - a.window);
       if (mine) {
         // ---- S^T = K Q^T
         f32x16 s[2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int kt = 0; kt < 2; ++kt) s[kt] = f32x16{};
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[kt][r] = 0.f;
-#pragma unroll
-          for (int n = 0; n < NCK / 2; ++n) {
-            const uint4 kf = sk[buf][2 * n + hi][kt * 32 + ktok];
-            if constexpr (Q8) {
-              s[kt] = mfma32<A>(fp8_to16<A>(kf.x, kf.y), qf[2 * n], s[kt]);
-              s[kt] = mfma32<A>(fp8_to16<A>(kf.z, kf.w), qf[2 * n + 1], s[kt]);
-            } else {
-              s[kt] = mfma32<A>(kf, qf[n], s[kt]);
-            }
-          }
-        }
-        if constexpr (Q8) {
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[kt][r] *= ss[buf][0][kt * 32 + key_of<KV>(r, hi)];
-        }
+            s[kt] = mfma32<A>(sh.k[slot][2 * n + hi][kt * 32 + ktok], qf[n], s[kt]);
         // ---- mask
-        const bool edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || bad;
+        const bool edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || any_bad;
         uint32_t live[2], seen[2];
         if (edge) {
+          unsigned long long bad = 0;
+          if (any_bad) {
+            const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
+            bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
+                           (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+          }
+          const int w = a.window > 0 ? a.window : 0x40000000;
 #pragma unroll
           for (int kt = 0; kt < 2; ++kt) {
-            live[kt] = seen[kt] = 0;
+            const uint32_t gone = ((uint32_t)(bad >> (kt * 32 + hi * 8)) & 0xffu) |
+                                  (((uint32_t)(bad >> (kt * 32 + 16 + hi * 8)) & 0xffu) << 8);
+            live[kt] = range_bits(kt, posmin - w + 1 - tile, posmax - tile) & ~gone;
+            seen[kt] = range_bits(kt, pos - w + 1 - tile, pos - tile) & ~gone;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int k = kt * 32 + key_of<KV>(r, hi), key = tile + k;
-              const bool lv = !((bad >> k) & 1) && key <= posmax && (a.window <= 0 || key > posmin - a.window);
-              const bool sv = lv && key <= pos && key >= vislo;
-              live[kt] |= (uint32_t)lv << r;
-              seen[kt] |= (uint32_t)sv << r;
-              s[kt][r] = sv ? s[kt][r] : -INFINITY;
-            }
+            for (int r = 0; r < 16; ++r)
+              if (!((seen[kt] >> r) & 1)) s[kt][r] = -INFINITY;
           }
         }
         // ---- running maximum and sum
         float top = s[0][0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, fmaxf(s[0][r], s[1][r]));
-        top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+        for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, s[0][r]), s[1][r]);
+        top = fmaxf(top, __shfl_xor(top, 32)) * sl;
         if (__ballot(top > m + 8.f)) {
           const float mn = fmaxf(m, top);
           const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
@@ -853,78 +1006,76 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a, int row_l
           m = mn;
         }
         const float mu = safe_max(m);
-        uint4 pf[4], pl[4];
+        u32x4 pf[4], unused;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
           float pr[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale_log2, -mu));
-          if constexpr (Q8) {
+            l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], sl, -mu));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              pr[r] *= ss[buf][1][kt * 32 + key_of<KV>(r, hi)];
-              if (edge && !((seen[kt] >> r) & 1)) pr[r] = 0.f;
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) p_operand<PT, SPLIT>(pr + 8 * q, pf[2 * kt + q], pl[2 * kt + q]);
+          for (int q = 0; q < 2; ++q) p_operand<A, false>(pr + 8 * q, pf[2 * kt + q], unused);
         }
         // ---- O^T += V^T P^T
-        auto v_of = [&](int kt, int q, int n) -> uint4 {
-          if constexpr (Q8) {
-            const uint4 u = sv[buf][kt * 2 + hi][n * 32 + col];
-            return q ? fp8_to16<PT>(u.z, u.w) : fp8_to16<PT>(u.x, u.y);
-          } else {
-            return sv[buf][kt * 4 + q * 2 + hi][n * 32 + col];
-          }
-        };
-        if (!edge) {
+        // in a tile that some row does not see whole: tokens that no row sees are
+        // taken out of V, and what is not finite is looked for
+        bool dead = false, odd_any = false;
+        if (edge) {
+          dead = __ballot((live[0] & live[1]) != 0xffffu) != 0;
+          uint32_t odd = 0;
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int n = 0; n < ND; ++n) {
+              u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
+              if (dead) v = keep8(v, live[q >> 1] >> (8 * (q & 1)));
+              odd |= not_finite<A>(v);
+            }
+          odd_any = __ballot(odd) != 0;
+        }
+        if (!dead && !odd_any) {
 #pragma unroll
-              for (int n = 0; n < ND; ++n) {
-                const uint4 v = v_of(kt, q, n);
-                o[n] = mfma32<PT>(v, pf[2 * kt + q], o[n]);
-                if (SPLIT) o[n] = mfma32<PT>(v, pl[2 * kt + q], o[n]);
-              }
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int n = 0; n < ND; ++n)
+              o[n] = mfma32<A>(sh.v[slot][2 * q + hi][n * 32 + col], pf[q], o[n]);
         } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t lv = (q < 2 ? live[0] : live[1]) >> (8 * (q & 1));
+            const uint32_t sv = (q < 2 ? seen[0] : seen[1]) >> (8 * (q & 1));
+            u32x4 pq = pf[0];
+            if (q == 1) pq = pf[1];
+            if (q == 2) pq = pf[2];
+            if (q == 3) pq = pf[3];
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
+            for (int n = 0; n < ND; ++n) {
+              u32x4 v = keep8(sh.v[slot][2 * q + hi][n * 32 + col], lv);
+              if (odd_any) {
+                const u32x4 vis = ones8<A>(sv);
+#pragma unroll 1
+                for (int cls = 0; cls < 3; ++cls) {
+                  const f32x16 hit = mfma32<A>(ones8<A>(class_bits<A>(v, cls)), vis, f32x16{});
+                  const float val = class_value(cls);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int n = 0; n < ND; ++n) {
-                uint4 v = keep8(v_of(kt, q, n), live[kt] >> (8 * q));
-                const uint32_t odd = class_bits<PT>(v, 3);
-                if (__ballot(odd != 0)) {
-                  const uint4 vis = ones8<PT>(seen[kt] >> (8 * q));
-                  for (int cls = 0; cls < 3; ++cls) {
-                    f32x16 hit;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) hit[r] = 0.f;
-                    hit = mfma32<PT>(ones8<PT>(class_bits<PT>(v, cls)), vis, hit);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? class_value(cls) : 0.f;
-                  }
-                  v = keep8(v, ~odd);
+                  for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? val : 0.f;
                 }
-                o[n] = mfma32<PT>(v, pf[2 * kt + q], o[n]);
-                if (SPLIT) o[n] = mfma32<PT>(v, pl[2 * kt + q], o[n]);
+                v = keep8(v, ~class_bits<A>(v, 3));
               }
+              o[n] = mfma32<A>(v, pq, o[n]);
+            }
+          }
         }
       }
-      bad = badn;
+      if (more) commit(slot ^ 1);
     }
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
     const bool whole = p.begins && p.ends;
     if (col < wrows) {
       if (whole) {
-        const int head = p.head * a.group + row % a.group;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int head = p.head * a.group + row - tq * a.group;
+        const float inv = l == 0.f ? 0.f : (DOWN ? 2.f : 1.f) / l;
         uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D;
 #pragma unroll
         for (int n = 0; n < ND; ++n)
@@ -939,35 +1090,44 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a, int row_l
           a.lse[(int64_t)(p.q.q0 + tq) * a.n_q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
         const int64_t at = ((int64_t)c.block * 2 + (n_piece == 0 ? 0 : 1)) * TR + wave * 32 + col;
+        const float up = DOWN ? 2.f : 1.f;
 #pragma unroll
         for (int n = 0; n < ND; ++n)
 #pragma unroll
           for (int b = 0; b < 4; ++b)
             *reinterpret_cast<f32x4*>(parts.o + at * D + n * 32 + b * 8 + hi * 4) =
-                f32x4{o[n][4 * b], o[n][4 * b + 1], o[n][4 * b + 2], o[n][4 * b + 3]};
+                f32x4{o[n][4 * b] * up, o[n][4 * b + 1] * up, o[n][4 * b + 2] * up, o[n][4 * b + 3] * up};
         if (hi == 0) parts.ml[at] = float2{m, l};
       }
     }
     if (n_piece == 0) describe<TR, D>(parts, c, &p);
     ++n_piece;
-    __syncthreads();  // the buffers of this piece have been read
+    __syncthreads();  // the slots of this piece have been read
   }
 }
 
+// Rows of a head of the longest sequence choose the kernel for all of a batch.
+inline bool few_rows(int32_t group, int32_t max_q_len) { return (int64_t)max_q_len * group <= 16; }
+inline int blocks_of(int n_cu) { return 2 * n_cu / 8 * 8; }
+
 template <typename A, typename KV, int D>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
-  const int G = a.n_cu * 2 / 8 * 8;
-  const int64_t most = (int64_t)a.max_q_len * a.group;  // rows of a head of the longest sequence
-  const int split = 16;
-  // up to `split` rows; alone if no sequence has more
-  const bool wide = most > split;
-  const int small = (int)(most < 16 ? most : 16);
-  hipLaunchKernelGGL((k_attend_rows<A, KV, D>), dim3(G), dim3(256), 0, s, a, 1, wide ? split : INT32_MAX);
-  hipLaunchKernelGGL((k_attend_join<A, D, 16>), dim3(G, (small + 3) / 4), dim3(256), 0, s, a, G);
-  if (wide) {
-    const int rows = (int)(most < 128 ? most : 128);
-    hipLaunchKernelGGL((k_attend_tiles<A, KV, D>), dim3(G), dim3(256), 0, s, a, split + 1, INT32_MAX);
-    hipLaunchKernelGGL((k_attend_join<A, D, 128>), dim3(G, (rows + 3) / 4), dim3(256), 0, s, a, G);
+  const int64_t most = (int64_t)a.max_q_len * a.group;
+  const bool few = few_rows(a.group, a.max_q_len);
+  const int G = blocks_of(a.n_cu);
+  constexpr int RB = 256 / (D / 4);   // rows of a block of the joining launch
+  if (few) {
+    hipLaunchKernelGGL((k_attend_rows<A, KV, D>), dim3(G), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attend_join<A, D, 16>), dim3(G, (unsigned)((most + RB - 1) / RB)), dim3(256), 0, s, a, G);
+  } else {
+    using TT = Tiles<A, KV, D>;
+    const int rows = (int)(most < TT::TR ? most : TT::TR);
+    const size_t lds = sizeof(typename TT::Shared);
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (attr != hipSuccess) return attr;
+    hipLaunchKernelGGL((k_attend_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a);
+    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)), dim3(256), 0, s, a, G);
   }
   return hipGetLastError();
 }
@@ -980,10 +1140,9 @@ hipError_t launch_d(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len) {
-  const int G = n_cu * 2 / 8 * 8;
-  const int TR = (int64_t)max_q_len * group > 16 ? 128 : 16;
-  const size_t D = (size_t)ty.D;
-  return (size_t)G * (sizeof(PartDesc) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
+  const bool few = few_rows(group, max_q_len);
+  const size_t G = (size_t)blocks_of(n_cu), TR = few ? 16 : 128, D = (size_t)ty.D;
+  return G * (sizeof(PartDesc) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
 }
 
 hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {

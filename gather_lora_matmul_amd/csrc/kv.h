@@ -47,13 +47,13 @@ __host__ __device__ inline uint32_t kv_div(const KvView& v, uint32_t x) {
   return (uint32_t)(((uint64_t)x * v.div_m) >> 32) >> v.div_s;
 #endif
 }
-// The multiplier of division by T (T >= 2): with 2^(k-1) < T <= 2^k,
-// m = ceil(2^(31 + k) / T) < 2^32, and x * m >> (31 + k) is exact below 2^31.
-inline void kv_div_init(KvView& v) {
+// The multiplier of division by d >= 2: with 2^(k-1) < d <= 2^k,
+// m = ceil(2^(31 + k) / d) < 2^32, and x * m >> (31 + k) is exact below 2^31.
+inline void div_init(int32_t d, uint32_t& m, int32_t& s) {
   int k = 1;
-  while ((1 << k) < v.T) ++k;
-  v.div_m = (uint32_t)((((uint64_t)1 << (31 + k)) + (uint64_t)v.T - 1) / (uint64_t)v.T);
-  v.div_s = k - 1;
+  while ((1 << k) < d) ++k;
+  m = (uint32_t)((((uint64_t)1 << (31 + k)) + (uint64_t)d - 1) / (uint64_t)d);
+  s = k - 1;
 }
 
 // Rows of one sequence's new tokens and their first position, with everything
@@ -94,7 +94,9 @@ struct AttendArgs {
   int64_t out_ld;
   float* lse;              // [n_tokens][n_q_heads] or null
   int32_t n_q_heads;
-  int32_t group;           // query heads of a kv head
+  int32_t group;           // query heads of a kv head, and the multiplier of division
+  uint32_t group_m;        // by it (if it is not 1)
+  int32_t group_s;
   int32_t max_q_len;
   float scale_log2;        // scale * log2(e)
   int32_t window;          // 0: none

@@ -67,7 +67,7 @@ lora_status view_of(const lora_pool* p, const lora_kv_desc* d, const lora_kv_bat
   v.page_bytes = p->page_bytes;
   v.n_pages = (int32_t)p->n_pages;
   v.T = T;
-  kv_div_init(v);
+  div_init(T, v.div_m, v.div_s);
   v.H = d->n_kv_heads;
   v.n_seqs = b->n_seqs;
   v.n_tokens = b->n_tokens;
@@ -187,6 +187,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   a.lse = lse_dev;
   a.n_q_heads = n_q_heads;
   a.group = n_q_heads / d->n_kv_heads;
+  div_init(a.group < 2 ? 2 : a.group, a.group_m, a.group_s);
   a.max_q_len = b->max_q_len;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
