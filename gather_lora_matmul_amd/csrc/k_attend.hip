@@ -410,6 +410,13 @@ __device__ __forceinline__ void describe(const Parts<TR, D>& parts, const Cut& c
   parts.desc[blockIdx.x] = d;
 }
 
+// Maximum of three in one instruction (fmaxf would quiet every operand first).  A
+// NaN among them is the result: then the running maximum stays, and the row's sum
+// becomes NaN by the exponential.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- the joining launch ----------------------------------------------------------
@@ -952,53 +959,73 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     issue(p.key0, 0);
     commit(0);
     int slot = 0;
-    for (int tile = p.key0; tile < p.key1; tile += KU, slot ^= 1) {
+    // The next tile's loads, then this tile's products.  EDGE: some row may not
+    // see all of the tile.  (A loop of its own for the others: one that holds both
+    // keeps two copies of the accumulators.)
+    auto step = [&](const int tile, auto edge_c) {
+      constexpr bool EDGE = decltype(edge_c)::value;
       const bool more = tile + KU < p.key1;
-      __syncthreads();   // this tile has arrived (the compiler waits for all loads), the last one is read
+      // this tile's loads have arrived, of every wave (a barrier alone does not wait
+      // for loads that go to LDS), and the last tile is read
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
       if (more) {
         if ((int)kv_div(kv, (uint32_t)(tile + 2 * KU - 1)) - b0 >= NIDS) load_ids(tile);
         issue(tile + KU, slot ^ 1);
       }
-      const bool mine = wrows > 0 && tile <= posmax && (a.window <= 0 || tile + KU - 1 > posmin - a.window);
-      if (mine) {
+      if (wrows > 0 &&
+          (!EDGE || (tile <= posmax && (a.window <= 0 || tile + KU - 1 > posmin - a.window)))) {
         // ---- S^T = K Q^T
-        f32x16 s[2];
+        // in groups of four products, whose operands were read a group ahead (the
+        // scheduler, left alone, reads each just before its use)
+        f32x16 s[2] = {f32x16{}, f32x16{}};
+        const u32x4* kp = &sh.k[slot][hi][ktok];   // piece 2 n of half kt: kp[2 * n * KU + kt * 32]
+        u32x4 kf[2][4];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) s[kt] = f32x16{};
+        for (int i = 0; i < 4; ++i) kf[0][i] = kp[2 * (i >> 1) * KU + (i & 1) * 32];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int g = 0; g < NQ / 2; ++g) {
+          if (g + 1 < NQ / 2) {
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
-            s[kt] = mfma32<A>(sh.k[slot][2 * n + hi][kt * 32 + ktok], qf[n], s[kt]);
-        // ---- mask
-        const bool edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || any_bad;
-        uint32_t live[2], seen[2];
-        if (edge) {
-          unsigned long long bad = 0;
-          if (any_bad) {
-            const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
-            bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
-                           (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+            for (int i = 0; i < 4; ++i) kf[(g + 1) & 1][i] = kp[2 * (2 * g + 2 + (i >> 1)) * KU + (i & 1) * 32];
           }
-          const int w = a.window > 0 ? a.window : 0x40000000;
+          __builtin_amdgcn_sched_barrier(0x6);
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            const uint32_t gone = ((uint32_t)(bad >> (kt * 32 + hi * 8)) & 0xffu) |
-                                  (((uint32_t)(bad >> (kt * 32 + 16 + hi * 8)) & 0xffu) << 8);
-            live[kt] = range_bits(kt, posmin - w + 1 - tile, posmax - tile) & ~gone;
-            seen[kt] = range_bits(kt, pos - w + 1 - tile, pos - tile) & ~gone;
+          for (int i = 0; i < 4; ++i) s[i & 1] = mfma32<A>(kf[g & 1][i], qf[2 * g + (i >> 1)], s[i & 1]);
+          __builtin_amdgcn_sched_barrier(0x6);
+        }
+        // ---- mask
+        bool edge = false;
+        uint32_t live[2] = {0xffffu, 0xffffu}, seen[2] = {0xffffu, 0xffffu};
+        if constexpr (EDGE) {
+          edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || any_bad;
+          if (edge) {
+            unsigned long long bad = 0;
+            if (any_bad) {
+              const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
+              bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
+                             (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+            }
+            const int w = a.window > 0 ? a.window : 0x40000000;
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (!((seen[kt] >> r) & 1)) s[kt][r] = -INFINITY;
+            for (int kt = 0; kt < 2; ++kt) {
+              const uint32_t gone = ((uint32_t)(bad >> (kt * 32 + hi * 8)) & 0xffu) |
+                                    (((uint32_t)(bad >> (kt * 32 + 16 + hi * 8)) & 0xffu) << 8);
+              live[kt] = range_bits(kt, posmin - w + 1 - tile, posmax - tile) & ~gone;
+              seen[kt] = range_bits(kt, pos - w + 1 - tile, pos - tile) & ~gone;
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (!((seen[kt] >> r) & 1)) s[kt][r] = -INFINITY;
+            }
           }
         }
         // ---- running maximum and sum
         float top = s[0][0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(fmaxf(top, s[0][r]), s[1][r]);
-        top = fmaxf(top, __shfl_xor(top, 32)) * sl;
+        for (int r = 0; r < 16; ++r) top = max3(top, s[0][r], s[1][r]);
+        top = max3(top, __shfl_xor(top, 32), top) * sl;
         if (__ballot(top > m + 8.f)) {
-          const float mn = fmaxf(m, top);
+          const float mn = top > m ? top : m;
           const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
           l *= f;
 #pragma unroll
@@ -1007,39 +1034,52 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
         const float mu = safe_max(m);
         u32x4 pf[4], unused;
+        auto take_exp = [&](int q) {   // P of the 16 tokens of step q
+          float pr[8];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          float pr[16];
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], sl, -mu));
-#pragma unroll
-          for (int q = 0; q < 2; ++q) p_operand<A, false>(pr + 8 * q, pf[2 * kt + q], unused);
-        }
+          for (int r = 0; r < 8; ++r)
+            l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q >> 1][8 * (q & 1) + r], sl, -mu));
+          p_operand<A, false>(pr, pf[q], unused);
+        };
         // ---- O^T += V^T P^T
-        // in a tile that some row does not see whole: tokens that no row sees are
-        // taken out of V, and what is not finite is looked for
-        bool dead = false, odd_any = false;
-        if (edge) {
-          dead = __ballot((live[0] & live[1]) != 0xffffu) != 0;
-          uint32_t odd = 0;
+        if constexpr (!EDGE) {
+          // the exponentials of one step and the operands' reads beside the products
+          // of the step before
+          const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
+          u32x4 vf[2][ND];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
+          take_exp(0);
 #pragma unroll
-            for (int n = 0; n < ND; ++n) {
-              u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
-              if (dead) v = keep8(v, live[q >> 1] >> (8 * (q & 1)));
-              odd |= not_finite<A>(v);
+          for (int q = 0; q < 4; ++q) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (q < 3) {
+#pragma unroll
+              for (int n = 0; n < ND; ++n) vf[(q + 1) & 1][n] = vp[2 * (q + 1) * D + n * 32];
             }
-          odd_any = __ballot(odd) != 0;
-        }
-        if (!dead && !odd_any) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int n = 0; n < ND; ++n)
-              o[n] = mfma32<A>(sh.v[slot][2 * q + hi][n * 32 + col], pf[q], o[n]);
+            for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
+            if (q < 3) take_exp(q + 1);
+          }
         } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) take_exp(q);
+          // in a tile that some row does not see whole: tokens that no row sees are
+          // taken out of V, and what is not finite is looked for
+          bool dead = false, odd_any = false;
+          if (edge) {
+            dead = __ballot((live[0] & live[1]) != 0xffffu) != 0;
+            uint32_t odd = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int n = 0; n < ND; ++n) {
+                u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
+                if (dead) v = keep8(v, live[q >> 1] >> (8 * (q & 1)));
+                odd |= not_finite<A>(v);
+              }
+            odd_any = __ballot(odd) != 0;
+          }
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const uint32_t lv = (q < 2 ? live[0] : live[1]) >> (8 * (q & 1));
@@ -1050,7 +1090,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             if (q == 3) pq = pf[3];
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
-              u32x4 v = keep8(sh.v[slot][2 * q + hi][n * 32 + col], lv);
+              u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
+              if (dead) v = keep8(v, lv);
               if (odd_any) {
                 const u32x4 vis = ones8<A>(sv);
 #pragma unroll 1
@@ -1068,6 +1109,22 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
       }
       if (more) commit(slot ^ 1);
+      slot ^= 1;
+    };
+    // tiles [clean0, clean1) that all rows of the block see whole, if their pages are there
+    const int bmin = base + token_of(a, p.row0), bmax = base + token_of(a, p.row0 + p.rows - 1);
+    const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
+    for (int tile = p.key0; tile < p.key1;) {
+      const int stop = min(clean1, p.key1);
+      if (tile >= clean0 && tile < stop && !any_bad) {
+        do {
+          step(tile, std::integral_constant<bool, false>{});
+          tile += KU;
+        } while (tile < stop && !any_bad);
+      } else {
+        step(tile, std::integral_constant<bool, true>{});
+        tile += KU;
+      }
     }
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
