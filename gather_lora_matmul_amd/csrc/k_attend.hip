@@ -160,7 +160,7 @@ __device__ __forceinline__ float class_value(int cls) {
 struct Piece {
   int seq, head, row0, rows;
   int key0, key1;        // keys to visit, key0 a multiple of KU
-  int64_t start;         // the tile's first unit in the whole sequence of units
+  int start;             // the tile's first unit in the whole sequence of units
   int first;             // block that has it
   bool begins, ends;     // the piece has the tile's first / last unit
   KvSeq q;
@@ -177,13 +177,6 @@ __device__ __forceinline__ int token_of(const AttendArgs& a, int row) {  // row 
 }
 // A value that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uni(int64_t x) {
-  return (int64_t)(((uint64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x));
-}
-__device__ __forceinline__ int64_t quot(int64_t x, int64_t y) {  // of numbers >= 0
-  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
-  return x / y;
-}
 
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
 // row's window, down to a multiple of KU, to the last row's own position.
@@ -212,16 +205,16 @@ __device__ __forceinline__ int wave_add(int x) {
   return x;
 }
 
+// All units of a call are fewer than 2^31 (attend_units, checked on the host).
 struct Cut {
-  int64_t pos, end;          // this block's range of units
-  int64_t total, each;       // all units; block L's range begins at L each + min(L, over)
-  int over;
-  int block, blocks;         // its number in the order of the ranges, and the blocks that have one
+  int pos, end;          // this block's range of units
+  int each, over;        // block L's range begins at L each + min(L, over)
+  int block, blocks;     // its number in the order of the ranges, and the blocks that have one
   int seq;
-  __device__ int64_t begin_of(int L) const { return L * each + min(L, over); }
-  __device__ int block_of(int64_t x) const {
-    const int64_t big = (each + 1) * over;
-    return (int)(x < big ? quot(x, each + 1) : over + quot(x - big, each));
+  __device__ int begin_of(int L) const { return L * each + min(L, over); }
+  __device__ int block_of(int x) const {
+    const int big = (each + 1) * over;
+    return x < big ? (int)((uint32_t)x / (uint32_t)(each + 1)) : over + (int)((uint32_t)(x - big) / (uint32_t)each);
   }
 };
 
@@ -230,12 +223,12 @@ struct Cut {
 // adds up the tiles of its sequence if they are few, all lanes together those of
 // each other one.
 template <int KU, int TR, int THREADS>
-__device__ __forceinline__ void cut_work(const AttendArgs& a, int64_t* pre, Cut& c) {
+__device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c) {
   const int n = a.kv.n_seqs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int W = THREADS / 64, FEW = 2;
-  int64_t* wsum = pre + kKvMaxSeqs + 1;
-  int64_t run = 0;
+  int* wsum = pre + kKvMaxSeqs + 1;
+  int run = 0;
   const bool small = n <= 64;   // every wave for itself
   for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
     const int s = s0 + (small ? lane : tid);
@@ -255,27 +248,16 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int64_t* pre, Cut&
       part = wave_add(part);
       if (lane == src) units += part;
     }
-    const int64_t x = (int64_t)units * a.kv.H;
-    int64_t sum = x;
-    if (!__ballot(x >> 25)) {
-      int y = (int)x;
+    int sum = units * a.kv.H;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int z = __shfl_up(y, d);
-        if (lane >= d) y += z;
-      }
-      sum = y;
-    } else {
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t y = __shfl_up(sum, d);
-        if (lane >= d) sum += y;
-      }
+    for (int d = 1; d < 64; d <<= 1) {
+      const int z = __shfl_up(sum, d);
+      if (lane >= d) sum += z;
     }
     if (!small) {
       if (lane == 63) wsum[wave] = sum;
       __syncthreads();
-      int64_t before = run, all = 0;
+      int before = run, all = 0;
       for (int w = 0; w < W; ++w) {
         if (w < wave) before += wsum[w];
         all += wsum[w];
@@ -289,19 +271,19 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int64_t* pre, Cut&
   }
   if (small ? lane == 0 : tid == 0) pre[0] = 0;
   if (!small) __syncthreads();
-  c.total = uni(pre[n]);
+  const int total = uni(pre[n]);
   // blocks b, b + 8, ... run on one XCD: give each XCD one contiguous eighth of
   // the ranges, so that the tiles that read the same keys share an L2
   const int G = (int)gridDim.x;
   const int b = (int)blockIdx.x;
-  c.blocks = c.total < G ? (int)c.total : G;
+  c.blocks = min(total, G);
   const int per = (c.blocks + 7) >> 3;
   const int L = (b & 7) * per + (b >> 3);
   c.block = L;
   c.pos = c.end = 0;
   if ((b >> 3) >= per || L >= c.blocks) return;
-  c.each = quot(c.total, c.blocks);
-  c.over = (int)(c.total - c.each * c.blocks);
+  c.each = (int)((uint32_t)total / (uint32_t)c.blocks);
+  c.over = total - c.each * c.blocks;
   c.pos = c.begin_of(L);
   c.end = c.begin_of(L + 1);
   // the sequence of the first unit
@@ -321,7 +303,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int64_t* pre, Cut&
 // The next piece of the range; advances c.  Sequences without units are passed.
 // Every wave computes it for itself, with all its lanes.
 template <int KU, int TR>
-__device__ __forceinline__ bool next_piece(const AttendArgs& a, const int64_t* pre, Cut& c, Piece& p) {
+__device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, Cut& c, Piece& p) {
   if (c.pos >= c.end) return false;
   while (uni(pre[c.seq + 1]) <= c.pos) ++c.seq;
   p.seq = c.seq;
@@ -329,10 +311,10 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int64_t* p
   p.q.q0 = uni(p.q.q0);
   p.q.q_len = uni(p.q.q_len);
   p.q.kv_len = uni(p.q.kv_len);
-  const int64_t before = uni(pre[c.seq]), off = c.pos - before;
-  const int hu = (int)quot(uni(pre[c.seq + 1]) - before, a.kv.H);
-  p.head = (int)quot(off, hu);
-  int rem = (int)(off - (int64_t)p.head * hu);
+  const int before = uni(pre[c.seq]);
+  const uint32_t hu = (uint32_t)(uni(pre[c.seq + 1]) - before) / (uint32_t)a.kv.H;
+  p.head = (int)((uint32_t)(c.pos - before) / hu);
+  int rem = c.pos - before - p.head * (int)hu;
   const int rows = p.q.q_len * a.group;
   int tile = 0;
   if (rows > TR) {
@@ -354,15 +336,15 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int64_t* p
       }
       rem -= __shfl(sum, 63);
     }
+    tile = uni(tile);
+    rem = uni(rem);
   }
-  p.row0 = uni(tile) * TR;
-  rem = uni(rem);
+  p.row0 = tile * TR;
   p.rows = min(TR, rows - p.row0);
   int lo = 0, hi = 0;
   tile_keys<KU>(a, p.q, p.row0, p.rows, lo, hi);
   const int units = (hi - lo + KU - 1) / KU;
-  const int64_t left = c.end - c.pos;
-  const int take = left < units - rem ? (int)left : units - rem;
+  const int take = min(c.end - c.pos, units - rem);
   p.begins = rem == 0;
   p.ends = rem + take == units;
   p.key0 = lo + rem * KU;
@@ -483,7 +465,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   using PT = typename S::PT;
   constexpr int E = S::E, KT = S::KT, KU = S::KU, TR = S::TR, NT = S::NT, NC = S::NC, ND = S::ND;
   constexpr bool Q8 = S::Q8;
-  __shared__ int64_t pre[kKvMaxSeqs + 1 + 4];
+  __shared__ int pre[kKvMaxSeqs + 1 + 4];
   __shared__ float sh_ml[4][TR][2];
   __shared__ __align__(16) float sh_o[4][TR][D + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -829,7 +811,7 @@ struct Tiles {
   struct Shared {
     u32x4 k[NS][D / 8][KU];
     u32x4 v[NS][KU / 8][D];
-    int64_t pre[kKvMaxSeqs + 1 + NW];
+    int pre[kKvMaxSeqs + 1 + NW];
     int ids[2][NIDS];
   };
 };
@@ -880,7 +862,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     const int32_t* ktab = kv.table + ((int64_t)p.seq * 2 * kv.H + p.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-    // ---- page ids of the blocks from b0 on, in LDS (absent ones as they are)
+    const int bmin = base + token_of(a, p.row0), bmax = base + token_of(a, p.row0 + p.rows - 1);
+    // ---- page ids of the blocks from b0 on, in LDS (absent ones as they are).  Blocks
+    // before the first row's window may be given back without any care
+    const int vis0 = a.window > 0 ? bmin - a.window + 1 : 0;
     const int b_last = min((int)kv_div(kv, (uint32_t)max(p.key1 - 1, 0)), kv.nb - 1);
     int b0 = 0;
     bool any_bad = false;
@@ -892,7 +877,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         int id = -1;
         if (b <= b_last) {
           id = (w ? vtab : ktab)[b];
-          bad |= (unsigned)id >= (unsigned)kv.n_pages;
+          bad |= (unsigned)id >= (unsigned)kv.n_pages && (b + 1) * kv.T > vis0;
         }
         sh.ids[w][i % NIDS] = id;
       }
@@ -965,6 +950,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     auto step = [&](const int tile, auto edge_c) {
       constexpr bool EDGE = decltype(edge_c)::value;
       const bool more = tile + KU < p.key1;
+      auto finish = [&] {
+        if (more) commit(slot ^ 1);
+        slot ^= 1;
+      };
       // this tile's loads have arrived, of every wave (a barrier alone does not wait
       // for loads that go to LDS), and the last tile is read
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -1001,7 +990,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || any_bad;
           if (edge) {
             unsigned long long bad = 0;
-            if (any_bad) {
+            if (__builtin_expect(any_bad, 0)) {
               const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
               bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
                              (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
@@ -1042,14 +1031,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           p_operand<A, false>(pr, pf[q], unused);
         };
         // ---- O^T += V^T P^T
-        if constexpr (!EDGE) {
-          // the exponentials of one step and the operands' reads beside the products
-          // of the step before
+        // the exponentials of one step and the operands' reads beside the products of
+        // the step before
+        auto products = [&](auto exps) {
           const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
           u32x4 vf[2][ND];
 #pragma unroll
           for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
-          take_exp(0);
+          if (exps.value) take_exp(0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             __builtin_amdgcn_sched_barrier(0);
@@ -1059,8 +1048,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             }
 #pragma unroll
             for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
-            if (q < 3) take_exp(q + 1);
+            if (exps.value && q < 3) take_exp(q + 1);
           }
+        };
+        if constexpr (!EDGE) {
+          products(std::true_type{});
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) take_exp(q);
@@ -1080,6 +1072,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
               }
             odd_any = __ballot(odd) != 0;
           }
+          if (__builtin_expect(!dead && !odd_any, 1)) {
+            products(std::false_type{});
+            return finish();
+          }
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const uint32_t lv = (q < 2 ? live[0] : live[1]) >> (8 * (q & 1));
@@ -1092,7 +1088,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             for (int n = 0; n < ND; ++n) {
               u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
               if (dead) v = keep8(v, lv);
-              if (odd_any) {
+              if (__builtin_expect(odd_any, 0)) {
                 const u32x4 vis = ones8<A>(sv);
 #pragma unroll 1
                 for (int cls = 0; cls < 3; ++cls) {
@@ -1108,11 +1104,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           }
         }
       }
-      if (more) commit(slot ^ 1);
-      slot ^= 1;
+      finish();
     };
     // tiles [clean0, clean1) that all rows of the block see whole, if their pages are there
-    const int bmin = base + token_of(a, p.row0), bmax = base + token_of(a, p.row0 + p.rows - 1);
     const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
     for (int tile = p.key0; tile < p.key1;) {
       const int stop = min(clean1, p.key1);
@@ -1200,6 +1194,13 @@ size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t 
   const bool few = few_rows(group, max_q_len);
   const size_t G = (size_t)blocks_of(n_cu), TR = few ? 16 : 128, D = (size_t)ty.D;
   return G * (sizeof(PartDesc) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
+}
+
+int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len) {
+  const bool few = few_rows(group, max_q_len);
+  const int TR = few ? 16 : 128, KU = few ? 128 : 64;
+  const int64_t tiles = ((int64_t)v.n_tokens * group + TR - 1) / TR + v.n_seqs;
+  return tiles * v.H * ((int64_t)v.nb * v.T / KU + 2);
 }
 
 hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {

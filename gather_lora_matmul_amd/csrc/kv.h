@@ -104,6 +104,8 @@ struct AttendArgs {
   int32_t n_cu;
 };
 size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len);
+// A bound of the units of work of a call, to stay below 2^31.
+int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len);
 hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s);
 
 struct VerifyArgs {

@@ -171,6 +171,8 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(LORA_E_ARG, "scale must be positive and finite");
   if (window < 0) return fail(LORA_E_ARG, "negative window");
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_q_len == 0) return LORA_OK;
+  if (attend_units(a.kv, n_q_heads / d->n_kv_heads, b->max_q_len) > INT32_MAX)
+    return fail(LORA_E_UNSUPPORTED, "more than 2^31 units of work: split the call's tokens");
   const int64_t row = (int64_t)n_q_heads * d->head_dim;
   LORA_TRY(check_rows(q_dev, q_ld, row, "q"));
   LORA_TRY(check_rows(out_dev, out_ld, row, "out"));
