@@ -9,10 +9,12 @@
 // that their sums, and with them the token, are the same for every split and
 // order of the work.
 //
-// Bound by the reads of one p row and (after a refusal) one q row a sequence.
-// Two launches: the sums of pieces of kPiece probabilities, all sequences' pieces
-// at once; then one block a sequence finds the piece that holds the level, reads
-// that piece again and finds the token.
+// Bound by the reads of one p row and (after a refusal) one q row a sequence.  The
+// rows are summed in regions of 512 probabilities (a wave each), a scan of the
+// regions' sums finds the one that holds the level, and that one is read again for
+// the token.  Enough sequences, or few probabilities, are one launch with a block
+// of 16 waves a sequence; else the regions' sums are a launch over the whole chip
+// and the scan is a second one.
 #include "kcommon.h"
 #include "kv.h"
 
@@ -20,24 +22,22 @@ namespace lora {
 
 namespace {
 
-constexpr int kPiece = 2048;
-constexpr int kThreads = 256;
-constexpr int kPer = kPiece / kThreads;
+constexpr int kRegion = 512;             // probabilities of a region: 8 a lane
+constexpr int kMaxRegions = (1 << 18) / kRegion;
 
-struct VerifySums {
-  uint64_t rest, all;   // of max(p - q, 0) and of p
+// A weight in whole multiples of 2^-44 as hi * 2^22 + lo: two exact products and
+// two conversions that round down.  Sums of 512 of them fit 32 bits.
+struct Weight {
+  uint32_t hi, lo;
 };
-
-// x clamped to [0, 1] (NaN: 0) in whole multiples of 2^-44, rounded down.
-__device__ __forceinline__ uint64_t fixed44(float x) {
-  if (!(x > 0.f)) return 0;
-  if (x >= 1.f) return 1ull << 44;
-  const uint32_t b = __float_as_uint(x);
-  const int e = (int)(b >> 23);
-  const uint32_t mant = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
-  const int sh = e - 106;   // mant * 2^(e - 150) * 2^44
-  return sh >= 0 ? (uint64_t)mant << sh : (sh > -24 ? mant >> -sh : 0);
+__device__ __forceinline__ Weight fixed44(float x) {
+  const float t = fminf(fmaxf(x, 0.f), 1.f) * 0x1p22f;   // NaN: 0
+  Weight w;
+  w.hi = (uint32_t)t;
+  w.lo = (uint32_t)(__builtin_amdgcn_fractf(t) * 0x1p22f);
+  return w;
 }
+__device__ __forceinline__ uint64_t whole(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 22) + lo; }
 
 template <typename T>
 __device__ __forceinline__ float prob(const void* base, int64_t i) {
@@ -59,8 +59,8 @@ __device__ __forceinline__ void rows_of(const VerifyArgs& a, int s, int& b, int&
 }
 
 // The drafted tokens of one sequence that are accepted; the same in every wave.
-// Every thread of the block calls it.
-template <typename T>
+// Every one of the block's THREADS threads calls it.
+template <typename T, int THREADS>
 __device__ __forceinline__ VerifySeq accept(const VerifyArgs& a, int s) {
   VerifySeq r;
   int b, e;
@@ -69,7 +69,7 @@ __device__ __forceinline__ VerifySeq accept(const VerifyArgs& a, int s) {
   r.k = e - b - 1;
   // each sequence with rows before this one has one row that is no draft's
   r.drow = (int64_t)b;
-  for (int i0 = 0; i0 < s; i0 += kThreads) {
+  for (int i0 = 0; i0 < s; i0 += THREADS) {
     const int i = i0 + (int)threadIdx.x;
     int ib = 0, ie = 0;
     if (i < s) rows_of(a, i, ib, ie);
@@ -97,183 +97,255 @@ __device__ __forceinline__ VerifySeq accept(const VerifyArgs& a, int s) {
   return r;
 }
 
-// Weights of the thread's probabilities of a piece: element piece * kPiece +
-// e(j) with e(j) = j * 256 + tid, or 4 (8) consecutive ones where rows are
-// aligned for 16-byte loads.
-template <typename T, bool VEC>
-__device__ __forceinline__ int elem(int j) {
-  constexpr int E = 16 / ET<T>::bytes;
-  return VEC ? (j / E * kThreads + (int)threadIdx.x) * E + j % E : j * kThreads + (int)threadIdx.x;
+// Rows of the token that follows the accepted ones: p, and q after a refusal.
+struct VerifyRows {
+  const char* p;
+  const char* q;   // null: nothing to subtract
+  int drop;        // token that the draft proposed with certainty, -1: none
+};
+template <typename T>
+__device__ __forceinline__ VerifyRows rows_at(const VerifyArgs& a, const VerifySeq& r) {
+  VerifyRows w;
+  w.p = reinterpret_cast<const char*>(a.target) + (int64_t)(r.q0 + r.first) * a.target_ld * ET<T>::bytes;
+  w.q = nullptr;
+  w.drop = -1;
+  if (r.first < r.k) {
+    if (a.draft) w.q = reinterpret_cast<const char*>(a.draft) + (r.drow + r.first) * a.draft_ld * ET<T>::bytes;
+    else w.drop = a.drafted[r.drow + r.first];
+  }
+  return w;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_piece(const void* base, int64_t row0, int v0, int vocab, float* f) {
-  constexpr int E = 16 / ET<T>::bytes;
-  if constexpr (VEC) {
+
+// Eight consecutive probabilities from v on, rows aligned to their elements only
+// (16-byte loads need no more here); past the row's end 0.
+template <typename T>
+__device__ __forceinline__ void load8(const char* row, int v, int vocab, float* f) {
+  constexpr int B = 8 * ET<T>::bytes;
+  if (v + 8 <= vocab) {
+    uint4 u[B / 16];
+    __builtin_memcpy(u, row + (int64_t)v * ET<T>::bytes, B);
 #pragma unroll
-    for (int j = 0; j < kPer; j += E) {
-      const int v = v0 + elem<T, true>(j);
-      if (v + E <= vocab) {
-        unpack16<T>(ld16(reinterpret_cast<const char*>(base) + (row0 + v) * ET<T>::bytes), f + j);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) f[j + i] = v + i < vocab ? prob<T>(base, row0 + v + i) : 0.f;
-      }
-    }
+    for (int i = 0; i < B / 16; ++i) unpack16<T>(u[i], f + i * (16 / ET<T>::bytes));
   } else {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int v = v0 + elem<T, false>(j);
-      f[j] = v < vocab ? prob<T>(base, row0 + v) : 0.f;
-    }
+    for (int j = 0; j < 8; ++j) f[j] = v + j < vocab ? prob<T>(row, v + j) : 0.f;
   }
 }
 
-// (p, max(p - q, 0)) of the thread's elements of a piece at the row of the new token.
-template <typename T, bool VEC>
-__device__ __forceinline__ void piece_weights(const VerifyArgs& a, const VerifySeq& r, int piece, float* p,
-                                              float* rest) {
-  const int v0 = piece * kPiece;
-  load_piece<T, VEC>(a.target, (int64_t)(r.q0 + r.first) * a.target_ld, v0, a.vocab, p);
-  if (r.first >= r.k) {
+// The lane's eight differences of a region (SELF: the target's own probabilities).
+template <typename T, bool SELF>
+__device__ __forceinline__ void region_rest(const VerifyRows& w, int region, int vocab, float* f) {
+  const int v = region * kRegion + (threadIdx.x & 63) * 8;
+  load8<T>(w.p, v, vocab, f);
+  if (SELF) return;
+  if (w.q) {
+    float q[8];
+    load8<T>(w.q, v, vocab, q);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) rest[j] = p[j];
-  } else if (a.draft) {
-    load_piece<T, VEC>(a.draft, (r.drow + r.first) * a.draft_ld, v0, a.vocab, rest);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) rest[j] = p[j] - rest[j];
-  } else {
-    const int tok = a.drafted[r.drow + r.first] - v0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) rest[j] = elem<T, VEC>(j) == tok ? 0.f : p[j];
+    for (int j = 0; j < 8; ++j) f[j] -= q[j];
   }
+  const int d = w.drop - v;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = j == d ? 0.f : f[j];
 }
 
-__device__ __forceinline__ uint64_t wave_add(uint64_t x) {
+__device__ __forceinline__ uint32_t wave_add(uint32_t x) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
-
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_verify_sums(VerifyArgs a, VerifySums* __restrict__ sums) {
-  __shared__ VerifySums sh[kThreads / 64];
-  const int s = blockIdx.y, piece = blockIdx.x;
-  const VerifySeq r = accept<T>(a, s);
-  if (r.k < 0) return;
-  float p[kPer], rest[kPer];
-  piece_weights<T, VEC>(a, r, piece, p, rest);
-  VerifySums w{0, 0};
+__device__ __forceinline__ uint64_t region_sum(const float* f) {
+  uint32_t hi = 0, lo = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    w.rest += fixed44(rest[j]);
-    w.all += fixed44(p[j]);
+  for (int j = 0; j < 8; ++j) {
+    const Weight w = fixed44(f[j]);
+    hi += w.hi;
+    lo += w.lo;
   }
-  w.rest = wave_add(w.rest);
-  w.all = wave_add(w.all);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = w;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 64; ++i) {
-      w.rest += sh[i].rest;
-      w.all += sh[i].all;
-    }
-    sums[(int64_t)s * gridDim.x + piece] = w;
-  }
+  return whole(wave_add(hi), wave_add(lo));
 }
 
-// Inclusive prefix sums of x over the block; total returned.
-__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sh, uint64_t& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ uint64_t wave_scan(uint64_t x) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint64_t y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 63) sh[wave] = x;
-  __syncthreads();
-  total = 0;
-  for (int i = 0; i < kThreads / 64; ++i) {
-    if (i < wave) x += sh[i];
-    total += sh[i];
-  }
-  __syncthreads();
   return x;
 }
 
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_verify_pick(VerifyArgs a, const VerifySums* __restrict__ sums,
-                                                           int pieces) {
-  __shared__ uint64_t sh[kThreads / 64];
-  __shared__ uint64_t weight[kPiece];
-  __shared__ uint64_t sh_before;
-  __shared__ int sh_piece, sh_token;
+// Sums of the regions first, first + step, .. of a sequence's rows, by one wave.
+template <typename T, bool SELF>
+__device__ __forceinline__ void sum_regions(const VerifyArgs& a, const VerifyRows& w, int first, int step,
+                                            int regions, uint64_t* sums) {
+  constexpr int U = 2;   // regions on their way at a time
+  for (int g = first; g < regions; g += U * step) {
+    float f[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (g + u * step < regions) region_rest<T, SELF>(w, g + u * step, a.vocab, f[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (g + u * step < regions) {
+        const uint64_t x = region_sum(f[u]);
+        if ((threadIdx.x & 63) == 0) sums[g + u * step] = x;
+      }
+  }
+}
+
+// From the regions' sums (LDS) to the token, by one wave: total, level, region,
+// token.  -2: all weights are 0.
+template <typename T, bool SELF>
+__device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows& w, int regions,
+                                    const uint64_t* sums) {
+  const int lane = threadIdx.x & 63;
+  constexpr int N = kMaxRegions / 64;
+  uint64_t own = 0, x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int g = lane * N + i;
+    x[i] = g < regions ? sums[g] : 0;
+    own += x[i];
+  }
+  const uint64_t end = wave_scan(own);
+  const uint64_t total = __shfl(end, 63);
+  if (total == 0) return -2;
+  float u = a.u_sample[s];
+  u = u > 0.f ? (u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f) : 0.f;
+  const uint64_t part = (uint64_t)(uint32_t)(u * 0x1p31f);
+  const uint64_t level = (total >> 31) * part + (((total & 0x7fffffffull) * part) >> 31);
+  // the lane, then its region, that pass the level (total > level, so there is one)
+  const int src = __builtin_ctzll(__ballot(end > level));
+  uint64_t before = end - own;
+  int at = N - 1;
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) {
+    uint64_t upto = end - own;
+#pragma unroll
+    for (int j = 0; j <= i; ++j) upto += x[j];
+    if (upto > level) at = i;
+  }
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i)
+    if (i < at) before += x[i];
+  const int region = __shfl(lane * N + at, src);
+  before = __shfl(before, src);
+  float f[8];
+  region_rest<T, SELF>(w, region, a.vocab, f);
+  uint64_t y[8], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const Weight e = fixed44(f[j]);
+    y[j] = whole(e.hi, e.lo);
+    sum += y[j];
+  }
+  const uint64_t up = before + wave_scan(sum);
+  const int tl = __builtin_ctzll(__ballot(up > level));
+  uint64_t c = up - sum;
+  int tok = 7;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c += y[j];
+    if (c > level && tok == 7) tok = j;
+  }
+  return __shfl(region * kRegion + lane * 8 + tok, tl);
+}
+
+// The token and the outputs of one sequence, from the regions' sums in LDS.
+template <typename T, int THREADS>
+__device__ __forceinline__ void finish(const VerifyArgs& a, int s, const VerifySeq& r, const VerifyRows& w,
+                                       int regions, uint64_t* sums, int* sh) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  if (wave == 0) {
+    const int tok = pick<T, false>(a, s, w, regions, sums);
+    if (tid == 0) *sh = tok;
+  }
+  __syncthreads();
+  int tok = *sh;
+  if (tok == -2) {   // the draft covers the target: the target's own probabilities
+    sum_regions<T, true>(a, w, wave, THREADS / 64, regions, sums);
+    __syncthreads();
+    if (wave == 0) {
+      tok = pick<T, true>(a, s, w, regions, sums);
+      if (tid == 0) *sh = tok == -2 ? -1 : tok;
+    }
+    __syncthreads();
+    tok = *sh;
+  }
+  for (int t = tid; t <= (r.k > 0 ? r.k : 0); t += THREADS)
+    a.tokens[r.q0 + t] = t < r.first ? a.drafted[r.drow + t] : (t == r.first ? tok : -1);
+  if (tid == 0) a.n_out[s] = r.first + 1;
+}
+
+// What the first of two launches leaves for the second, ahead of a sequence's sums.
+struct VerifyHead {
+  VerifySeq r;
+  int64_t pad;
+};
+static_assert(sizeof(VerifyHead) % 8 == 0, "sums follow");
+__host__ __device__ inline size_t seq_words(int regions) { return sizeof(VerifyHead) / 8 + (size_t)regions; }
+
+template <typename T>
+__global__ __launch_bounds__(1024) void k_verify_one(VerifyArgs a, int regions) {
+  __shared__ uint64_t sums[kMaxRegions];
+  __shared__ int sh;
   const int s = blockIdx.x, tid = threadIdx.x;
-  const VerifySeq r = accept<T>(a, s);
+  const VerifySeq r = accept<T, 1024>(a, s);
   if (r.k < 0) {
     if (tid == 0) a.n_out[s] = 0;
     return;
   }
-  // pieces <= 256: a thread each
-  VerifySums mine{0, 0};
-  if (tid < pieces) mine = sums[(int64_t)s * pieces + tid];
-  uint64_t total, total_all;
-  const uint64_t up = block_scan(mine.rest, sh, total);
-  const uint64_t up_all = block_scan(mine.all, sh, total_all);
-  const bool rest = total > 0;   // else the draft covers the target: its own probabilities
-  const uint64_t T_ = rest ? total : total_all;
-  float u = a.u_sample[s];
-  u = u > 0.f ? (u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f) : 0.f;
-  const uint64_t part = (uint64_t)(uint32_t)(u * 0x1p31f);
-  const uint64_t level = (T_ >> 31) * part + (((T_ & 0x7fffffffull) * part) >> 31);
-  const uint64_t x = rest ? up : up_all, m = rest ? mine.rest : mine.all;
-  if (tid == 0) sh_token = -1;
-  if (x > level && x - m <= level) {
-    sh_piece = tid;
-    sh_before = x - m;
-  }
+  const VerifyRows w = rows_at<T>(a, r);
+  sum_regions<T, false>(a, w, tid >> 6, 16, regions, sums);
   __syncthreads();
-  if (T_ > 0) {
-    float p[kPer], re[kPer];
-    const int piece = sh_piece;
-    piece_weights<T, VEC>(a, r, piece, p, re);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) weight[elem<T, VEC>(j)] = fixed44(rest ? re[j] : p[j]);
-    __syncthreads();
-    uint64_t own = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) own += weight[tid * kPer + j];
-    uint64_t all;
-    const uint64_t end = sh_before + block_scan(own, sh, all);
-    if (end > level && end - own <= level) {
-      uint64_t c = end - own;
-      int j = 0;
-      for (; j < kPer - 1; ++j) {
-        c += weight[tid * kPer + j];
-        if (c > level) break;
-      }
-      sh_token = piece * kPiece + tid * kPer + j;
-    }
-    __syncthreads();
-  }
-  for (int t = tid; t <= (r.k > 0 ? r.k : 0); t += kThreads)
-    a.tokens[r.q0 + t] = t < r.first ? a.drafted[r.drow + t] : (t == r.first ? sh_token : -1);
-  if (tid == 0) a.n_out[s] = r.first + 1;
+  finish<T, 1024>(a, s, r, w, regions, sums, &sh);
 }
 
 template <typename T>
+__global__ __launch_bounds__(256) void k_verify_sums(VerifyArgs a, uint64_t* __restrict__ ws, int regions) {
+  const int s = blockIdx.y, tid = threadIdx.x;
+  uint64_t* head = ws + s * seq_words(regions);
+  const VerifySeq r = accept<T, 256>(a, s);
+  if (blockIdx.x == 0 && tid == 0) reinterpret_cast<VerifyHead*>(head)->r = r;
+  if (r.k < 0) return;
+  const VerifyRows w = rows_at<T>(a, r);
+  sum_regions<T, false>(a, w, blockIdx.x * 4 + (tid >> 6), gridDim.x * 4, regions,
+                        head + sizeof(VerifyHead) / 8);
+}
+
+template <typename T>
+__global__ __launch_bounds__(512) void k_verify_pick(VerifyArgs a, const uint64_t* __restrict__ ws, int regions) {
+  __shared__ uint64_t sums[kMaxRegions];
+  __shared__ int sh;
+  const int s = blockIdx.x, tid = threadIdx.x;
+  const uint64_t* head = ws + s * seq_words(regions);
+  const VerifySeq r = reinterpret_cast<const VerifyHead*>(head)->r;
+  if (tid < regions) sums[tid] = head[sizeof(VerifyHead) / 8 + tid];
+  if (r.k < 0) {
+    if (tid == 0) a.n_out[s] = 0;
+    return;
+  }
+  __syncthreads();
+  finish<T, 512>(a, s, r, rows_at<T>(a, r), regions, sums, &sh);
+}
+
+// One launch where a block a sequence is enough to read the rows.  Measured on
+// MI355X, us of one launch / of two, by sequences, f32 with drafts: 32000
+// probabilities 6.7 / 8.5 (1), 8.7 / 8.4 (16), 9.5 / 10.1 (128); 131071 15.4 / 8.2
+// (1), 21.6 / 16.5 (64), 22.9 / 23.2 (128), 35.7 / 40.0 (256); 262144 26.8 / 8.3
+// (1), 44.3 / 38.4 (128), 72 / 82 (256).
+bool one_launch(const VerifyArgs& a) { return a.vocab <= 32768 || a.n_seqs >= 192; }
+
+template <typename T>
 hipError_t launch(const VerifyArgs& a, hipStream_t s) {
-  const int pieces = (a.vocab + kPiece - 1) / kPiece;
-  VerifySums* sums = reinterpret_cast<VerifySums*>(a.ws);
-  auto ok16 = [](const void* p, int64_t ld) {
-    return ((uintptr_t)p & 15) == 0 && (ld * ET<T>::bytes & 15) == 0;
-  };
-  const dim3 grid((unsigned)pieces, (unsigned)a.n_seqs);
-  if (ok16(a.target, a.target_ld) && (!a.draft || ok16(a.draft, a.draft_ld))) {
-    hipLaunchKernelGGL((k_verify_sums<T, true>), grid, dim3(kThreads), 0, s, a, sums);
-    hipLaunchKernelGGL((k_verify_pick<T, true>), dim3(a.n_seqs), dim3(kThreads), 0, s, a, sums, pieces);
+  const int regions = (a.vocab + kRegion - 1) / kRegion;
+  if (one_launch(a)) {
+    hipLaunchKernelGGL((k_verify_one<T>), dim3(a.n_seqs), dim3(1024), 0, s, a, regions);
   } else {
-    hipLaunchKernelGGL((k_verify_sums<T, false>), grid, dim3(kThreads), 0, s, a, sums);
-    hipLaunchKernelGGL((k_verify_pick<T, false>), dim3(a.n_seqs), dim3(kThreads), 0, s, a, sums, pieces);
+    uint64_t* ws = reinterpret_cast<uint64_t*>(a.ws);
+    hipLaunchKernelGGL((k_verify_sums<T>), dim3((regions + 7) / 8, a.n_seqs), dim3(256), 0, s, a, ws, regions);
+    hipLaunchKernelGGL((k_verify_pick<T>), dim3(a.n_seqs), dim3(512), 0, s, a, ws, regions);
   }
   return hipGetLastError();
 }
@@ -281,7 +353,7 @@ hipError_t launch(const VerifyArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t verify_workspace(int32_t n_seqs, int32_t vocab) {
-  return (size_t)n_seqs * (size_t)((vocab + kPiece - 1) / kPiece) * sizeof(VerifySums);
+  return (size_t)n_seqs * seq_words((vocab + kRegion - 1) / kRegion) * sizeof(uint64_t);
 }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
