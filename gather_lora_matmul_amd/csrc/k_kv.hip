@@ -21,21 +21,28 @@ constexpr int kWaves = 4;  // waves of a block
 // (q_len + 2 E - 2) / E <= q_len / E + 2 of them, which is less than the
 // distance to the next sequence's first number.  A number therefore names its
 // sequence without any prefix sums, and a wave finds it with two probes of 64.
+// The lengths of the sequences probed last come with the probe: they are a load
+// less on the way to the rows.
 template <int E>
-__device__ __forceinline__ int kv_find_seq(const KvView& v, int w, int lane) {
+__device__ __forceinline__ int kv_find_seq(const KvView& v, int w, int lane, KvSeq& q) {
   int base = 0;
   for (int stride = v.n_seqs > 64 ? 64 : 1;; stride = 1) {
     const int s = base + lane * stride;
+    KvSeq mine{0, 0, 0};
     bool le = false;
     if (s < v.n_seqs) {
-      int q0 = v.q_start[s];
-      q0 = q0 < 0 ? 0 : (q0 > v.n_tokens ? v.n_tokens : q0);
-      le = q0 / E + 2 * s <= w;
+      mine = kv_seq(v, s);
+      le = mine.q0 / E + 2 * s <= w;
     }
     const unsigned long long m = __ballot(le);
-    if (!m) return base;
-    base += (63 - __builtin_clzll(m)) * stride;
-    if (stride == 1) return base;
+    const int at = m ? 63 - __builtin_clzll(m) : 0;
+    base += at * stride;
+    if (stride == 1) {
+      q.q0 = __builtin_amdgcn_readlane(mine.q0, at);
+      q.q_len = __builtin_amdgcn_readlane(mine.q_len, at);
+      q.kv_len = __builtin_amdgcn_readlane(mine.kv_len, at);
+      return base;
+    }
   }
 }
 
@@ -48,8 +55,8 @@ struct Group {
 
 template <int E, int D>
 __device__ __forceinline__ bool kv_group(const KvView& v, int w, int h, int lane, Group& g) {
-  const int s = kv_find_seq<E>(v, w, lane);
-  const KvSeq q = kv_seq(v, s);
+  KvSeq q;
+  const int s = kv_find_seq<E>(v, w, lane, q);
   const int p0 = q.kv_len > q.q_len ? q.kv_len - q.q_len : 0;  // rows before position 0 have no place
   const int first = p0 / E;
   const int pos = (first + (w - (q.q0 / E + 2 * s))) * E;
@@ -75,7 +82,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_write16(KvView v, const uint
                                                              const uint16_t* __restrict__ vv, int64_t ld,
                                                              int items) {
   const int lane = threadIdx.x & 63;
-  const int item = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   if (item >= items) return;
   const int w = item / v.H, h = item - w * v.H;
   Group g;
@@ -136,7 +143,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_read16(KvView v, uint16_t* _
                                                             uint16_t* __restrict__ vv, int64_t ld,
                                                             int items) {
   const int lane = threadIdx.x & 63;
-  const int item = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   if (item >= items) return;
   const int w = item / v.H, h = item - w * v.H;
   Group g;
@@ -203,7 +210,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_write8(KvView v, const uint1
                                                             const uint16_t* __restrict__ vv, int64_t ld,
                                                             int items) {
   __shared__ __align__(16) uint32_t sh[kWaves][16][D / 4];  // V codes [token][element]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int item = blockIdx.x * kWaves + wave;
   if (item >= items) return;
   const int w = item / v.H, h = item - w * v.H;
@@ -302,7 +309,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_kv_read8(KvView v, uint16_t* __
                                                            uint16_t* __restrict__ vv, int64_t ld,
                                                            int items) {
   const int lane = threadIdx.x & 63;
-  const int item = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   if (item >= items) return;
   const int w = item / v.H, h = item - w * v.H;
   Group g;
