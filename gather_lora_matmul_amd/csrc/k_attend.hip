@@ -206,7 +206,7 @@ __device__ __forceinline__ int wave_add(int x) {
 }
 
 // All units of a call are fewer than 2^31 (attend_units, checked on the host).
-struct Cut {
+struct Cut {               // ("block": the worker, which may be a wave)
   int pos, end;          // this block's range of units
   int each, over;        // block L's range begins at L each + min(L, over)
   int block, blocks;     // its number in the order of the ranges, and the blocks that have one
@@ -222,14 +222,17 @@ struct Cut {
 // block computes them itself: the lengths are a few KB that stay in L2.  A lane
 // adds up the tiles of its sequence if they are few, all lanes together those of
 // each other one.
-template <int KU, int TR, int THREADS>
-__device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c) {
+// Of `workers` workers (blocks, or waves) this is number i of those on its XCD.
+// A worker gets MINU units at least, as long as that leaves a worker a tile.
+template <int KU, int TR, int THREADS, int MINU>
+__device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, int workers, int i) {
   const int n = a.kv.n_seqs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int W = THREADS / 64, FEW = 2;
   int* wsum = pre + kKvMaxSeqs + 1;
   int run = 0;
   const bool small = n <= 64;   // every wave for itself
+  int n_tiles = 0;
   for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
     const int s = s0 + (small ? lane : tid);
     int units = 0;
@@ -248,6 +251,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c) 
       part = wave_add(part);
       if (lane == src) units += part;
     }
+    if (MINU > 1 && small) n_tiles = wave_add(tiles) * a.kv.H;
     int sum = units * a.kv.H;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -274,14 +278,12 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c) 
   const int total = uni(pre[n]);
   // blocks b, b + 8, ... run on one XCD: give each XCD one contiguous eighth of
   // the ranges, so that the tiles that read the same keys share an L2
-  const int G = (int)gridDim.x;
-  const int b = (int)blockIdx.x;
-  c.blocks = min(total, G);
+  c.blocks = min(MINU > 1 && small ? max((total + MINU - 1) / MINU, n_tiles) : total, workers);
   const int per = (c.blocks + 7) >> 3;
-  const int L = (b & 7) * per + (b >> 3);
+  const int L = ((int)blockIdx.x & 7) * per + i;
   c.block = L;
   c.pos = c.end = 0;
-  if ((b >> 3) >= per || L >= c.blocks) return;
+  if (i >= per || L >= c.blocks) return;
   c.each = (int)((uint32_t)total / (uint32_t)c.blocks);
   c.over = total - c.each * c.blocks;
   c.pos = c.begin_of(L);
@@ -373,10 +375,8 @@ struct Parts {
 };
 
 // Tell the joining launch about this block's first piece: a tile's parts are
-// joined by the block whose first piece is the last of several.
-template <int TR, int D>
-__device__ __forceinline__ void describe(const Parts<TR, D>& parts, const Cut& c, const Piece* p) {
-  if (threadIdx.x != 0) return;
+// joined by the block whose first piece is the last of several.  One lane.
+__device__ __forceinline__ void describe(PartDesc* at, const Cut& c, const Piece* p) {
   PartDesc d{};
   d.last = -1;
   if (p && p->ends && !p->begins) {
@@ -389,7 +389,7 @@ __device__ __forceinline__ void describe(const Parts<TR, D>& parts, const Cut& c
     d.rows = p->rows;
     d.q0 = p->q.q0;
   }
-  parts.desc[blockIdx.x] = d;
+  *at = d;
 }
 
 // Maximum of three in one instruction (fmaxf would quiet every operand first).  A
@@ -402,33 +402,62 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- the joining launch ----------------------------------------------------------
-// D / 4 lanes a row: weights of the parts by their maxima, then a weighted sum.
-// Bound by the reads of the parts; each is a contiguous D * 4 bytes.
-template <typename A, int D, int TR>
+// RB rows a block: weights of the parts by their maxima, then a
+// weighted sum, D / 4 lanes a part and several parts at a time.  Bound by the reads
+// of the parts; each is a contiguous D * 4 bytes.
+template <typename A, int D, int TR, int RB>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
+  constexpr int LR = D / 4, PG = 256 / RB / LR;            // lanes of a part, parts at a time
+  constexpr int RW = 256 / RB < 64 ? 256 / RB : 64;        // lanes of a row in a wave
+  __shared__ __align__(16) f32x4 sh_acc[4][LR];
+  __shared__ float sh_sum[4];
   const Parts<TR, D> parts(a.ws, G);
   const PartDesc d = parts.desc[blockIdx.x];
   const int L = d.last;
   if (L < 0) return;
-  constexpr int LR = D / 4, RB = 256 / LR;   // lanes of a row, rows of a block
-  const int li = threadIdx.x % LR;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = tid % LR, pg = tid % (256 / RB) / LR;
   auto slot = [&](int j) { return (int64_t)(2 * j + (j == d.first ? d.first_slot : 0)) * TR; };
-  for (int r = blockIdx.y * RB + threadIdx.x / LR; r < d.rows; r += gridDim.y * RB) {
+  for (int r0 = blockIdx.y * RB; r0 < d.rows; r0 += gridDim.y * RB) {
+    const int r = r0 + tid / (256 / RB);
+    const bool in = r < d.rows;
     float M = -INFINITY;
-    for (int j = d.first + li; j <= L; j += LR) M = fmaxf(M, parts.ml[slot(j) + r].x);
+    if (in)
+      for (int j = d.first + lane % RW; j <= L; j += RW) M = fmaxf(M, parts.ml[slot(j) + r].x);
 #pragma unroll
-    for (int x = LR / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
+    for (int x = RW / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
     const float Mu = safe_max(M);
     f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
     float sum = 0.f;
+    if (in)
 #pragma unroll 4
-    for (int j = d.first; j <= L; ++j) {
-      const int64_t at = slot(j) + r;
-      const float2 ml = parts.ml[at];
-      const float w = exp2f(ml.x - Mu);  // an empty part: exp2(-inf) = 0
-      sum += w * ml.y;
-      acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
+      for (int j = d.first + pg; j <= L; j += PG) {
+        const int64_t at = slot(j) + r;
+        const float2 ml = parts.ml[at];
+        const float w = exp2f(ml.x - Mu);  // an empty part: exp2(-inf) = 0
+        sum += w * ml.y;
+        acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
+      }
+#pragma unroll
+    for (int x = LR; x < RW; x <<= 1) {
+      sum += __shfl_xor(sum, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor(acc[i], x);
     }
+    if constexpr (RB < 4) {   // the row's other waves
+      if (lane < LR) sh_acc[wave][li] = acc;
+      if (lane == 0) sh_sum[wave] = sum;
+      __syncthreads();
+      if (wave % (4 / RB) == 0) {
+#pragma unroll
+        for (int w = 1; w < 4 / RB; ++w) {
+          acc += sh_acc[wave + w][li];
+          sum += sh_sum[wave + w];
+        }
+      }
+      __syncthreads();
+    }
+    if (!in || pg != 0) continue;
     const int row = d.row0 + r;
     const int t = token_of(a, row), head = d.head * a.group + row - t * a.group;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -441,16 +470,19 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
 }
 
 // ---- up to 16 rows ---------------------------------------------------------------
-// Four waves a block, each with its own keys, all with all of the tile's rows; K
-// and V go from memory to registers (every byte is used once: LDS would only add
+// K and V go from memory to registers (every byte is used once: LDS would only add
 // a trip).  A wave's tile is 4 E keys: 16 KB at D = 128, its next pieces loaded
-// as soon as the products have taken the last ones.
-template <typename A, typename KV, int D>
+// as soon as the products have taken the last ones.  With few (sequence, head)
+// pairs the four waves of a block take a tile of rows together, each every fourth
+// tile of keys, and join their results in LDS; with many (SOLO) every wave works
+// for itself, its range of the units cut as the blocks' ones are: no wave waits
+// for another, and short sequences take their turns on 4 times as many workers.
+template <typename A, typename KV, int D, bool SOLO>
 struct Skinny {
   static constexpr bool Q8 = is_quant<KV>();
   static constexpr int E = ET<KV>::E;
   static constexpr int KT = 4 * E;       // keys of a wave's tile
-  static constexpr int KU = 4 * KT;      // keys of a unit (all waves)
+  static constexpr int KU = SOLO ? KT : 4 * KT;   // keys of a unit
   static constexpr int TR = 16;
   static constexpr int NT = E / 4;       // K operands of 16 tokens
   static constexpr int NC = D / (4 * E); // 16-byte pieces of a K row a lane loads
@@ -459,24 +491,27 @@ struct Skinny {
   using PT = typename std::conditional<Q8, bf16_t, A>::type;  // type of P and V in the second one
 };
 
-template <typename A, typename KV, int D>
+template <typename A, typename KV, int D, bool SOLO>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_rows(AttendArgs a) {
-  using S = Skinny<A, KV, D>;
+  using S = Skinny<A, KV, D, SOLO>;
   using PT = typename S::PT;
   constexpr int E = S::E, KT = S::KT, KU = S::KU, TR = S::TR, NT = S::NT, NC = S::NC, ND = S::ND;
   constexpr bool Q8 = S::Q8;
   __shared__ int pre[kKvMaxSeqs + 1 + 4];
-  __shared__ float sh_ml[4][TR][2];
-  __shared__ __align__(16) float sh_o[4][TR][D + 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float sh_ml[SOLO ? 1 : 4][TR][2];
+  __shared__ __align__(16) float sh_o[SOLO ? 1 : 4][TR][D + 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 15, g = lane >> 4;   // query column, lane group
   const KvView& kv = a.kv;
   Cut c;
-  cut_work<KU, TR, 256>(a, pre, c);
-  const Parts<TR, D> parts(a.ws, (int)gridDim.x);
+  const int workers = SOLO ? 4 * (int)gridDim.x : (int)gridDim.x;
+  cut_work<KU, TR, 256, 1>(a, pre, c, workers, SOLO ? ((int)blockIdx.x >> 3) * 4 + wave : (int)blockIdx.x >> 3);
+  const Parts<TR, D> parts(a.ws, workers);
+  PartDesc* desc = parts.desc + (SOLO ? (int)blockIdx.x * 4 + wave : (int)blockIdx.x);
+  const bool speaker = SOLO ? lane == 0 : tid == 0;
   Piece p;
   int n_piece = 0;
-  if (c.pos >= c.end) describe<TR, D>(parts, c, nullptr);
+  if (c.pos >= c.end && speaker) describe(desc, c, nullptr);
   while (next_piece<KU, TR>(a, pre, c, p)) {
     // ---- queries: operand B of the first product, column = row of the tile
     const int row = p.row0 + min(col, p.rows - 1);
@@ -549,7 +584,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       kscale = ldv(kv.scales + (int64_t)(ok ? kp : 0) * kv.T + (vt - vb * kv.T));
     };
 
-    int tile = p.key0 + wave * KT;
+    int tile = p.key0 + (SOLO ? 0 : wave * KT);
     const bool any = tile < p.key1;
     Ids id, idn;
     if (any) {
@@ -694,16 +729,41 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         idn = find(tile + 2 * KU);
       }
     }
-    // ---- the waves' results
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    if constexpr (SOLO) {
+      const int slot = n_piece == 0 ? 0 : 1;
+      if (col < p.rows) {
+        if (p.begins && p.ends) {
+          const int head = p.head * a.group + row - tq * a.group;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D + 4 * g;
+#pragma unroll
+          for (int n = 0; n < ND; ++n) {
+            const f32x4 x = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o[n];
+            *reinterpret_cast<uint2*>(out + 16 * n) = uint2{pack2<A>(x[0] * inv, x[1] * inv), pack2<A>(x[2] * inv, x[3] * inv)};
+          }
+          if (a.lse && g == 0)
+            a.lse[(int64_t)(p.q.q0 + tq) * a.n_q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          const int64_t at = ((int64_t)c.block * 2 + slot) * TR + col;
+#pragma unroll
+          for (int n = 0; n < ND; ++n) *reinterpret_cast<f32x4*>(parts.o + at * D + 16 * n + 4 * g) = o[n];
+          if (g == 0) parts.ml[at] = float2{m, l};
+        }
+      }
+      if (n_piece == 0 && speaker) describe(desc, c, &p);
+      ++n_piece;
+      continue;
+    }
+    // ---- the waves' results
     if (lane < 16) {
-      sh_ml[wave][col][0] = m;
-      sh_ml[wave][col][1] = l;
+      sh_ml[SOLO ? 0 : wave][col][0] = m;
+      sh_ml[SOLO ? 0 : wave][col][1] = l;
     }
     if (col < p.rows)
 #pragma unroll
-      for (int n = 0; n < ND; ++n) *reinterpret_cast<f32x4*>(&sh_o[wave][col][16 * n + 4 * g]) = o[n];
+      for (int n = 0; n < ND; ++n) *reinterpret_cast<f32x4*>(&sh_o[SOLO ? 0 : wave][col][16 * n + 4 * g]) = o[n];
     __syncthreads();
     const bool whole = p.begins && p.ends;
     const int slot = n_piece == 0 ? 0 : 1;
@@ -711,12 +771,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, sh_ml[w][r][0]);
+      for (int w = 0; w < (SOLO ? 1 : 4); ++w) M = fmaxf(M, sh_ml[w][r][0]);
       const float Mu = safe_max(M);
       float sum = 0.f;
       f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < (SOLO ? 1 : 4); ++w) {
         const float f = exp2f(sh_ml[w][r][0] - Mu);
         sum += f * sh_ml[w][r][1];
         acc += f * *reinterpret_cast<const f32x4*>(&sh_o[w][r][d]);
@@ -735,7 +795,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (d == 0) parts.ml[at] = float2{M, sum};
       }
     }
-    if (n_piece == 0) describe<TR, D>(parts, c, &p);
+    if (n_piece == 0 && speaker) describe(desc, c, &p);
     ++n_piece;
     __syncthreads();
   }
@@ -835,11 +895,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int col = lane & 31, hi = lane >> 5;
   const KvView& kv = a.kv;
   Cut c;
-  cut_work<KU, TR, NW * 64>(a, sh.pre, c);
+  cut_work<KU, TR, NW * 64, 4>(a, sh.pre, c, (int)gridDim.x, (int)blockIdx.x >> 3);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
   Piece p;
   int n_piece = 0;
-  if (c.pos >= c.end) describe<TR, D>(parts, c, nullptr);
+  if (c.pos >= c.end && tid == 0) describe(parts.desc + blockIdx.x, c, nullptr);
   // row col of a K operand is this token of a tile of 32: a lane's 16 scores are
   // those of tokens hi * 8 .. + 7 and 16 + hi * 8 .. + 7
   const int ktok = (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
@@ -851,6 +911,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int row = min(wrow0 + col, p.row0 + p.rows - 1);
     const int tq = token_of(a, row);
     const int pos = base + tq;
+    const int win = a.window > 0 ? a.window : 0x40000000;
     const int posmin = base + token_of(a, wrow0);
     const int posmax = base + token_of(a, wrow0 + max(wrows, 1) - 1);
     u32x4 qf[NQ];
@@ -929,31 +990,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int i = 0; i < ND; ++i) o[i] = f32x16{};
     float m = -INFINITY, l = 0.f;
-    // bits of the lane's 16 tokens of half kt (register r: bit r) that lie in [lo, up] of the tile
-    auto range_bits = [&](int kt, int lo, int up) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int k0 = kt * 32 + q * 16 + hi * 8;
-        const int x = min(max(lo - k0, 0), 8), y = min(max(up - k0 + 1, 0), 8);
-        bits |= (((1u << y) - 1u) & ~((1u << x) - 1u)) << (8 * q);
-      }
-      return bits;
+    // bits of the tokens k0 .. k0 + 7 of the tile that lie in [lo, up]
+    auto run_bits = [](int k0, int lo, int up) {
+      const int x = min(max(lo - k0, 0), 8), y = min(max(up - k0 + 1, 0), 8);
+      return ((1u << y) - 1u) & ~((1u << x) - 1u);
     };
     load_ids(p.key0);
     issue(p.key0, 0);
     commit(0);
     int slot = 0;
-    // The next tile's loads, then this tile's products.  EDGE: some row may not
-    // see all of the tile.  (A loop of its own for the others: one that holds both
-    // keeps two copies of the accumulators.)
-    auto step = [&](const int tile, auto edge_c) {
-      constexpr bool EDGE = decltype(edge_c)::value;
+    // tiles from clean0 to before clean1 are seen whole by all rows of the block, if their pages are there
+    const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
+    for (int tile = p.key0; tile < p.key1; tile += KU, slot ^= 1) {
       const bool more = tile + KU < p.key1;
-      auto finish = [&] {
-        if (more) commit(slot ^ 1);
-        slot ^= 1;
-      };
       // this tile's loads have arrived, of every wave (a barrier alone does not wait
       // for loads that go to LDS), and the last tile is read
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -962,8 +1011,57 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if ((int)kv_div(kv, (uint32_t)(tile + 2 * KU - 1)) - b0 >= NIDS) load_ids(tile);
         issue(tile + KU, slot ^ 1);
       }
-      if (wrows > 0 &&
-          (!EDGE || (tile <= posmax && (a.window <= 0 || tile + KU - 1 > posmin - a.window)))) {
+      const bool edge = tile < clean0 || tile >= clean1 || any_bad;
+      unsigned long long bad = 0;
+      if (edge) {
+        // tokens that no row of the block sees are taken out of V in LDS (0 times what
+        // lies there need not be 0), and what is not finite is looked for
+        if (__builtin_expect(any_bad, 0)) {
+          const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
+          bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
+                         (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+        }
+        const int first = max(bmin - win + 1 - tile, 0), last = min(bmax - tile, KU - 1);   // seen tokens
+        unsigned long long alive = last >= first ? (~0ull >> (63 - last + first)) << first : 0;
+        alive &= ~bad;
+        u32x4* vt = &sh.v[slot][0][0];
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int i = tid; i < KU / 8 * D; i += 256) {
+          const uint32_t byte = (uint32_t)(alive >> (i / D * 8)) & 0xffu;
+          u32x4 v = vt[i];
+          if (byte != 0xffu) {
+            v = keep8(v, byte);
+            vt[i] = v;
+          }
+          odd |= not_finite<A>(v);
+        }
+        if (__builtin_expect(__syncthreads_or(odd != 0), 0)) {
+          // their values go to the rows that see their tokens, then they leave V
+          if (wrows > 0)
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
+              const u32x4 vis = ones8<A>(run_bits(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
+#pragma unroll
+              for (int n = 0; n < ND; ++n) {
+                const u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
+#pragma unroll 1
+                for (int cls = 0; cls < 3; ++cls) {
+                  const f32x16 hit = mfma32<A>(ones8<A>(class_bits<A>(v, cls)), vis, f32x16{});
+                  const float val = class_value(cls);
+#pragma unroll
+                  for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? val : 0.f;
+                }
+              }
+            }
+          __syncthreads();
+#pragma unroll 1
+          for (int i = tid; i < KU / 8 * D; i += 256) vt[i] = keep8(vt[i], ~class_bits<A>(vt[i], 3));
+          __syncthreads();
+        }
+      }
+      if (wrows > 0 && tile <= posmax && tile + KU - 1 > posmin - win) {
         // ---- S^T = K Q^T
         // in groups of four products, whose operands were read a group ahead (the
         // scheduler, left alone, reads each just before its use)
@@ -984,28 +1082,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           __builtin_amdgcn_sched_barrier(0x6);
         }
         // ---- mask
-        bool edge = false;
-        uint32_t live[2] = {0xffffu, 0xffffu}, seen[2] = {0xffffu, 0xffffu};
-        if constexpr (EDGE) {
-          edge = tile + KU - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) || any_bad;
-          if (edge) {
-            unsigned long long bad = 0;
-            if (__builtin_expect(any_bad, 0)) {
-              const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
-              bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
-                             (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
-            }
-            const int w = a.window > 0 ? a.window : 0x40000000;
+        if (edge) {
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-              const uint32_t gone = ((uint32_t)(bad >> (kt * 32 + hi * 8)) & 0xffu) |
-                                    (((uint32_t)(bad >> (kt * 32 + 16 + hi * 8)) & 0xffu) << 8);
-              live[kt] = range_bits(kt, posmin - w + 1 - tile, posmax - tile) & ~gone;
-              seen[kt] = range_bits(kt, pos - w + 1 - tile, pos - tile) & ~gone;
+          for (int h = 0; h < 4; ++h) {
+            const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
+            const uint32_t seen = run_bits(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (!((seen[kt] >> r) & 1)) s[kt][r] = -INFINITY;
-            }
+            for (int r = 0; r < 8; ++r)
+              if (!((seen >> r) & 1)) s[h >> 1][8 * (h & 1) + r] = -INFINITY;
           }
         }
         // ---- running maximum and sum
@@ -1015,7 +1099,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         top = max3(top, __shfl_xor(top, 32), top) * sl;
         if (__ballot(top > m + 8.f)) {
           const float mn = top > m ? top : m;
-          const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+          const float f = m == -INFINITY ? 1.f : exp2f(m - mn);   // (nothing yet, or what is not finite)
           l *= f;
 #pragma unroll
           for (int n = 0; n < ND; ++n) o[n] *= f;
@@ -1033,92 +1117,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         // ---- O^T += V^T P^T
         // the exponentials of one step and the operands' reads beside the products of
         // the step before
-        auto products = [&](auto exps) {
-          const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
-          u32x4 vf[2][ND];
+        const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
+        u32x4 vf[2][ND];
 #pragma unroll
-          for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
-          if (exps.value) take_exp(0);
+        for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
+        take_exp(0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (q < 3) {
+        for (int q = 0; q < 4; ++q) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (q < 3) {
 #pragma unroll
-              for (int n = 0; n < ND; ++n) vf[(q + 1) & 1][n] = vp[2 * (q + 1) * D + n * 32];
-            }
-#pragma unroll
-            for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
-            if (exps.value && q < 3) take_exp(q + 1);
+            for (int n = 0; n < ND; ++n) vf[(q + 1) & 1][n] = vp[2 * (q + 1) * D + n * 32];
           }
-        };
-        if constexpr (!EDGE) {
-          products(std::true_type{});
-        } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) take_exp(q);
-          // in a tile that some row does not see whole: tokens that no row sees are
-          // taken out of V, and what is not finite is looked for
-          bool dead = false, odd_any = false;
-          if (edge) {
-            dead = __ballot((live[0] & live[1]) != 0xffffu) != 0;
-            uint32_t odd = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int n = 0; n < ND; ++n) {
-                u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
-                if (dead) v = keep8(v, live[q >> 1] >> (8 * (q & 1)));
-                odd |= not_finite<A>(v);
-              }
-            odd_any = __ballot(odd) != 0;
-          }
-          if (__builtin_expect(!dead && !odd_any, 1)) {
-            products(std::false_type{});
-            return finish();
-          }
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t lv = (q < 2 ? live[0] : live[1]) >> (8 * (q & 1));
-            const uint32_t sv = (q < 2 ? seen[0] : seen[1]) >> (8 * (q & 1));
-            u32x4 pq = pf[0];
-            if (q == 1) pq = pf[1];
-            if (q == 2) pq = pf[2];
-            if (q == 3) pq = pf[3];
-#pragma unroll
-            for (int n = 0; n < ND; ++n) {
-              u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
-              if (dead) v = keep8(v, lv);
-              if (__builtin_expect(odd_any, 0)) {
-                const u32x4 vis = ones8<A>(sv);
-#pragma unroll 1
-                for (int cls = 0; cls < 3; ++cls) {
-                  const f32x16 hit = mfma32<A>(ones8<A>(class_bits<A>(v, cls)), vis, f32x16{});
-                  const float val = class_value(cls);
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? val : 0.f;
-                }
-                v = keep8(v, ~class_bits<A>(v, 3));
-              }
-              o[n] = mfma32<A>(v, pq, o[n]);
-            }
-          }
+          for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
+          if (q < 3) take_exp(q + 1);
         }
       }
-      finish();
-    };
-    // tiles [clean0, clean1) that all rows of the block see whole, if their pages are there
-    const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
-    for (int tile = p.key0; tile < p.key1;) {
-      const int stop = min(clean1, p.key1);
-      if (tile >= clean0 && tile < stop && !any_bad) {
-        do {
-          step(tile, std::integral_constant<bool, false>{});
-          tile += KU;
-        } while (tile < stop && !any_bad);
-      } else {
-        step(tile, std::integral_constant<bool, true>{});
-        tile += KU;
-      }
+      if (more) commit(slot ^ 1);
     }
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
@@ -1151,7 +1167,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (hi == 0) parts.ml[at] = float2{m, l};
       }
     }
-    if (n_piece == 0) describe<TR, D>(parts, c, &p);
+    if (n_piece == 0 && tid == 0) describe(parts.desc + blockIdx.x, c, &p);
     ++n_piece;
     __syncthreads();  // the slots of this piece have been read
   }
@@ -1161,15 +1177,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 inline bool few_rows(int32_t group, int32_t max_q_len) { return (int64_t)max_q_len * group <= 16; }
 inline int blocks_of(int n_cu) { return 2 * n_cu / 8 * 8; }
 
+// Every wave for itself once there are two (sequence, head) pairs a block.
+inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_seqs * H >= 2 * blocks_of(n_cu); }
+
 template <typename A, typename KV, int D>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
   const int64_t most = (int64_t)a.max_q_len * a.group;
   const bool few = few_rows(a.group, a.max_q_len);
   const int G = blocks_of(a.n_cu);
-  constexpr int RB = 256 / (D / 4);   // rows of a block of the joining launch
-  if (few) {
-    hipLaunchKernelGGL((k_attend_rows<A, KV, D>), dim3(G), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_attend_join<A, D, 16>), dim3(G, (unsigned)((most + RB - 1) / RB)), dim3(256), 0, s, a, G);
+  if (few && solo_waves(a.kv.n_seqs, a.kv.H, a.n_cu)) {
+    hipLaunchKernelGGL((k_attend_rows<A, KV, D, true>), dim3(G), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(4 * G, (unsigned)most), dim3(256), 0, s, a, 4 * G);
+  } else if (few) {
+    hipLaunchKernelGGL((k_attend_rows<A, KV, D, false>), dim3(G), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(G, (unsigned)most), dim3(256), 0, s, a, G);
   } else {
     using TT = Tiles<A, KV, D>;
     const int rows = (int)(most < TT::TR ? most : TT::TR);
@@ -1178,7 +1199,8 @@ hipError_t launch(const AttendArgs& a, hipStream_t s) {
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (attr != hipSuccess) return attr;
     hipLaunchKernelGGL((k_attend_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a);
-    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)), dim3(256), 0, s, a, G);
+    constexpr int RB = 256 / (D / 4);
+    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)), dim3(256), 0, s, a, G);
   }
   return hipGetLastError();
 }
@@ -1190,15 +1212,17 @@ hipError_t launch_d(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len) {
+size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len, int32_t n_seqs,
+                        int32_t H) {
   const bool few = few_rows(group, max_q_len);
-  const size_t G = (size_t)blocks_of(n_cu), TR = few ? 16 : 128, D = (size_t)ty.D;
+  const size_t G = (size_t)blocks_of(n_cu) * (few && solo_waves(n_seqs, H, n_cu) ? 4 : 1);
+  const size_t TR = few ? 16 : 128, D = (size_t)ty.D;
   return G * (sizeof(PartDesc) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
 }
 
 int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len) {
   const bool few = few_rows(group, max_q_len);
-  const int TR = few ? 16 : 128, KU = few ? 128 : 64;
+  const int TR = few ? 16 : 128, KU = few ? 32 : 64;
   const int64_t tiles = ((int64_t)v.n_tokens * group + TR - 1) / TR + v.n_seqs;
   return tiles * v.H * ((int64_t)v.nb * v.T / KU + 2);
 }

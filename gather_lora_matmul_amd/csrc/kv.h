@@ -103,7 +103,8 @@ struct AttendArgs {
   char* ws;
   int32_t n_cu;
 };
-size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len);
+size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len, int32_t n_seqs,
+                        int32_t H);
 // A bound of the units of work of a call, to stay below 2^31.
 int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len);
 hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s);

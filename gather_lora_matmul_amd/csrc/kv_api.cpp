@@ -155,7 +155,8 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* p, const lora_kv_desc
   LORA_TRY(geometry(p, d, ty, T));
   if (!b || !bytes) return fail(LORA_E_ARG, "null batch or size");
   LORA_TRY(check_heads(d, n_q_heads, b));
-  *bytes = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len);
+  *bytes = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len, b->n_seqs,
+                            d->n_kv_heads);
   return LORA_OK;
 }
 
@@ -177,7 +178,8 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   LORA_TRY(check_rows(q_dev, q_ld, row, "q"));
   LORA_TRY(check_rows(out_dev, out_ld, row, "out"));
   if ((uintptr_t)lse_dev & 3u) return fail(LORA_E_ARG, "lse not 4-byte aligned");
-  const size_t need = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len);
+  const size_t need = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len, b->n_seqs,
+                                       d->n_kv_heads);
   if (!workspace_dev || ws_bytes < need)
     return fail(LORA_E_ARG, "workspace of %zu bytes, this call needs %zu (lora_kv_attend_workspace_size)",
                 ws_bytes, need);
