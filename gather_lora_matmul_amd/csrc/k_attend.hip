@@ -169,7 +169,8 @@ struct PartDesc {        // a tile whose last of several parts a block has
   int32_t last;          // that block, -1: none
   int32_t first;         // block of its first part
   int32_t first_slot;
-  int32_t head, row0, rows, q0, pad;
+  int32_t head, row0, rows, q0;
+  int32_t share;         // groups of lanes of the joining launch that a row gets
 };
 
 __device__ __forceinline__ int token_of(const AttendArgs& a, int row) {  // row / group
@@ -223,8 +224,7 @@ struct Cut {               // ("block": the worker, which may be a wave)
 // adds up the tiles of its sequence if they are few, all lanes together those of
 // each other one.
 // Of `workers` workers (blocks, or waves) this is number i of those on its XCD.
-// A worker gets MINU units at least, as long as that leaves a worker a tile.
-template <int KU, int TR, int THREADS, int MINU>
+template <int KU, int TR, int THREADS>
 __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, int workers, int i) {
   const int n = a.kv.n_seqs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -232,7 +232,6 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
   int* wsum = pre + kKvMaxSeqs + 1;
   int run = 0;
   const bool small = n <= 64;   // every wave for itself
-  int n_tiles = 0;
   for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
     const int s = s0 + (small ? lane : tid);
     int units = 0;
@@ -251,7 +250,6 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
       part = wave_add(part);
       if (lane == src) units += part;
     }
-    if (MINU > 1 && small) n_tiles = wave_add(tiles) * a.kv.H;
     int sum = units * a.kv.H;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -278,7 +276,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
   const int total = uni(pre[n]);
   // blocks b, b + 8, ... run on one XCD: give each XCD one contiguous eighth of
   // the ranges, so that the tiles that read the same keys share an L2
-  c.blocks = min(MINU > 1 && small ? max((total + MINU - 1) / MINU, n_tiles) : total, workers);
+  c.blocks = min(total, workers);
   const int per = (c.blocks + 7) >> 3;
   const int L = ((int)blockIdx.x & 7) * per + i;
   c.block = L;
@@ -361,14 +359,16 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, 
 // that is another.
 template <int TR, int D>
 struct Parts {
-  static __host__ __device__ size_t desc_bytes(int G) { return (size_t)G * sizeof(PartDesc); }
+  static __host__ __device__ size_t desc_bytes(int G) { return (size_t)G * (sizeof(PartDesc) + sizeof(int)); }
   static __host__ __device__ size_t ml_bytes(int G) { return (size_t)G * 2 * TR * 2 * sizeof(float); }
   static __host__ __device__ size_t o_bytes(int G) { return (size_t)G * 2 * TR * D * sizeof(float); }
   PartDesc* desc;
+  int* items;   // of each desc, for the list of the joining launch
   float2* ml;   // [slot][row]: maximum (log2 scale), sum
   float* o;     // [slot][row][D]
   __device__ Parts(char* ws, int G) {
     desc = reinterpret_cast<PartDesc*>(ws);
+    items = reinterpret_cast<int*>(ws + G * sizeof(PartDesc));
     ml = reinterpret_cast<float2*>(ws + desc_bytes(G));
     o = reinterpret_cast<float*>(ws + desc_bytes(G) + ml_bytes(G));
   }
@@ -469,6 +469,92 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
   }
 }
 
+// The same for few tiles of 128 rows with very many parts: the rows of all tiles that have parts are items of one list,
+// which the blocks take in turn.  The NG groups of D / 4 lanes of a block take NG /
+// P rows at a time, P groups the parts of each, where P leaves a group four parts
+// or more (PartDesc::share).
+template <typename A, int D, int TR>
+__global__ __launch_bounds__(256) void k_attend_join_list(AttendArgs a, int G) {
+  constexpr int LR = D / 4, NG = 256 / LR, W = 4, MAXG = 1024;
+  __shared__ __align__(16) f32x4 sh_acc[NG][LR];
+  __shared__ float sh_sum[NG];
+  __shared__ int pre[MAXG + 1], wsum[W];
+  const Parts<TR, D> parts(a.ws, G);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = tid % LR, gi = tid / LR;
+  int run = 0;
+  for (int g0 = 0; g0 < G; g0 += 256) {
+    int sum = g0 + tid < G ? parts.items[g0 + tid] : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int z = __shfl_up(sum, d);
+      if (lane >= d) sum += z;
+    }
+    if (lane == 63) wsum[wave] = sum;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < W; ++w) {
+      if (w < wave) sum += wsum[w];
+      all += wsum[w];
+    }
+    if (g0 + tid < G) pre[g0 + tid + 1] = run + sum;
+    run += all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+  for (int it = blockIdx.x; it < run; it += gridDim.x) {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= it) lo = mid;
+      else hi = mid;
+    }
+    const PartDesc d = parts.desc[lo];
+    const int L = d.last, P = d.share, R = NG / P;
+    const int r = (it - pre[lo]) * R + gi / P, pg = gi % P;
+    const bool in = r < d.rows;
+    auto slot = [&](int j) { return (int64_t)(2 * j + (j == d.first ? d.first_slot : 0)) * TR; };
+    float M = -INFINITY;
+    if (in)
+      for (int j = d.first + li; j <= L; j += LR) M = fmaxf(M, parts.ml[slot(j) + r].x);
+#pragma unroll
+    for (int x = LR / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
+    const float Mu = safe_max(M);
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
+    if (in)
+#pragma unroll 4
+      for (int j = d.first + pg; j <= L; j += P) {
+        const int64_t at = slot(j) + r;
+        const float2 ml = parts.ml[at];
+        const float w = exp2f(ml.x - Mu);
+        sum += w * ml.y;
+        acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
+      }
+    if (P > 1) {
+      sh_acc[gi][li] = acc;
+      if (li == 0) sh_sum[gi] = sum;
+      __syncthreads();
+      if (pg == 0)
+        for (int k = 1; k < P; ++k) {
+          acc += sh_acc[gi + k][li];
+          sum += sh_sum[gi + k];
+        }
+      __syncthreads();
+    }
+    if (!in || pg != 0) continue;
+    const int row = d.row0 + r;
+    const int t = token_of(a, row), head = d.head * a.group + row - t * a.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(d.q0 + t) * a.out_ld + (int64_t)head * D + li * 4;
+    *reinterpret_cast<uint2*>(out) = uint2{pack2<A>(acc[0] * inv, acc[1] * inv), pack2<A>(acc[2] * inv, acc[3] * inv)};
+    if (a.lse && li == 0)
+      a.lse[(int64_t)(d.q0 + t) * a.n_q_heads + head] = sum == 0.f ? -INFINITY : (Mu + log2f(sum)) * kLn2;
+  }
+}
+
 // ---- up to 16 rows ---------------------------------------------------------------
 // K and V go from memory to registers (every byte is used once: LDS would only add
 // a trip).  A wave's tile is 4 E keys: 16 KB at D = 128, its next pieces loaded
@@ -505,7 +591,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const KvView& kv = a.kv;
   Cut c;
   const int workers = SOLO ? 4 * (int)gridDim.x : (int)gridDim.x;
-  cut_work<KU, TR, 256, 1>(a, pre, c, workers, SOLO ? ((int)blockIdx.x >> 3) * 4 + wave : (int)blockIdx.x >> 3);
+  cut_work<KU, TR, 256>(a, pre, c, workers, SOLO ? ((int)blockIdx.x >> 3) * 4 + wave : (int)blockIdx.x >> 3);
   const Parts<TR, D> parts(a.ws, workers);
   PartDesc* desc = parts.desc + (SOLO ? (int)blockIdx.x * 4 + wave : (int)blockIdx.x);
   const bool speaker = SOLO ? lane == 0 : tid == 0;
@@ -895,11 +981,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int col = lane & 31, hi = lane >> 5;
   const KvView& kv = a.kv;
   Cut c;
-  cut_work<KU, TR, NW * 64, 4>(a, sh.pre, c, (int)gridDim.x, (int)blockIdx.x >> 3);
+  cut_work<KU, TR, NW * 64>(a, sh.pre, c, (int)gridDim.x, (int)blockIdx.x >> 3);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
   Piece p;
   int n_piece = 0;
-  if (c.pos >= c.end && tid == 0) describe(parts.desc + blockIdx.x, c, nullptr);
+  auto tell = [&](const Piece* q) {
+    PartDesc* d = parts.desc + blockIdx.x;
+    describe(d, c, q);
+    constexpr int NG = 1024 / D;
+    int n = 0;
+    if (d->last >= 0) {
+      int P = 1;
+      while (P < NG && 8 * P <= d->last - d->first + 1) P *= 2;
+      d->share = P;
+      n = (d->rows * P + NG - 1) / NG;
+    }
+    parts.items[blockIdx.x] = n;
+  };
+  if (c.pos >= c.end && tid == 0) tell(nullptr);
   // row col of a K operand is this token of a tile of 32: a lane's 16 scores are
   // those of tokens hi * 8 .. + 7 and 16 + hi * 8 .. + 7
   const int ktok = (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
@@ -1167,7 +1266,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (hi == 0) parts.ml[at] = float2{m, l};
       }
     }
-    if (n_piece == 0 && tid == 0) describe(parts.desc + blockIdx.x, c, &p);
+    if (n_piece == 0 && tid == 0) tell(&p);
     ++n_piece;
     __syncthreads();  // the slots of this piece have been read
   }
@@ -1175,7 +1274,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 // Rows of a head of the longest sequence choose the kernel for all of a batch.
 inline bool few_rows(int32_t group, int32_t max_q_len) { return (int64_t)max_q_len * group <= 16; }
-inline int blocks_of(int n_cu) { return 2 * n_cu / 8 * 8; }
+inline int blocks_of(int n_cu) { return std::min(2 * n_cu / 8 * 8, 1024); }
 
 // Every wave for itself once there are two (sequence, head) pairs a block.
 inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_seqs * H >= 2 * blocks_of(n_cu); }
@@ -1193,14 +1292,24 @@ hipError_t launch(const AttendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(G, (unsigned)most), dim3(256), 0, s, a, G);
   } else {
     using TT = Tiles<A, KV, D>;
-    const int rows = (int)(most < TT::TR ? most : TT::TR);
     const size_t lds = sizeof(typename TT::Shared);
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (attr != hipSuccess) return attr;
     hipLaunchKernelGGL((k_attend_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a);
-    constexpr int RB = 256 / (D / 4);
-    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)), dim3(256), 0, s, a, G);
+    // tiles of which none has many parts: four blocks each; else the list.  Measured
+    // (us of a call, list / this): 32 sequences of 5 x 8 rows 86.7 / 84.6, 2 of 256 x
+    // 8 rows over 4096 tokens 110 / 104, 64 x 4 rows of 8 heads over 2000 tokens 28.8
+    // / 34.0, 100 x 8 rows of one head over 30000 tokens 43.9 / 118
+    const int64_t tiles = a.kv.H * std::max<int64_t>(a.kv.n_seqs, (int64_t)a.kv.n_tokens * a.group / TT::TR);
+    if (2 * tiles >= G) {
+      constexpr int RB = 256 / (D / 4);
+      const int rows = (int)std::min<int64_t>(most, TT::TR);
+      hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)),
+                         dim3(256), 0, s, a, G);
+    } else {
+      hipLaunchKernelGGL((k_attend_join_list<A, D, TT::TR>), dim3(2 * G), dim3(256), 0, s, a, G);
+    }
   }
   return hipGetLastError();
 }
@@ -1217,7 +1326,7 @@ size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t 
   const bool few = few_rows(group, max_q_len);
   const size_t G = (size_t)blocks_of(n_cu) * (few && solo_waves(n_seqs, H, n_cu) ? 4 : 1);
   const size_t TR = few ? 16 : 128, D = (size_t)ty.D;
-  return G * (sizeof(PartDesc) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
+  return G * (sizeof(PartDesc) + sizeof(int) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
 }
 
 int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len) {
