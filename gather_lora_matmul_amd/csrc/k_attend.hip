@@ -135,6 +135,28 @@ __device__ __forceinline__ uint32_t class_bits(const u32x4& u, int cls) {
   }
   return bits;
 }
+// Byte e of sixteen kept where bit e is set, else zero.
+__device__ __forceinline__ u32x4 keep16b(u32x4 u, uint32_t bits) {
+  auto m = [](uint32_t b) {
+    return ((b & 1) ? 0xffu : 0u) | ((b & 2) ? 0xff00u : 0u) | ((b & 4) ? 0xff0000u : 0u) | ((b & 8) ? 0xff000000u : 0u);
+  };
+  u.x &= m(bits);
+  u.y &= m(bits >> 4);
+  u.z &= m(bits >> 8);
+  u.w &= m(bits >> 12);
+  return u;
+}
+// Not zero if one of sixteen FP8 codes is NaN (all ones but for the sign).
+__device__ __forceinline__ uint32_t nan_codes(const u32x4& u) {
+  constexpr uint32_t kM = 0x7f7f7f7fu, kO = 0x01010101u;
+  return (((u.x & kM) + kO) | ((u.y & kM) + kO) | ((u.z & kM) + kO) | ((u.w & kM) + kO)) & 0x80808080u;
+}
+// Bits of the N tokens from k0 on that lie in [lo, up].
+template <int N>
+__device__ __forceinline__ uint32_t run_bits(int k0, int lo, int up) {
+  const int x = min(max(lo - k0, 0), N), y = min(max(up - k0 + 1, 0), N);
+  return ((1u << y) - 1u) & ~((1u << x) - 1u);
+}
 // Not zero if one of eight values is not finite: adding one to an exponent of all
 // ones carries into the sign's place.
 template <typename T>
@@ -605,7 +627,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int pos = p.q.kv_len - p.q.q_len + tq;
     const int posmin = p.q.kv_len - p.q.q_len + token_of(a, p.row0);
     const int posmax = p.q.kv_len - p.q.q_len + token_of(a, p.row0 + p.rows - 1);
-    const int vislo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int win = a.window > 0 ? a.window : 0x40000000;
     u32x4 qf[S::NQ];
     {
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(p.q.q0 + tq) * a.q_ld +
@@ -682,13 +704,59 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     for (; tile < p.key1; tile += KU) {
       const bool more = tile + KU < p.key1;
+      const bool kbad = (unsigned)id.kp >= (unsigned)kv.n_pages, vbad = (unsigned)id.vp >= (unsigned)kv.n_pages;
+      const bool edge = tile + KT - 1 > posmin || tile <= posmax - win || __ballot(kbad || vbad);
+      uint32_t seen = 0xffffu;   // of the lane's tokens g E + e: seen by the lane's row
+      if (edge) {
+        // group g's K page is known to the lanes with col / 4 == g
+        const unsigned long long kb = __ballot(kbad);
+        const bool gone = vbad || ((kb >> (g * 4)) & 1);
+        const int k0 = tile + g * E;
+        seen = gone ? 0u : run_bits<E>(k0, pos - win + 1, pos);
+        // what no row sees is taken out of V (0 times what lies there need not be 0);
+        // values that are not finite go to the rows that see them, then they leave V
+        const uint32_t live = gone ? 0u : run_bits<E>(k0, posmin - win + 1, min(posmax, p.key1 - 1));
+        uint32_t odd = 0;
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+          vf[n] = Q8 ? keep16b(vf[n], live) : keep8(vf[n], live);
+          odd |= Q8 ? nan_codes(vf[n]) : not_finite<A>(vf[n]);
+        }
+        if (Q8) vscale = keep16b(vscale, live);
+        if (__builtin_expect(__ballot(odd != 0) != 0, 0)) {
+#pragma unroll
+          for (int n = 0; n < ND; ++n)
+#pragma unroll 1
+            for (int q = 0; q < E / 8; ++q) {
+              const u32x4 vis = ones8<PT>(seen >> (8 * q));
+              const u32x4 v = Q8 ? (q ? fp8_to16<PT>(vf[n].z, vf[n].w) : fp8_to16<PT>(vf[n].x, vf[n].y)) : vf[n];
+#pragma unroll 1
+              for (int cls = 0; cls < 3; ++cls) {
+                const f32x4 hit = mfma16<PT>(ones8<PT>(class_bits<PT>(v, cls)), vis, f32x4{0.f, 0.f, 0.f, 0.f});
+                const float val = class_value(cls);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][i] += hit[i] > 0.f ? val : 0.f;
+              }
+            }
+#pragma unroll
+          for (int n = 0; n < ND; ++n) {
+            if constexpr (Q8) {
+              vf[n] = keep16b(vf[n], ~(class_bits<PT>(fp8_to16<PT>(vf[n].x, vf[n].y), 3) |
+                                       class_bits<PT>(fp8_to16<PT>(vf[n].z, vf[n].w), 3) << 8));
+            } else {
+              vf[n] = keep8(vf[n], ~class_bits<A>(vf[n], 3));
+            }
+          }
+        }
+      }
       // ---- S^T = K Q^T
       f32x4 s[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < NT; ++t) s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
           if constexpr (Q8) {
             s[t] = mfma16<A>(fp8_to16<A>(kf[t][n].x, kf[t][n].y), qf[2 * n], s[t]);
             s[t] = mfma16<A>(fp8_to16<A>(kf[t][n].z, kf[t][n].w), qf[2 * n + 1], s[t]);
@@ -696,8 +764,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             s[t] = mfma16<A>(kf[t][n], qf[n], s[t]);
           }
         }
-      }
-      const Ids idc = id;
       if constexpr (Q8) {
         const uint32_t w[4] = {kscale.x, kscale.y, kscale.z, kscale.w};
 #pragma unroll
@@ -705,30 +771,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[t][i] *= __uint_as_float(((w[t] >> (8 * i)) & 0xffu) << 23);
       }
+      // the ids after next are asked for ahead of the V loads: waiting for them
+      // does not wait for those
+      Ids idn2 = idn;
       if (more) {
         load_k(idn);
         load_ks(tile + KU);
+        idn2 = find(tile + 2 * KU);
       }
-      // ---- mask
-      const bool kbad = (unsigned)idc.kp >= (unsigned)kv.n_pages, vbad = (unsigned)idc.vp >= (unsigned)kv.n_pages;
-      const bool edge = tile + KT - 1 > posmin || (a.window > 0 && tile <= posmax - a.window) ||
-                        __ballot(kbad || vbad);
-      uint32_t live = 0xffffu;   // of the lane's tokens g E + e: seen by some row
-      uint32_t seen = 0xffffu;   // ... by the lane's row
       if (edge) {
-        // group g's K page is known to the lanes with col / 4 == g
-        const unsigned long long kb = __ballot(kbad);
-        const bool gone = vbad || ((kb >> (g * 4)) & 1);
-        live = seen = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int key = tile + g * E + e;
-          const bool lv = !gone && key <= posmax && key < p.key1 &&
-                          (a.window <= 0 || key > posmin - a.window);
-          const bool sv = lv && key <= pos && key >= vislo;
-          live |= (uint32_t)lv << e;
-          seen |= (uint32_t)sv << e;
-        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -738,17 +789,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       // ---- running maximum and sum
       float top = s[0][0];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+      for (int t = 0; t < NT; ++t) {
+        top = max3(top, s[t][0], s[t][1]);
+        top = max3(top, s[t][2], s[t][3]);
+      }
+      top = max3(top, __shfl_xor(top, 16), top);
+      top = max3(top, __shfl_xor(top, 32), top);
       top *= a.scale_log2;
       // the maximum follows only when it would grow by more than 8 (a factor of
       // 256, which every type of P holds): else no rescaling
       if (__ballot(top > m + 8.f)) {
-        const float mn = fmaxf(m, top);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float mn = top > m ? top : m;
+        const float f = m == -INFINITY ? 1.f : exp2f(m - mn);   // (nothing yet, or what is not finite)
         l *= f;
 #pragma unroll
         for (int n = 0; n < ND; ++n) o[n] *= f;
@@ -764,55 +816,29 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if constexpr (Q8) {
         const uint32_t w[4] = {vscale.x, vscale.y, vscale.z, vscale.w};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          pr[e] *= __uint_as_float(((w[e / 4] >> (8 * (e & 3))) & 0xffu) << 23);
-          if (edge && !((seen >> e) & 1)) pr[e] = 0.f;
-        }
+        for (int e = 0; e < 16; ++e) pr[e] *= __uint_as_float(((w[e / 4] >> (8 * (e & 3))) & 0xffu) << 23);
       }
       u32x4 pf[E / 8], pl[E / 8];
 #pragma unroll
       for (int q = 0; q < E / 8; ++q) p_operand<PT, true>(pr + 8 * q, pf[q], pl[q]);
       // ---- O^T += V^T P^T
-      if (!edge) {
 #pragma unroll
-        for (int n = 0; n < ND; ++n) {
-          if constexpr (Q8) {
-            const u32x4 v0 = fp8_to16<PT>(vf[n].x, vf[n].y), v1 = fp8_to16<PT>(vf[n].z, vf[n].w);
-            o[n] = mfma16<PT>(v0, pf[0], o[n]);
-            o[n] = mfma16<PT>(v1, pf[E / 8 - 1], o[n]);
-            o[n] = mfma16<PT>(v0, pl[0], o[n]);
-            o[n] = mfma16<PT>(v1, pl[E / 8 - 1], o[n]);
-          } else {
-            o[n] = mfma16<PT>(vf[n], pf[0], o[n]);
-            o[n] = mfma16<PT>(vf[n], pl[0], o[n]);
-          }
+      for (int n = 0; n < ND; ++n) {
+        if constexpr (Q8) {
+          const u32x4 v0 = fp8_to16<PT>(vf[n].x, vf[n].y), v1 = fp8_to16<PT>(vf[n].z, vf[n].w);
+          o[n] = mfma16<PT>(v0, pf[0], o[n]);
+          o[n] = mfma16<PT>(v1, pf[E / 8 - 1], o[n]);
+          o[n] = mfma16<PT>(v0, pl[0], o[n]);
+          o[n] = mfma16<PT>(v1, pl[E / 8 - 1], o[n]);
+        } else {
+          o[n] = mfma16<PT>(vf[n], pf[0], o[n]);
+          o[n] = mfma16<PT>(vf[n], pl[0], o[n]);
         }
-      } else {
-#pragma unroll
-        for (int n = 0; n < ND; ++n)
-#pragma unroll
-          for (int q = 0; q < E / 8; ++q) {
-            u32x4 v = vf[n];
-            if constexpr (Q8) v = q ? fp8_to16<PT>(vf[n].z, vf[n].w) : fp8_to16<PT>(vf[n].x, vf[n].y);
-            v = keep8(v, live >> (8 * q));
-            const uint32_t odd = class_bits<PT>(v, 3);
-            if (__ballot(odd != 0)) {
-              const u32x4 vis = ones8<PT>(seen >> (8 * q));
-              for (int cls = 0; cls < 3; ++cls) {
-                const f32x4 hit = mfma16<PT>(ones8<PT>(class_bits<PT>(v, cls)), vis, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][i] += hit[i] > 0.f ? class_value(cls) : 0.f;
-              }
-              v = keep8(v, ~odd);
-            }
-            o[n] = mfma16<PT>(v, pf[q], o[n]);
-            o[n] = mfma16<PT>(v, pl[q], o[n]);
-          }
       }
       if (more) {
         load_v(idn);
         id = idn;
-        idn = find(tile + 2 * KU);
+        idn = idn2;
       }
     }
     l += __shfl_xor(l, 16);
@@ -1089,11 +1115,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int i = 0; i < ND; ++i) o[i] = f32x16{};
     float m = -INFINITY, l = 0.f;
-    // bits of the tokens k0 .. k0 + 7 of the tile that lie in [lo, up]
-    auto run_bits = [](int k0, int lo, int up) {
-      const int x = min(max(lo - k0, 0), 8), y = min(max(up - k0 + 1, 0), 8);
-      return ((1u << y) - 1u) & ~((1u << x) - 1u);
-    };
     load_ids(p.key0);
     issue(p.key0, 0);
     commit(0);
@@ -1141,7 +1162,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
-              const u32x4 vis = ones8<A>(run_bits(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
+              const u32x4 vis = ones8<A>(run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
 #pragma unroll
               for (int n = 0; n < ND; ++n) {
                 const u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
@@ -1185,7 +1206,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
-            const uint32_t seen = run_bits(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
+            const uint32_t seen = run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
 #pragma unroll
             for (int r = 0; r < 8; ++r)
               if (!((seen >> r) & 1)) s[h >> 1][8 * (h & 1) + r] = -INFINITY;
