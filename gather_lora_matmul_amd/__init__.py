@@ -695,7 +695,7 @@ def _kv_rows(cache: KvCache, batch: KvBatch, t, what: str, heads: Optional[int] 
         raise ValueError("expected a device tensor")
     if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d.head_dim):
         raise ValueError("%s: a token's heads must be contiguous" % what)
-    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), t.shape[1] * d.head_dim)
+    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else t.shape[1] * d.head_dim
 
 
 def _kv_copy_args(cache: KvCache, batch: KvBatch, k, v):
@@ -874,7 +874,8 @@ def prepare_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tok
         _check_tensor(t, what, None, need)
     _check_tensor(u_accept, "u_accept", 0, n_drafts)
     _check_tensor(u_sample, "u_sample", 0, n_seqs)
-    ld = [max(int(t.stride(0)), vocab) if t is not None else 0 for t in (target, draft)]
+    # the distance of the rows; one row (or none) has no stride of its own
+    ld = [0 if t is None else int(t.stride(0)) if t.shape[0] > 1 else vocab for t in (target, draft)]
     d = VerifyDesc(n_seqs, n_tokens, n_drafts, vocab, code[target.dtype], 0, ld[0], ld[1], _dev_ptr(q_start),
                    _dev_ptr(drafted), target.data_ptr(),
                    draft.data_ptr() if draft is not None and n_drafts else None, _dev_ptr(u_accept),

@@ -41,12 +41,7 @@ lora_status geometry(const lora_pool* p, const lora_kv_desc* d, KvTypes& ty, int
   return LORA_OK;
 }
 
-lora_status view_of(const lora_pool* p, const lora_kv_desc* d, const lora_kv_batch* b, KvTypes& ty,
-                    KvView& v) {
-  int32_t T = 0;
-  const lora_status st = geometry(p, d, ty, T);
-  if (st) return st;
-  if (p->host_only) return fail(LORA_E_STATE, "host-only pool cannot run kernels");
+lora_status batch_sizes(const lora_kv_batch* b, int32_t T) {
   if (!b) return fail(LORA_E_ARG, "null batch");
   if (b->n_seqs < 0 || b->n_seqs > kKvMaxSeqs)
     return fail(LORA_E_ARG, "n_seqs %d not in [0, %d]", b->n_seqs, kKvMaxSeqs);
@@ -56,6 +51,16 @@ lora_status view_of(const lora_pool* p, const lora_kv_desc* d, const lora_kv_bat
     return fail(LORA_E_ARG, "max_q_len %d not in [0, n_tokens]", b->max_q_len);
   if (b->max_blocks < 1 || (int64_t)b->max_blocks * T > (1 << 28))
     return fail(LORA_E_ARG, "max_blocks %d (a sequence holds 1 block to 2^28 tokens)", b->max_blocks);
+  return LORA_OK;
+}
+
+lora_status view_of(const lora_pool* p, const lora_kv_desc* d, const lora_kv_batch* b, KvTypes& ty,
+                    KvView& v) {
+  int32_t T = 0;
+  lora_status st = geometry(p, d, ty, T);
+  if (st) return st;
+  st = batch_sizes(b, T);
+  if (st) return st;
   if (b->n_seqs > 0 && (!b->q_start_dev || !b->kv_len_dev || !b->table_dev))
     return fail(LORA_E_ARG, "null batch pointer");
   if (((uintptr_t)b->q_start_dev | (uintptr_t)b->kv_len_dev | (uintptr_t)b->table_dev) & 3u)
@@ -75,6 +80,12 @@ lora_status view_of(const lora_pool* p, const lora_kv_desc* d, const lora_kv_bat
   v.q_start = b->q_start_dev;
   v.kv_len = b->kv_len_dev;
   v.table = b->table_dev;
+  return LORA_OK;
+}
+
+// Asked last, so that a host-only pool reports a wrong argument first.
+lora_status runnable(const lora_pool* p) {
+  if (p->host_only) return fail(LORA_E_STATE, "host-only pool cannot run kernels");
   return LORA_OK;
 }
 
@@ -120,6 +131,7 @@ static lora_status kv_copy(const lora_pool* p, const lora_kv_desc* d, const lora
   const int E = 16 / elt_bytes(ty.kv);
   if (((int64_t)b->n_tokens / E + 2 * (int64_t)b->n_seqs) * d->n_kv_heads > INT32_MAX - 8)
     return fail(LORA_E_UNSUPPORTED, "more than 2^31 token groups");
+  LORA_TRY(runnable(p));
   if (write)
     return hip_status(launch_kv_write(ty, view, k, v, ld, (hipStream_t)stream), "kv_write");
   return hip_status(launch_kv_read(ty, view, const_cast<void*>(k), const_cast<void*>(v), ld,
@@ -153,7 +165,8 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* p, const lora_kv_desc
   KvTypes ty;
   int32_t T = 0;
   LORA_TRY(geometry(p, d, ty, T));
-  if (!b || !bytes) return fail(LORA_E_ARG, "null batch or size");
+  LORA_TRY(batch_sizes(b, T));
+  if (!bytes) return fail(LORA_E_ARG, "null size");
   LORA_TRY(check_heads(d, n_q_heads, b));
   *bytes = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len, b->n_seqs,
                             d->n_kv_heads);
@@ -169,7 +182,8 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   AttendArgs a;
   LORA_TRY(view_of(p, d, b, ty, a.kv));
   LORA_TRY(check_heads(d, n_q_heads, b));
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(LORA_E_ARG, "scale must be positive and finite");
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return fail(LORA_E_ARG, "scale must be positive and finite");
   if (window < 0) return fail(LORA_E_ARG, "negative window");
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_q_len == 0) return LORA_OK;
   if (attend_units(a.kv, n_q_heads / d->n_kv_heads, b->max_q_len) > INT32_MAX)
@@ -184,6 +198,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
     return fail(LORA_E_ARG, "workspace of %zu bytes, this call needs %zu (lora_kv_attend_workspace_size)",
                 ws_bytes, need);
   if ((uintptr_t)workspace_dev & 255u) return fail(LORA_E_ARG, "workspace not 256-byte aligned");
+  LORA_TRY(runnable(p));
   a.q = q_dev;
   a.q_ld = q_ld;
   a.out = out_dev;

@@ -198,3 +198,18 @@ def test_graph_replays():
         torch.cuda.synchronize()
         want = oracle(k, drafted.cpu().numpy(), t.cpu().numpy(), d.cpu().numpy(), u.cpu().numpy(), us.cpu().numpy())
         assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(n_out.cpu().numpy(), want[1])
+
+
+def test_rows_that_share_memory_are_refused():
+    # rows expanded from one would have no stride: the call must not read past them
+    vocab, dev = 40, "cuda"
+    i32 = dict(dtype=torch.int32, device=dev)
+    row = torch.full((1, vocab), 1 / vocab, device=dev)
+    ws = torch.empty(L.lora_spec_verify_workspace_size(2, vocab), dtype=torch.uint8, device=dev)
+    args = lambda target, draft: (torch.tensor([0, 2, 4], **i32), torch.zeros(2, **i32), target, draft,
+                                  torch.zeros(2, device=dev), torch.zeros(2, device=dev),
+                                  torch.empty(4, **i32), torch.empty(2, **i32), ws)
+    with pytest.raises(L.LoraError, match="target_ld"):
+        L.lora_spec_verify(*args(row.expand(4, vocab), None))
+    with pytest.raises(L.LoraError, match="draft_ld"):
+        L.lora_spec_verify(*args(row.repeat(4, 1), row.expand(2, vocab)))
