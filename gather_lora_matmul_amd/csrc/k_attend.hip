@@ -228,7 +228,8 @@ __device__ __forceinline__ int wave_add(int x) {
   return x;
 }
 
-// All units of a call are fewer than 2^31 (attend_units, checked on the host).
+// All units of a call are fewer than 2^31 (attend_units, checked on the host), if its
+// q_start ascend; a call whose units are more all the same does nothing.
 struct Cut {               // ("block": the worker, which may be a wave)
   int pos, end;          // this block's range of units
   int each, over;        // block L's range begins at L each + min(L, over)
@@ -262,7 +263,8 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int W = THREADS / 64, FEW = 2;
   int* wsum = pre + kKvMaxSeqs + 1;
-  int run = 0;
+  uint32_t run = 0;
+  bool past = false;            // too many units
   const bool small = n <= 64;   // every wave for itself
   int longest = 0;              // units of the longest tile, if no window is set
   for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
@@ -283,10 +285,10 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
       part = wave_add(part);
       if (lane == src) units += part;
     }
-    int sum = units * a.kv.H;
+    uint32_t sum = (uint32_t)(units * a.kv.H);   // (of one sequence: below 2^31)
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int z = __shfl_up(sum, d);
+      const uint32_t z = __shfl_up(sum, d);
       if (lane >= d) sum += z;
     }
     if (preT && small) {
@@ -302,26 +304,29 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
       if (lane == 0) preT[0] = 0;
     }
     if (!small) {
-      if (lane == 63) wsum[wave] = sum;
+      if (lane == 63) wsum[wave] = (int)sum;
       __syncthreads();
-      int before = run, all = 0;
+      uint32_t before = run, all = 0;
       for (int w = 0; w < W; ++w) {
-        if (w < wave) before += wsum[w];
-        all += wsum[w];
+        if (w < wave) before += (uint32_t)wsum[w];
+        all += (uint32_t)wsum[w];
       }
-      if (s < n) pre[s + 1] = before + sum;
+      sum += before;
+      if (s < n) pre[s + 1] = (int)sum;
       run += all;
       __syncthreads();
     } else if (s < n) {
-      pre[s + 1] = sum;   // the same from every wave
+      pre[s + 1] = (int)sum;   // the same from every wave
     }
+    // the first prefix sum past 2^31 is below 2^32: its bit 31 shows
+    past |= s < n && (int)sum < 0;
   }
   if (small ? lane == 0 : tid == 0) pre[0] = 0;
-  if (!small) __syncthreads();
-  const int all_units = uni(pre[n]);
+  past = small ? __ballot(past) != 0 : __syncthreads_or(past) != 0;
+  const int all_units = past ? 0 : uni(pre[n]);
   c.unit0 = c.tile = c.tiles = 0;
   c.step = workers;
-  if (preT && small && n > 0) {
+  if (preT && small && all_units > 0) {
     const int T = uni(preT[n]), whole = T / workers * workers;
     // (8 T longest <= 9 units: the longest tile at most an eighth over the average)
     if (whole > 0 && (int64_t)T * uni(longest) * 8 <= (int64_t)all_units * 9) {

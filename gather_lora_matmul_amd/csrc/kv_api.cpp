@@ -209,7 +209,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   div_init(a.group < 2 ? 2 : a.group, a.group_m, a.group_s);
   a.max_q_len = b->max_q_len;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
+  a.window = window > (1 << 28) ? 0 : window;   // no position is farther back; keeps differences in 32 bits
   a.ws = (char*)workspace_dev;
   a.n_cu = p->n_cu;
   return hip_status(launch_attend(ty, a, (hipStream_t)stream), "kv_attend");

@@ -590,3 +590,36 @@ def test_fp8_pool_holds_a_cache():
             c.fill()
             q = torch.randn((c.n, 2, 128), device="cuda", generator=c.gen).to(TD["f16"])
             check(c, q, 0.1)
+
+
+@pytest.mark.parametrize("q_len", [[1, 4], [20, 90]])
+def test_attend_widest_window(q_len):
+    # a window of 2^31 - 1 reaches as far back as none, also from positions before 0
+    with Case("bf16", "bf16", 8192, 1, 128, q_len, [3, 50], seed=23) as c:
+        c.fill()
+        q = torch.randn((c.n, 2, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        want, lse = check(c, q, 0.1)
+        for w in (2 ** 31 - 1, 2 ** 28, 2 ** 28 + 1):
+            out, ls = attend(c, q, 0.1, window=w)
+            assert torch.equal(out, want) and torch.equal(ls, lse)
+
+
+@pytest.mark.parametrize("n_seqs,n,length", [(1024, 32768, 1 << 18), (60, 1 << 19, 1 << 18), (60, 1 << 18, 1 << 20)])
+def test_attend_of_overlapping_rows_does_nothing_when_they_are_too_many(n_seqs, n, length):
+    # every other sequence claims all the rows: more units (a tile of 128 rows with 64
+    # keys) than 2^31, which no ascending q_start of a call that is not refused can
+    # have; if they are fewer (the second case), the rows see absent pages
+    last = length - n + np.minimum(np.arange(128 // 8 - 1, n, 128 // 8), n - 1)   # position of each tile's last row
+    units = (n_seqs // 2) * int(np.maximum(1, -(-(last + 1) // 64)).sum())
+    with Case("f16", "f16", 4096, 1, 128, [1], [1], seed=24) as c:
+        nb = length // c.T
+        i32 = dict(dtype=torch.int32, device="cuda")
+        b = L.KvBatch(torch.tensor([0, n], **i32).repeat(n_seqs // 2 + 1)[:n_seqs + 1],
+                      torch.full((n_seqs,), length, **i32), torch.full((n_seqs, 2, 1, nb), -1, **i32), n, n)
+        q = torch.zeros((n, 8, 128), dtype=torch.float16, device="cuda")
+        out, lse = attend(c, q, 0.1, batch=b)
+        torch.cuda.synchronize()
+        if units >= 1 << 31:
+            assert torch.all(out == 5) and torch.all(lse == 5)
+        else:
+            assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
