@@ -984,19 +984,27 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---- more rows -------------------------------------------------------------------
-// Tiles of 128 rows: four waves of 32, which share tiles of 64 keys through LDS
-// (two slots, one barrier a tile).  The LDS image is the 16-bit pages' own order,
-// [piece][token] and [token group][element] of 16 bytes, so that operand reads are
-// contiguous over lanes and free of bank conflicts; 16-bit pages are loaded there
+// Tiles of 128 or 256 rows: four or eight waves of 32, which share tiles of 64 keys
+// through LDS (two slots, one barrier a tile).  The LDS image is the 16-bit pages' own
+// order, [piece][token] and [token group][element] of 16 bytes, so that operand reads
+// are contiguous over lanes and free of bank conflicts; 16-bit pages are loaded there
 // directly, FP8 ones through registers, where the codes get their scales (2 scales
 // a pair of V codes, one a K row: the products and the softmax then know nothing
 // of FP8).
 //
-// The matrix cores and the vector ALUs are about equally long busy with a tile (2 x
-// 512 cycles for the products of 32 rows with 64 keys of 128 elements, 32
-// exponentials of 16 cycles and about 100 other instructions a lane), so only what
-// overlaps is fast: two blocks share a CU, whose waves drift apart because no
-// barrier ties them.
+// Of 64 keys of 128 elements a wave's 32 rows cost 1024 cycles of the matrix cores and
+// about 1130 of the vector ALUs (32 exponentials of 16 cycles, about 150 other
+// instructions a lane): only what overlaps is fast.  Two waves share a SIMD.
+//   Four waves (short work): two blocks share a CU, drifting apart because no barrier
+// ties them; a tile's products and its exponentials overlap within the second product
+// only.  A pair of wave tiles takes 5050 cycles (2048 over 16384 tokens, 64 heads on 8,
+// bf16: 1091 us, 945 TFLOP/s).
+//   Eight waves (long work): a step weaves the exponentials of one tile with its second
+// product and the first product of the next tile, and spreads the loads among them
+// (4390 cycles, 949 us, 1086 TFLOP/s: a matrix product of 8192^3 runs at 1236).  The
+// loads to LDS arrive at 53 bytes a cycle and CU, and issuing a tile's at once stops a
+// wave for 600 to 1300 cycles; 256 rows halve them a row.  Weaving alone (four waves:
+// 1055 us) and more rows alone (1079) give less, and both cost the short calls.
 __device__ __forceinline__ void load_lds16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -1046,9 +1054,40 @@ __device__ __forceinline__ u32x4 fp8_to16v(uint32_t w0, uint32_t w1, uint32_t s0
   return u32x4{o[0], o[1], o[2], o[3]};
 }
 
-template <typename A, typename KV, int D>
+// The order of the products of a step beside its 32 exponentials: op below 64 is
+// product n = op / 2 of half op % 2 of the next scores, else 64 + q ND + n block n of
+// the output with the 16 tokens of step q, whose P is complete after exponential
+// 8 q + 7.  at: the exponential before which it goes.
+template <int NQ, int ND>
+struct Weave {
+  static constexpr int n = 2 * NQ + 4 * ND, ring = 4;
+  struct Table {
+    int op[n], at[n];
+  };
+  static constexpr Table make() {
+    Table t{};
+    constexpr int share[4] = {3, 2, 2, 1};
+    int j = 0, k = 0;
+    for (int q = 0; q < 4; ++q) {
+      const int ks = share[q] * NQ / 4, vs = q ? ND : 0, all = ks + vs;
+      for (int i = 0, ki = 0, vi = 0; i < all; ++i, ++j) {
+        const bool key = vi == vs || (ki < ks && ki * vs <= vi * ks);
+        if (key) ++ki, t.op[j] = k++;
+        else t.op[j] = 64 + (q - 1) * ND + vi++;
+        t.at[j] = 8 * q + i * 8 / all;
+      }
+    }
+    for (int i = 0; i < ND; ++i, ++j) t.op[j] = 64 + 3 * ND + i, t.at[j] = 32;
+    return t;
+  }
+  static constexpr Table table = make();
+  static constexpr const int (&op)[n] = table.op;
+  static constexpr const int (&at)[n] = table.at;
+};
+
+template <typename A, typename KV, int D, int NW>
 struct Tiles {
-  static constexpr int NW = 4, TR = 32 * NW, KU = 64, NS = 2;
+  static constexpr int TR = 32 * NW, KU = 64, NS = 2;
   static constexpr int NIDS = 512;   // blocks of the page-id window in LDS
   struct Shared {
     u32x4 k[NS][D / 8][KU];
@@ -1059,11 +1098,11 @@ struct Tiles {
   };
 };
 
-template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_tiles(AttendArgs a) {
-  using TT = Tiles<A, KV, D>;
+template <typename A, typename KV, int D, int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_tiles(AttendArgs a) {
+  using TT = Tiles<A, KV, D, NW>;
   constexpr bool Q8 = is_quant<KV>();
-  constexpr int NW = TT::NW, TR = TT::TR, KU = TT::KU, NIDS = TT::NIDS;
+  constexpr int TR = TT::TR, KU = TT::KU, NIDS = TT::NIDS;
   constexpr int E = ET<KV>::E;
   constexpr int ND = D / 32, NQ = D / 16;
   constexpr int KL = D / E;                 // wave loads of K (and of V) of a tile
@@ -1143,39 +1182,56 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // ---- loads of one tile; lane = token for the page lookups
     u32x4 stk[Q8 ? LPW : 1], stv[Q8 ? LPW : 1], vsc[Q8 ? LPW : 1];
     float ksc = 0.f;
-    auto issue = [&](int tile, int slot) {
-      const int t = tile + lane, b = (int)kv_div(kv, (uint32_t)t), sl_ = t - b * kv.T;
-      int kp = sh.ids[0][b - b0], vp = sh.ids[1][b - b0];
-      kp = (unsigned)kp < (unsigned)kv.n_pages ? kp : 0;
-      vp = (unsigned)vp < (unsigned)kv.n_pages ? vp : 0;
-      const char* kb = kv.pages + (int64_t)kp * kv.page_bytes + (wave * kv.T + sl_) * 16;
-#pragma unroll
-      for (int i = 0; i < LPW; ++i) {
-        const char* src = kb + i * NW * kv.T * 16;
-        if constexpr (!Q8) load_lds16(src, &sh.k[slot][wave + NW * i][0]);
-        else stk[i] = ldv(src);
-      }
-      if constexpr (Q8) ksc = scale_of(kv.scales[(int64_t)kp * kv.T + sl_], DOWN);
-#pragma unroll
-      for (int i = 0; i < LPW; ++i) {
-        const int j = wave * LPW + i, gr = j * 64 / D, d0 = j * 64 % D;
-        const int pg = __builtin_amdgcn_readlane(vp, gr * E), s0 = __builtin_amdgcn_readlane(sl_, gr * E);
-        const char* src = kv.pages + (int64_t)pg * kv.page_bytes + ((s0 / E) * D + d0 + lane) * 16;
-        if constexpr (!Q8) {
-          load_lds16(src, &sh.v[slot][gr][d0]);
-        } else {
-          stv[i] = ldv(src);
-          vsc[i] = ldv(kv.scales + (int64_t)pg * kv.T + s0);
-        }
+    // where a lane's token of K and V lies: page and slot of it
+    int kpg = 0, kst = 0, vpg = 0, vst = 0;
+    auto find = [&](int which, int tile, int& page, int& slot_of) {
+      const int t = tile + lane, b = (int)kv_div(kv, (uint32_t)t);
+      slot_of = t - b * kv.T;
+      const int id = sh.ids[which][min(b - b0, NIDS - 1)];
+      page = (unsigned)id < (unsigned)kv.n_pages ? id : 0;
+    };
+    auto load_k = [&](int i, int slot) {
+      const char* src = kv.pages + (int64_t)kpg * kv.page_bytes + ((wave + i * NW) * kv.T + kst) * 16;
+      if constexpr (!Q8) load_lds16(src, &sh.k[slot][wave + NW * i][0]);
+      else stk[i] = ldv(src);
+      if constexpr (Q8)
+        if (i == 0) ksc = scale_of(kv.scales[(int64_t)kpg * kv.T + kst], DOWN);
+    };
+    auto load_v = [&](int i, int slot) {
+      const int j = wave * LPW + i, gr = j * 64 / D, d0 = j * 64 % D;
+      const int pg = __builtin_amdgcn_readlane(vpg, gr * E), s0 = __builtin_amdgcn_readlane(vst, gr * E);
+      const char* src = kv.pages + (int64_t)pg * kv.page_bytes + ((s0 / E) * D + d0 + lane) * 16;
+      if constexpr (!Q8) {
+        load_lds16(src, &sh.v[slot][gr][d0]);
+      } else {
+        stv[i] = ldv(src);
+        vsc[i] = ldv(kv.scales + (int64_t)pg * kv.T + s0);
       }
     };
-    auto commit = [&](int slot) {   // FP8: what was loaded goes to LDS
+    auto issue_k = [&](int tile, int slot) {
+      find(0, tile, kpg, kst);
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) load_k(i, slot);
+    };
+    auto issue_v = [&](int tile, int slot) {
+      find(1, tile, vpg, vst);
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) load_v(i, slot);
+    };
+    auto commit_k = [&](int slot) {   // FP8: what was loaded goes to LDS
       if constexpr (Q8) {
 #pragma unroll
         for (int i = 0; i < LPW; ++i) {
           const int ch = wave + NW * i;
           sh.k[slot][2 * ch][lane] = fp8_to16s<A>(stk[i].x, stk[i].y, ksc);
           sh.k[slot][2 * ch + 1][lane] = fp8_to16s<A>(stk[i].z, stk[i].w, ksc);
+        }
+      }
+    };
+    auto commit_v = [&](int slot) {
+      if constexpr (Q8) {
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) {
           const int j = wave * LPW + i, gr = j * 64 / D, d = j * 64 % D + lane;
           sh.v[slot][2 * gr][d] = fp8_to16v<A>(stv[i].x, stv[i].y, vsc[i].x, vsc[i].y, DOWN);
           sh.v[slot][2 * gr + 1][d] = fp8_to16v<A>(stv[i].z, stv[i].w, vsc[i].z, vsc[i].w, DOWN);
@@ -1187,145 +1243,269 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int i = 0; i < ND; ++i) o[i] = f32x16{};
     float m = -INFINITY, l = 0.f;
     load_ids(p.key0);
-    issue(p.key0, 0);
-    commit(0);
-    int slot = 0;
+    issue_k(p.key0, 0);
+    issue_v(p.key0, 0);
+    commit_k(0);
+    commit_v(0);
     // tiles from clean0 to before clean1 are seen whole by all rows of the block, if their pages are there
     const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
-    for (int tile = p.key0; tile < p.key1; tile += KU, slot ^= 1) {
-      const bool more = tile + KU < p.key1;
-      // this tile's loads have arrived, of every wave (a barrier alone does not wait
-      // for loads that go to LDS), and the last tile is read
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (more) {
-        if ((int)kv_div(kv, (uint32_t)(tile + 2 * KU - 1)) - b0 >= NIDS) load_ids(tile);
-        issue(tile + KU, slot ^ 1);
-      }
-      const bool edge = tile < clean0 || tile >= clean1 || any_bad;
+    auto is_edge = [&](int tile) { return tile < clean0 || tile >= clean1 || any_bad; };
+    auto sees = [&](int tile) {   // this wave's rows see something of it
+      return wrows > 0 && tile <= posmax && tile + KU - 1 > posmin - win;
+    };
+    // An edge tile's V before the products: tokens that no row of the block sees are
+    // taken out in LDS (0 times what lies there need not be 0), and what is not finite
+    // goes to the rows that see it.  Returns the tokens without pages.
+    auto clean = [&](int tile, int slot) {
       unsigned long long bad = 0;
-      if (edge) {
-        // tokens that no row of the block sees are taken out of V in LDS (0 times what
-        // lies there need not be 0), and what is not finite is looked for
-        if (__builtin_expect(any_bad, 0)) {
-          const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
-          bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
-                         (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+      if (__builtin_expect(any_bad, 0)) {
+        const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
+        bad = __ballot((unsigned)sh.ids[0][b] >= (unsigned)kv.n_pages ||
+                       (unsigned)sh.ids[1][b] >= (unsigned)kv.n_pages);
+      }
+      const int first = max(bmin - win + 1 - tile, 0), last = min(bmax - tile, KU - 1);   // seen tokens
+      unsigned long long alive = last >= first ? (~0ull >> (63 - last + first)) << first : 0;
+      alive &= ~bad;
+      u32x4* vt = &sh.v[slot][0][0];
+      uint32_t odd = 0;
+#pragma unroll 1
+      for (int i = tid; i < KU / 8 * D; i += NW * 64) {
+        const uint32_t byte = (uint32_t)(alive >> (i / D * 8)) & 0xffu;
+        u32x4 v = vt[i];
+        if (byte != 0xffu) {
+          v = keep8(v, byte);
+          vt[i] = v;
         }
-        const int first = max(bmin - win + 1 - tile, 0), last = min(bmax - tile, KU - 1);   // seen tokens
-        unsigned long long alive = last >= first ? (~0ull >> (63 - last + first)) << first : 0;
-        alive &= ~bad;
-        u32x4* vt = &sh.v[slot][0][0];
-        uint32_t odd = 0;
+        odd |= not_finite<A>(v);
+      }
+      if (__builtin_expect(__syncthreads_or(odd != 0), 0)) {
+        // their values go to the rows that see their tokens, then they leave V
+        if (wrows > 0)
 #pragma unroll 1
-        for (int i = tid; i < KU / 8 * D; i += 256) {
-          const uint32_t byte = (uint32_t)(alive >> (i / D * 8)) & 0xffu;
-          u32x4 v = vt[i];
-          if (byte != 0xffu) {
-            v = keep8(v, byte);
-            vt[i] = v;
-          }
-          odd |= not_finite<A>(v);
-        }
-        if (__builtin_expect(__syncthreads_or(odd != 0), 0)) {
-          // their values go to the rows that see their tokens, then they leave V
-          if (wrows > 0)
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
-              const u32x4 vis = ones8<A>(run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
+          for (int q = 0; q < 4; ++q) {
+            const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
+            const u32x4 vis = ones8<A>(run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
 #pragma unroll
-              for (int n = 0; n < ND; ++n) {
-                const u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
+            for (int n = 0; n < ND; ++n) {
+              const u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
 #pragma unroll 1
-                for (int cls = 0; cls < 3; ++cls) {
-                  const f32x16 hit = mfma32<A>(ones8<A>(class_bits<A>(v, cls)), vis, f32x16{});
-                  const float val = class_value(cls);
+              for (int cls = 0; cls < 3; ++cls) {
+                const f32x16 hit = mfma32<A>(ones8<A>(class_bits<A>(v, cls)), vis, f32x16{});
+                const float val = class_value(cls);
 #pragma unroll
-                  for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? val : 0.f;
-                }
+                for (int r = 0; r < 16; ++r) o[n][r] += hit[r] > 0.f ? val : 0.f;
               }
             }
-          __syncthreads();
-#pragma unroll 1
-          for (int i = tid; i < KU / 8 * D; i += 256) vt[i] = keep8(vt[i], ~class_bits<A>(vt[i], 3));
-          __syncthreads();
-        }
-      }
-      if (wrows > 0 && tile <= posmax && tile + KU - 1 > posmin - win) {
-        // ---- S^T = K Q^T
-        // in groups of four products, whose operands were read a group ahead (the
-        // scheduler, left alone, reads each just before its use)
-        f32x16 s[2] = {f32x16{}, f32x16{}};
-        const u32x4* kp = &sh.k[slot][hi][ktok];   // piece 2 n of half kt: kp[2 * n * KU + kt * 32]
-        u32x4 kf[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kf[0][i] = kp[2 * (i >> 1) * KU + (i & 1) * 32];
-#pragma unroll
-        for (int g = 0; g < NQ / 2; ++g) {
-          if (g + 1 < NQ / 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kf[(g + 1) & 1][i] = kp[2 * (2 * g + 2 + (i >> 1)) * KU + (i & 1) * 32];
           }
-          __builtin_amdgcn_sched_barrier(0x6);
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < KU / 8 * D; i += NW * 64) vt[i] = keep8(vt[i], ~class_bits<A>(vt[i], 3));
+        __syncthreads();
+      }
+      return bad;
+    };
+    auto mask = [&](f32x16(&s)[2], int tile, unsigned long long bad) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i & 1] = mfma32<A>(kf[g & 1][i], qf[2 * g + (i >> 1)], s[i & 1]);
-          __builtin_amdgcn_sched_barrier(0x6);
+      for (int h = 0; h < 4; ++h) {
+        const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
+        const uint32_t seen = run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (!((seen >> r) & 1)) s[h >> 1][8 * (h & 1) + r] = -INFINITY;
+      }
+    };
+    auto top_of = [](const f32x16(&x)[2]) {
+      float t = x[0][0];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) t = max3(t, x[0][r], x[1][r]);
+      return t;
+    };
+    // The running maximum follows the lane's largest score (and its partner's, which
+    // has the row's other keys); returns what the exponentials subtract.
+    auto follow = [&](float top) {
+      const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      top = __builtin_elementwise_maximum(__uint_as_float(both[0]), __uint_as_float(both[1])) * sl;
+      if (__ballot(top > m + 8.f)) {
+        const float mn = top > m ? top : m;
+        const float f = m == -INFINITY ? 1.f : exp2f(m - mn);   // (nothing yet, or what is not finite)
+        l *= f;
+#pragma unroll
+        for (int n = 0; n < ND; ++n) o[n] *= f;
+        m = mn;
+      }
+      return safe_max(m);
+    };
+    // the loads have arrived, of every wave (a barrier alone does not wait for loads
+    // that go to LDS), and what the next ones will overwrite is read
+    auto arrived = [&] {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
+    };
+    if constexpr (NW == 4) {
+      int slot = 0;
+      for (int tile = p.key0; tile < p.key1; tile += KU, slot ^= 1) {
+        const bool more = tile + KU < p.key1;
+        arrived();
+        if (more) {
+          if ((int)kv_div(kv, (uint32_t)(tile + 2 * KU - 1)) - b0 >= NIDS) load_ids(tile);
+          issue_k(tile + KU, slot ^ 1);
+          issue_v(tile + KU, slot ^ 1);
         }
-        // ---- mask
-        if (edge) {
+        const bool edge = is_edge(tile);
+        unsigned long long bad = 0;
+        if (edge) bad = clean(tile, slot);
+        if (sees(tile)) {
+          // ---- S^T = K Q^T
+          // in groups of four products, whose operands were read a group ahead (the
+          // scheduler, left alone, reads each just before its use)
+          f32x16 s[2] = {f32x16{}, f32x16{}};
+          const u32x4* kp = &sh.k[slot][hi][ktok];   // piece 2 n of half kt: kp[2 * n * KU + kt * 32]
+          u32x4 kf[2][4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
-            const uint32_t seen = run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
+          for (int i = 0; i < 4; ++i) kf[0][i] = kp[2 * (i >> 1) * KU + (i & 1) * 32];
+#pragma unroll
+          for (int g = 0; g < NQ / 2; ++g) {
+            if (g + 1 < NQ / 2) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) kf[(g + 1) & 1][i] = kp[2 * (2 * g + 2 + (i >> 1)) * KU + (i & 1) * 32];
+            }
+            __builtin_amdgcn_sched_barrier(0x6);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i & 1] = mfma32<A>(kf[g & 1][i], qf[2 * g + (i >> 1)], s[i & 1]);
+            __builtin_amdgcn_sched_barrier(0x6);
+          }
+          if (edge) mask(s, tile, bad);
+          const float mu = follow(top_of(s));
+          u32x4 pf[4], unused;
+          auto take_exp = [&](int q) {   // P of the 16 tokens of step q
+            float pr[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-              if (!((seen >> r) & 1)) s[h >> 1][8 * (h & 1) + r] = -INFINITY;
+              l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q >> 1][8 * (q & 1) + r], sl, -mu));
+            p_operand<A, false>(pr, pf[q], unused);
+          };
+          // ---- O^T += V^T P^T
+          // the exponentials of one step and the operands' reads beside the products of
+          // the step before
+          const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
+          u32x4 vf[2][ND];
+#pragma unroll
+          for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
+          take_exp(0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (q < 3) {
+#pragma unroll
+              for (int n = 0; n < ND; ++n) vf[(q + 1) & 1][n] = vp[2 * (q + 1) * D + n * 32];
+            }
+#pragma unroll
+            for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
+            if (q < 3) take_exp(q + 1);
           }
         }
-        // ---- running maximum and sum
-        float top = s[0][0];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = max3(top, s[0][r], s[1][r]);
-        top = max3(top, __shfl_xor(top, 32), top) * sl;
-        if (__ballot(top > m + 8.f)) {
-          const float mn = top > m ? top : m;
-          const float f = m == -INFINITY ? 1.f : exp2f(m - mn);   // (nothing yet, or what is not finite)
-          l *= f;
-#pragma unroll
-          for (int n = 0; n < ND; ++n) o[n] *= f;
-          m = mn;
-        }
-        const float mu = safe_max(m);
-        u32x4 pf[4], unused;
-        auto take_exp = [&](int q) {   // P of the 16 tokens of step q
-          float pr[8];
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q >> 1][8 * (q & 1) + r], sl, -mu));
-          p_operand<A, false>(pr, pf[q], unused);
-        };
-        // ---- O^T += V^T P^T
-        // the exponentials of one step and the operands' reads beside the products of
-        // the step before
-        const u32x4* vp = &sh.v[slot][hi][col];    // step q, block n: vp[2 * q * D + n * 32]
-        u32x4 vf[2][ND];
-#pragma unroll
-        for (int n = 0; n < ND; ++n) vf[0][n] = vp[n * 32];
-        take_exp(0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (q < 3) {
-#pragma unroll
-            for (int n = 0; n < ND; ++n) vf[(q + 1) & 1][n] = vp[2 * (q + 1) * D + n * 32];
-          }
-#pragma unroll
-          for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
-          if (q < 3) take_exp(q + 1);
+        if (more) {
+          commit_k(slot ^ 1);
+          commit_v(slot ^ 1);
         }
       }
-      if (more) commit(slot ^ 1);
+    } else {
+      float next_top = 0.f;   // of the lane's scores of the next tile, before they are masked
+      // One tile, whose scores s the step before has computed; sn becomes the next tile's.
+      // K is loaded two tiles ahead, V one.  The step before the first tile only does the
+      // latter.
+      auto step = [&](auto parity, f32x16(&s)[2], f32x16(&sn)[2], const int tile, const bool before) {
+        constexpr int par = decltype(parity)::value;
+        const bool kmore = tile + 2 * KU < p.key1, vmore = !before && tile + KU < p.key1;
+        arrived();
+        if (kmore && (int)kv_div(kv, (uint32_t)(tile + 3 * KU - 1)) - b0 >= NIDS) load_ids(max(tile, p.key0));
+        const bool edge = !before && is_edge(tile);
+        unsigned long long bad = 0;
+        if (edge) bad = clean(tile, par);
+        const u32x4* kp = &sh.k[par ^ 1][hi][ktok];   // piece 2 n of half kt: kp[2 * n * KU + kt * 32]
+        const u32x4* vp = &sh.v[par][hi][col];        // step q, block n: vp[2 * q * D + n * 32]
+        if (!before && sees(tile)) {
+          find(0, tile + 2 * KU, kpg, kst);
+          find(1, tile + KU, vpg, vst);
+          if (edge) mask(s, tile, bad);
+          const float mu = follow(edge ? top_of(s) : next_top);
+          // ---- P of this tile, the next tile's S^T = K Q^T and O^T += V^T P^T, woven: a
+          // product and an exponential (32 cycles and about 26) at a time, in this order
+          using Order = Weave<NQ, ND>;
+          constexpr int R = Order::ring;
+          u32x4 fr[R];
+          auto read = [&](int j) {   // operand of product j
+            const int w = Order::op[j];
+            if (w < 64) fr[j % R] = kp[2 * (w >> 1) * KU + (w & 1) * 32];
+            else fr[j % R] = vp[2 * ((w - 64) / ND) * D + (w - 64) % ND * 32];
+          };
+          u32x4 pf[4];
+          auto product = [&](int j) {
+            const int w = Order::op[j];
+            if (w < 64) sn[w & 1] = mfma32<A>(fr[j % R], qf[w >> 1], w < 2 ? f32x16{} : sn[w & 1]);
+            else o[(w - 64) % ND] = mfma32<A>(fr[j % R], pf[(w - 64) / ND], o[(w - 64) % ND]);
+            if (j + R < Order::n) read(j + R);
+          };
+#pragma unroll
+          for (int j = 0; j < R; ++j) read(j);
+          float y[2] = {0.f, 0.f};   // the pair before
+          int j = 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            __builtin_amdgcn_sched_barrier(0);
+            const float x = __builtin_fmaf(s[e >> 4][e & 15], sl, -mu);
+            if (e && !(e & 1)) pf[(e - 1) >> 3][((e - 1) >> 1) & 3] = pack2<A>(y[0], y[1]);
+            if (j < Order::n && Order::at[j] == e) product(j++);
+            if (e % (16 / LPW) == 0) {   // the loads, one at a time
+              const int i = e / (16 / LPW);
+              if (i < LPW) load_k(i, par);
+              else load_v(i - LPW, par ^ 1);
+            }
+            if (e) l += y[(e - 1) & 1];
+            asm volatile("" : "+v"(l));   // (else the sums gather after the last product)
+            y[e & 1] = __builtin_amdgcn_exp2f(x);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          pf[3][3] = pack2<A>(y[0], y[1]);
+          l += y[1];
+          float t0 = sn[0][0], t1 = sn[1][0];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if (j < Order::n && (r & 1) == 0) product(j++);
+            t0 = max3(t0, sn[0][2 * r], sn[0][2 * r + 1]);
+            t1 = max3(t1, sn[1][2 * r], sn[1][2 * r + 1]);
+            asm volatile("" : "+v"(t0), "+v"(t1));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (; j < Order::n; ++j) product(j);
+          next_top = max3(t0, t1, t1);
+        } else {
+          if (kmore) issue_k(tile + 2 * KU, par);
+          if (vmore) issue_v(tile + KU, par ^ 1);
+          if (tile + KU < p.key1 && sees(tile + KU)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                sn[h] = mfma32<A>(kp[2 * n * KU + h * 32], qf[n], n ? sn[h] : f32x16{});
+            next_top = top_of(sn);
+          }
+        }
+        if (kmore) commit_k(par);
+        if (vmore) commit_v(par ^ 1);
+      };
+      f32x16 s0[2], s1[2];
+      int tile = p.key0 - KU;
+      step(std::integral_constant<int, 1>{}, s1, s0, tile, true);
+      for (tile += KU;; tile += KU) {
+        step(std::integral_constant<int, 0>{}, s0, s1, tile, false);
+        if ((tile += KU) >= p.key1) break;
+        step(std::integral_constant<int, 1>{}, s1, s0, tile, false);
+        if (tile + KU >= p.key1) break;
+      }
+      // the loads past the last tile, ahead of the next piece's into the same slots
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
@@ -1373,6 +1553,47 @@ inline int blocks_of(int n_cu) { return std::min(2 * n_cu / 8 * 8, 1024); }
 // Every wave for itself once there are two (sequence, head) pairs a block.
 inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_seqs * H >= 2 * blocks_of(n_cu); }
 
+// Tiles of 256 rows in eight waves, one block a CU, where sequences have 512 rows on
+// average and a block gets 24 units or more, as far as the host can tell: if the caches
+// are as long as their tables (or the window).  Measured, us of a call with four / eight
+// waves, 64 query heads on 8 unless said, bf16 (FP8), by new tokens over keys: 2048 over
+// 16384 1091 / 949 (1208 / 967), the same in a window of 1000 115 / 98, 2 x 256 over 4096
+// 105 / 102 (120 / 104), 4000 over 4000 of 32 heads on 32 206 / 197, 1000 over 30000 of 8
+// on 1 164 / 153; and below the line 4 x 128 over 2000 69 / 72, 512 over 512 48 / 56, 4096
+// over 4096 of 8 on 1 109 / 128, 32 x 5 over 4096 84 / 100, 16 x 300 over 300 of 32 on
+// 32 65 / 76.
+inline bool wide_tiles(const AttendArgs& a, int blocks) {
+  const int64_t rows = (int64_t)a.kv.n_tokens * a.group;
+  if (rows < 512 * (int64_t)a.kv.n_seqs) return false;
+  int64_t keys = (int64_t)a.kv.nb * a.kv.T - a.max_q_len / 2;
+  if (a.window > 0) keys = std::min<int64_t>(keys, a.window);
+  return rows / 256 * a.kv.H * (keys / 64) >= 24 * (int64_t)blocks;
+}
+
+template <typename A, typename KV, int D, int NW>
+hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
+  using TT = Tiles<A, KV, D, NW>;
+  const size_t lds = sizeof(typename TT::Shared);
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D, NW>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW>), dim3(G), dim3(NW * 64), lds, s, a);
+  // tiles of which none has many parts: four blocks each; else the list.  Measured
+  // (us of a call, list / this): 32 sequences of 5 x 8 rows 86.7 / 84.6, 2 of 256 x
+  // 8 rows over 4096 tokens 110 / 104, 64 x 4 rows of 8 heads over 2000 tokens 28.8
+  // / 34.0, 100 x 8 rows of one head over 30000 tokens 43.9 / 118
+  const int64_t tiles = a.kv.H * std::max<int64_t>(a.kv.n_seqs, (int64_t)a.kv.n_tokens * a.group / TT::TR);
+  if (2 * tiles >= G) {
+    constexpr int RB = 256 / (D / 4);
+    const int rows = (int)std::min<int64_t>((int64_t)a.max_q_len * a.group, TT::TR);
+    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)),
+                       dim3(256), 0, s, a, G);
+  } else {
+    hipLaunchKernelGGL((k_attend_join_list<A, D, TT::TR>), dim3(2 * G), dim3(256), 0, s, a, G);
+  }
+  return hipGetLastError();
+}
+
 template <typename A, typename KV, int D>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
   const int64_t most = (int64_t)a.max_q_len * a.group;
@@ -1385,25 +1606,10 @@ hipError_t launch(const AttendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attend_rows<A, KV, D, false>), dim3(G), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(G, (unsigned)most), dim3(256), 0, s, a, G);
   } else {
-    using TT = Tiles<A, KV, D>;
-    const size_t lds = sizeof(typename TT::Shared);
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (attr != hipSuccess) return attr;
-    hipLaunchKernelGGL((k_attend_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a);
-    // tiles of which none has many parts: four blocks each; else the list.  Measured
-    // (us of a call, list / this): 32 sequences of 5 x 8 rows 86.7 / 84.6, 2 of 256 x
-    // 8 rows over 4096 tokens 110 / 104, 64 x 4 rows of 8 heads over 2000 tokens 28.8
-    // / 34.0, 100 x 8 rows of one head over 30000 tokens 43.9 / 118
-    const int64_t tiles = a.kv.H * std::max<int64_t>(a.kv.n_seqs, (int64_t)a.kv.n_tokens * a.group / TT::TR);
-    if (2 * tiles >= G) {
-      constexpr int RB = 256 / (D / 4);
-      const int rows = (int)std::min<int64_t>(most, TT::TR);
-      hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)),
-                         dim3(256), 0, s, a, G);
-    } else {
-      hipLaunchKernelGGL((k_attend_join_list<A, D, TT::TR>), dim3(2 * G), dim3(256), 0, s, a, G);
-    }
+    // FP8 of 64 elements has too few loads in a tile for eight waves
+    constexpr bool wide = D / ET<KV>::E % 8 == 0;
+    if (wide && wide_tiles(a, G / 16 * 8)) return launch_tiles<A, KV, D, wide ? 8 : 4>(a, G / 16 * 8, s);
+    return launch_tiles<A, KV, D, 4>(a, G, s);
   }
   return hipGetLastError();
 }

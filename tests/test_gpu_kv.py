@@ -623,3 +623,102 @@ def test_attend_of_overlapping_rows_does_nothing_when_they_are_too_many(n_seqs, 
             assert torch.all(out == 5) and torch.all(lse == 5)
         else:
             assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+# Batches whose rows and tables make them calls of the tiles of 256 rows (8 waves), which
+# the host chooses by the tables' capacity: short caches in long tables
+WIDE = [("f16", "f16", 4096, 128), ("bf16", "bf16", 5120, 128), ("bf16", "fp8", 5120, 128), ("f16", "fp8", 4096, 128),
+        ("f16", "f16", 5120, 64), ("bf16", "bf16", 2056, 64)]
+
+
+def wide_case(act, kv, page, D, H, G, q_len, kv_len, **kw):
+    keys = 64 * (24 * 512 * 256 // (sum(q_len) * G * H) + 64)     # capacity, with room for any number of CUs
+    T = page * 2 // (D * (1 if kv == "fp8" else 2))
+    return Case(act, kv, page, H, D, q_len, kv_len, extra_blocks=keys // (T // 16 * 16 or 8), **kw)
+
+
+@pytest.mark.parametrize("act,kv,page,D", WIDE)
+@pytest.mark.parametrize("H,G,q_len,kv_len,window", [
+    (1, 8, [130], [130], 0),                 # from the first position on
+    (2, 3, [256, 200], [256, 463], 0),       # tiles with one row left over, odd positions
+    (1, 16, [5, 70], [700, 71], 0),          # few and many rows, one key before them
+    (1, 8, [100, 64], [350, 1000], 0),
+])
+def test_attend_wide_chunks(act, kv, page, D, H, G, q_len, kv_len, window):
+    log("[case] attend wide %s/%s page %d D %d H %d G %d %s %s window %d" % (act, kv, page, D, H, G, q_len, kv_len, window))
+    with wide_case(act, kv, page, D, H, G, q_len, kv_len, seed=25) as c:
+        c.fill()
+        q = torch.randn((c.n, H * G, D), device="cuda", generator=c.gen).to(TD[act])
+        check(c, q, 0.09, window)
+
+
+@pytest.mark.parametrize("act,kv", [("f16", "f16"), ("bf16", "fp8")])
+def test_attend_wide_absent_pages_and_rows_without_keys(act, kv):
+    # pages that are gone at the start, in the middle and at the end; rows before position 0
+    q_len, kv_len = [90, 60], [400, 33]
+    with wide_case(act, kv, 4096, 128, 1, 8, q_len, kv_len, seed=26, drop=[(0, 0), (0, 3)]) as c:
+        c.fill()
+        there = [np.repeat((c.table_host[s] >= 0).all((0, 1)), c.T)[:m] for s, m in enumerate(kv_len)]
+        q = torch.randn((c.n, 8, 128), device="cuda", generator=c.gen).to(TD[act])
+        check(c, q, 0.1, there=there)
+        c.table[0, 1, :, 5] = c.n_pages + 3
+        there[0][5 * c.T:6 * c.T] = False
+        check(c, q, 0.1, there=there)
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "fp8"])
+def test_attend_wide_what_is_not_seen_has_no_influence(kv):
+    # infinities and NaN in K and V: rows that see them get them, others not
+    act = "bf16" if kv == "fp8" else kv
+    with wide_case(act, kv, 4096, 128, 1, 8, [90, 70], [300, 200], seed=27) as c:
+        c.fill()
+        q = torch.randn((c.n, 8, 128), device="cuda", generator=c.gen).to(TD[act])
+        want, _ = check(c, q, 0.1)
+        # tokens 250 and 299 of the first sequence, 140 of the second: seen by later rows only
+        for s, j, d, val in ((0, 250, 5, float("nan")), (0, 299, 7, float("inf")), (1, 140, 100, -float("inf"))):
+            at = j + (300 if s else 0)
+            c.v[at, 0, d] = val
+            x = c.v[at:at + 1].double().cpu().numpy()
+            c.vd[s][j:j + 1] = dequant(*quant(x)) if c.fp8 else x
+        starts = torch.tensor([0, 300, 500], dtype=torch.int32, device="cuda")
+        L.lora_kv_write(c.cache, L.KvBatch(starts, c.kvl, torch.from_numpy(c.full_table).cuda(), 500, 300), c.k, c.v)
+        out, _ = check(c, q, 0.1)
+        assert torch.equal(out[:40], want[:40]) and torch.equal(out[90:100], want[90:100])
+
+
+def check_rows(c, q, scale, window, tokens, got):
+    """Some tokens of a batch of one sequence (tolerances as in check, bf16)."""
+    o, l = got[0][tokens].double().cpu().numpy(), got[1][tokens].double().cpu().numpy()
+    x, H, base = q[tokens].double().cpu().numpy(), q.shape[1], c.kv_len[0] - c.n
+    for i, t in enumerate(tokens):
+        pos = base + t
+        lo = max(0, pos - window + 1) if window else 0
+        for h in range(H):
+            k, v = c.kd[0][lo:pos + 1, h * c.H // H], c.vd[0][lo:pos + 1, h * c.H // H]
+            s = scale * (k @ x[i, h])
+            p = np.exp(s - s.max())
+            want, size = p @ v / p.sum(), p @ np.abs(v) / p.sum()
+            d = c.D * 2.0 ** -24 * scale * (np.abs(k) @ np.abs(x[i, h])).max()
+            assert np.all(np.abs(o[i, h] - want) <= 1.1 * 2.0 ** -8 * size + 1.01 * 2.0 ** -8 * np.abs(want)
+                          + (np.expm1(2 * d) + 1e-7) * size), (t, h)
+            ls = s.max() + np.log(p.sum())
+            assert abs(l[i, h] - ls) <= d + 2.0 ** -21 * max(1, abs(ls)), (t, h)
+
+
+def test_attend_wide_repeats_and_spans_many_tiles():
+    # several tiles of 256 rows a head, whole rounds of them and a cut rest, twice the same bits
+    with wide_case("bf16", "bf16", 4096, 64, 8, 8, [1100], [1100], seed=28) as c:
+        c.fill()
+        q = torch.randn((c.n, 64, 64), device="cuda", generator=c.gen).to(TD["bf16"])
+        a, b = attend(c, q, 0.1), attend(c, q, 0.1)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        check_rows(c, q, 0.1, 0, [0, 1, 31, 32, 255, 256, 700, 1023, 1024, 1098, 1099], a)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attend_wide_in_a_window(kv):
+    # 64 heads on one and a window of 2000: tiles enough for the wide form
+    with Case("bf16", kv, 8192, 1, 128, [900], [3100], seed=29) as c:
+        c.fill()
+        q = torch.randn((c.n, 64, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        check_rows(c, q, 0.1, 2000, [0, 1, 3, 4, 63, 64, 500, 898, 899], attend(c, q, 0.1, window=2000))
