@@ -6,10 +6,10 @@
 // there.  One pass over the keys with a running maximum and sum.
 //
 // The rows of one kv head are its G query heads times the sequence's new tokens:
-// row r is token r / G, head h G + r % G.  Two kernels share the sequences by
-// their row count: up to 16 rows (single tokens and few drafted ones: bound by
-// HBM) and more (chunks: bound by the matrix cores).  Both compute the transposed
-// products
+// row r is token r / G, head h G + r % G.  The longest sequence's row count chooses
+// one of two kernels: up to 16 rows (FP8 caches: 32; single tokens and few drafted
+// ones: bound by HBM) and more (chunks: bound by the matrix cores and the vector
+// ALUs).  Both compute the transposed products
 //   S^T = K Q^T      O^T = V^T P^T
 // so that a query is a column: its scores lie in one lane group's registers, the
 // row maximum and sum need one exchange between lanes, and P leaves the first
@@ -496,7 +496,8 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f
 // ---- the joining launch ----------------------------------------------------------
 // RB rows a block: weights of the parts by their maxima, then a
 // weighted sum, D / 4 lanes a part and several parts at a time.  Bound by the reads
-// of the parts; each is a contiguous D * 4 bytes.
+// of the parts; each is a contiguous D * 4 bytes.  Measured 3.7 us (one token of 517,
+// 32 heads, 2.5 at the least) to 8 us (32 sequences of 40 rows, 8 heads).
 template <typename A, int D, int TR, int RB>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
   constexpr int LR = D / 4, PG = 256 / RB / LR;            // lanes of a part, parts at a time
@@ -655,6 +656,10 @@ __global__ __launch_bounds__(256) void k_attend_join_list(AttendArgs a, int G) {
 // tile of keys, and join their results in LDS; with many (SOLO) every wave works
 // for itself, its range of the units cut as the blocks' ones are: no wave waits
 // for another, and short sequences take their turns on 4 times as many workers.
+// Measured: 64 sequences of 20 to 2048 tokens, 32 heads of 128, bf16, 1.15 GB of K and
+// V, 214 us, 5.4 TB/s; 3 of 40001 to 131071 tokens, 8 heads for 64, FP8, 600 MB, 114 us,
+// 5.3 TB/s (a device copy of 1 GiB moves 4.8 TB/s, a sum reads 4.0); one of 517 tokens,
+// 32 heads, 9.3 us, of which two empty launches are 4.6.
 template <typename A, typename KV, int D, bool SOLO>
 struct Skinny {
   static constexpr bool Q8 = is_quant<KV>();
@@ -1547,10 +1552,21 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
 }
 
 // Rows of a head of the longest sequence choose the kernel for all of a batch.
-inline bool few_rows(int32_t group, int32_t max_q_len) { return (int64_t)max_q_len * group <= 16; }
+// One tile of 16 of them, or of FP8 caches two (the tiles of 128 rows convert every code
+// for whatever rows there are).  Measured, us by k_attend_rows / k_attend_tiles, new
+// tokens of 64 query heads on 8 unless said: 16 rows, bf16, 2 over 500 11.0 / 14.7, 2
+// over 30000 32.0 / 37.8, 32 x 2 over 2000 51.8 / 50.2; 32 rows, bf16, 4 over 500 12.1 /
+// 14.8, 4 over 30000 47.5 / 39.2, 64 x 32 over 500 of 32 heads on 32 215 / 116; 32 rows,
+// FP8, 12.9 / 15.3, 31.4 / 39.2, 101 / 125; 40 and 48 rows, FP8, 5 over 30000 39.8 /
+// 43.4, 32 x 5 over 2000 85 / 58, 32 x 6 87 / 59.
+inline bool few_rows(bool fp8, int32_t group, int32_t max_q_len) {
+  return (int64_t)max_q_len * group <= (fp8 ? 32 : 16);
+}
 inline int blocks_of(int n_cu) { return std::min(2 * n_cu / 8 * 8, 1024); }
 
-// Every wave for itself once there are two (sequence, head) pairs a block.
+// Every wave for itself once there are two (sequence, head) pairs a block.  Measured, us
+// by blocks / by waves: 64 sequences of 16 tokens, 32 heads, 22 / 10, of 20 to 2048 250 /
+// 214; with fewer pairs a wave's range ends inside its tiles and the parts cost more.
 inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_seqs * H >= 2 * blocks_of(n_cu); }
 
 // Tiles of 256 rows in eight waves, one block a CU, where sequences have 512 rows on
@@ -1596,8 +1612,8 @@ hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
 
 template <typename A, typename KV, int D>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
-  const int64_t most = (int64_t)a.max_q_len * a.group;
-  const bool few = few_rows(a.group, a.max_q_len);
+  const int64_t most = std::min<int64_t>((int64_t)a.max_q_len * a.group, 16);   // rows of a tile
+  const bool few = few_rows(is_quant<KV>(), a.group, a.max_q_len);
   const int G = blocks_of(a.n_cu);
   if (few && solo_waves(a.kv.n_seqs, a.kv.H, a.n_cu)) {
     hipLaunchKernelGGL((k_attend_rows<A, KV, D, true>), dim3(G), dim3(256), 0, s, a);
@@ -1623,14 +1639,14 @@ hipError_t launch_d(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {
 
 size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len, int32_t n_seqs,
                         int32_t H) {
-  const bool few = few_rows(group, max_q_len);
+  const bool few = few_rows(ty.kv == LORA_FP8_E4M3, group, max_q_len);
   const size_t G = (size_t)blocks_of(n_cu) * (few && solo_waves(n_seqs, H, n_cu) ? 4 : 1);
   const size_t TR = few ? 16 : 128, D = (size_t)ty.D;
   return G * (sizeof(PartDesc) + sizeof(int) + 2 * TR * 2 * sizeof(float) + 2 * TR * D * sizeof(float));
 }
 
 int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len) {
-  const bool few = few_rows(group, max_q_len);
+  const bool few = few_rows(v.scales != nullptr, group, max_q_len);
   const int TR = few ? 16 : 128, KU = few ? 32 : 64;
   const int64_t tiles = ((int64_t)v.n_tokens * group + TR - 1) / TR + v.n_seqs;
   return tiles * v.H * ((int64_t)v.nb * v.T / KU + 2);

@@ -625,6 +625,17 @@ def test_attend_of_overlapping_rows_does_nothing_when_they_are_too_many(n_seqs, 
             assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
 
 
+@pytest.mark.parametrize("act,kv,page,D", [("f16", "f16", 4096, 128), ("bf16", "fp8", 5120, 128), ("f16", "fp8", 4096, 64)])
+@pytest.mark.parametrize("H,G,q_len,window", [(1, 1, [17, 32, 5], 0), (2, 8, [2, 4, 3], 0), (1, 16, [2, 1, 0], 40),
+                                              (3, 3, [10, 1, 7], 1), (1, 1, [31, 33, 2], 0), (1, 17, [1, 1, 1], 0)])
+def test_attend_between_the_kernels(act, kv, page, D, H, G, q_len, window):
+    # 16 and 32 rows of a head and their neighbours: one and two tiles of 16 rows, and tiles of 128
+    with Case(act, kv, page, H, D, q_len, [300, 33, 129], seed=30) as c:
+        c.fill()
+        q = torch.randn((c.n, H * G, D), device="cuda", generator=c.gen).to(TD[act])
+        check(c, q, 0.09, window)
+
+
 # Batches whose rows and tables make them calls of the tiles of 256 rows (8 waves), which
 # the host chooses by the tables' capacity: short caches in long tables
 WIDE = [("f16", "f16", 4096, 128), ("bf16", "bf16", 5120, 128), ("bf16", "fp8", 5120, 128), ("f16", "fp8", 4096, 128),
