@@ -25,8 +25,9 @@
  *   - Pointers named *_dev are device pointers (HBM), *_host are host pointers.
  *     The caller owns every buffer it passes in; the library never frees them.
  *   - `stream` is a hipStream_t (NULL: the null stream).  Compute entry points
- *     (lora_bgmv_*, lora_sgmv_*, lora_apply) are stream-ordered: they neither
- *     allocate memory nor wait for the device.  Set-up calls (pool creation,
+ *     (lora_bgmv_*, lora_sgmv_*, lora_apply, lora_kv_write / read / attend,
+ *     lora_spec_verify) are stream-ordered: they neither allocate memory nor
+ *     wait for the device.  Set-up calls (pool creation,
  *     upload, evict, page-table build, plan create/build/prepare) may do both.
  *   - x rows are d_in elements of the pool's activation dtype (act_dtype:
  *     the page dtype, except 16-bit activations on FP8 pools), y rows d_out
@@ -437,8 +438,8 @@ typedef struct {
  * device and never trusted: rows outside [0, n_tokens] and positions past the
  * table's max_blocks * T are cut off, and tokens whose K or V page id lies
  * outside [0, n_pages) (e.g. -1: given back, or never there) are absent.
- * max_q_len: the longest q_len (a bound for workspaces and the choice of
- * kernels; results do not depend on it). */
+ * max_q_len: the longest q_len (it chooses among kernels; a wrong one changes no
+ * more than the rounding and the time). */
 typedef struct {
   int32_t n_seqs;          /* 0..1024                                            */
   int32_t n_tokens;        /* rows of the new tensors, 0..2^24                   */
@@ -480,11 +481,16 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * h / (n_q_heads / n_kv_heads).  The token at position i sees the present tokens
  * j with j <= i and, if window > 0, j > i - window:
  *   out_i = sum_j p_ij v_j,  p_i. = softmax of scale * q_i . k_j over those j
- * in fp32, with p rounded to 16 bits (FP8 caches: bf16) for the products with v,
- * and one rounding at the store.  A token that sees none gets zeros.  What is
+ * with fp32 scores, maxima and sums.  For the products with v, p goes in 16-bit
+ * terms: two (relative 2^-16 of bf16, 2^-22 of f16) in calls of few rows, where
+ * max_q_len * n_q_heads / n_kv_heads <= 16 (FP8 caches: 32), else one of act_dtype
+ * (2^-8, 2^-11).  One rounding at the store.  A token that sees none gets zeros.  What is
  * not seen has no influence, whatever it holds.  lse (optional, NULL)
  * [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j), -inf for none.  Rows
- * of q that belong to no sequence are not written.  Stream-ordered, no host
+ * of out that belong to no sequence are not written.  LORA_E_UNSUPPORTED for
+ * calls that could need 2^31 units of work (a tile of rows with 64 keys, if every
+ * cache filled its table); overlapping rows of a q_start that does not ascend are
+ * undefined, and nothing at all if they make that many.  Stream-ordered, no host
  * wait, no allocation (graph-capturable); workspace_dev: 256-byte aligned, at
  * least lora_kv_attend_workspace_size bytes, no initial contents; calls that
  * share one must not overlap.  Runs of one batch give the same bits. */
