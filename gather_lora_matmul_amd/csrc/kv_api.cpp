@@ -182,7 +182,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   AttendArgs a;
   LORA_TRY(view_of(p, d, b, ty, a.kv));
   LORA_TRY(check_heads(d, n_q_heads, b));
-  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+  if (!(scale > 0.f) || !std::isfinite(scale * 2.8853900817779268f))   // (f16 over FP8 doubles it)
     return fail(LORA_E_ARG, "scale must be positive and finite");
   if (window < 0) return fail(LORA_E_ARG, "negative window");
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_q_len == 0) return LORA_OK;
