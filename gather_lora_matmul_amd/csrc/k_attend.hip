@@ -97,21 +97,21 @@ __device__ __forceinline__ u32x4 keep8(u32x4 u, uint32_t bits) {
   return u;
 }
 
-// P in the 16 bits of the second product's operand: rounded, relative 2^-8 (bf16)
-// or 2^-11 (f16) a term at most, and where SPLIT what the rounding left as a
-// second operand (together 2^-16 of bf16, 2^-22 of f16).  The sums take P
-// unrounded: lse is an fp32 result.
-template <typename T, bool SPLIT>
+// P in the 16 bits of the second product's operands: rounded, relative 2^-8 (bf16)
+// or 2^-11 (f16) at most, and what the rounding left as a second operand (together
+// 2^-16 of bf16, 2^-22 of f16): the results' error is that of fp32 weights.  Only the
+// tiles of 256 rows, bound by the matrix cores, take the first term alone.  The sums
+// take P unrounded: lse is an fp32 result.
+template <typename T>
 __device__ __forceinline__ void p_operand(const float* p, u32x4& hi, u32x4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[i] = pack2<T>(p[2 * i], p[2 * i + 1]);
-    if (SPLIT)
-      l[i] = pack2<T>(p[2 * i] - bits_to_f<T>(h[i] & 0xffffu), p[2 * i + 1] - bits_to_f<T>(h[i] >> 16));
+    l[i] = pack2<T>(p[2 * i] - bits_to_f<T>(h[i] & 0xffffu), p[2 * i + 1] - bits_to_f<T>(h[i] >> 16));
   }
   hi = u32x4{h[0], h[1], h[2], h[3]};
-  if (SPLIT) lo = u32x4{l[0], l[1], l[2], l[3]};
+  lo = u32x4{l[0], l[1], l[2], l[3]};
 }
 
 // Values without a finite number in V must reach the rows that see their token
@@ -895,7 +895,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       }
       u32x4 pf[E / 8], pl[E / 8];
 #pragma unroll
-      for (int q = 0; q < E / 8; ++q) p_operand<PT, true>(pr + 8 * q, pf[q], pl[q]);
+      for (int q = 0; q < E / 8; ++q) p_operand<PT>(pr + 8 * q, pf[q], pl[q]);
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int n = 0; n < ND; ++n) {
@@ -1010,6 +1010,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // loads to LDS arrive at 53 bytes a cycle and CU, and issuing a tile's at once stops a
 // wave for 600 to 1300 cycles; 256 rows halve them a row.  Weaving alone (four waves:
 // 1055 us) and more rows alone (1079) give less, and both cost the short calls.
+//   Four waves take P in two 16-bit terms: their results are then as near as fp32 weights
+// make them, and their matrix cores wait for loads (with one term: 32 x 5 over 900 to
+// 4100 tokens, 64 heads on 8, 86.3 us against 88.4 with two, FP8 92.0 against 100.2; 4 x
+// 128 over 2000 70.2 against 82.0, 16 x 300 over 300 of 32 heads on 32 68.2 against 72.3,
+// the mixed batch of 15 heads of 64 in a window of 1000 59.1 against 65.0).  Eight waves
+// take one, because the matrix cores bound them: of the calls above 2048 over 16384 takes
+// 1011 us with one term and 1493 with two, and what one term costs is that an output's
+// error grows from its own rounding's to 1.4 times that.
 __device__ __forceinline__ void load_lds16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -1381,13 +1389,13 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
           }
           if (edge) mask(s, tile, bad);
           const float mu = follow(top_of(s));
-          u32x4 pf[4], unused;
+          u32x4 pf[4], pl[4];
           auto take_exp = [&](int q) {   // P of the 16 tokens of step q
             float pr[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r)
               l += pr[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q >> 1][8 * (q & 1) + r], sl, -mu));
-            p_operand<A, false>(pr, pf[q], unused);
+            p_operand<A>(pr, pf[q], pl[q]);
           };
           // ---- O^T += V^T P^T
           // the exponentials of one step and the operands' reads beside the products of
@@ -1406,6 +1414,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
             }
 #pragma unroll
             for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pf[q], o[n]);
+#pragma unroll
+            for (int n = 0; n < ND; ++n) o[n] = mfma32<A>(vf[q & 1][n], pl[q], o[n]);
             if (q < 3) take_exp(q + 1);
           }
         }

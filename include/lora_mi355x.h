@@ -481,10 +481,11 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * h / (n_q_heads / n_kv_heads).  The token at position i sees the present tokens
  * j with j <= i and, if window > 0, j > i - window:
  *   out_i = sum_j p_ij v_j,  p_i. = softmax of scale * q_i . k_j over those j
- * with fp32 scores, maxima and sums.  For the products with v, p goes in 16-bit
- * terms: two (relative 2^-16 of bf16, 2^-22 of f16) in calls of few rows, where
- * max_q_len * n_q_heads / n_kv_heads <= 16 (FP8 caches: 32), else one of act_dtype
- * (2^-8, 2^-11).  One rounding at the store.  A token that sees none gets zeros.  What is
+ * with fp32 scores, maxima and sums.  For the products with v, p goes in two 16-bit
+ * terms (relative 2^-16 of bf16, 2^-22 of f16; bf16 for FP8 caches in calls of at
+ * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11): where there
+ * are 512 rows a head and sequence on average, and full tables (or the window) would
+ * give every compute unit 24 tiles of 256 rows and 64 keys.  One rounding at the store.  A token that sees none gets zeros.  What is
  * not seen has no influence, whatever it holds.  lse (optional, NULL)
  * [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j), -inf for none.  Rows
  * of out that belong to no sequence are not written.  LORA_E_UNSUPPORTED for
