@@ -202,15 +202,16 @@ __device__ __forceinline__ int token_of(const AttendArgs& a, int row) {  // row 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
-// row's window, down to a multiple of KU, to the last row's own position.
+// row's window, down to a multiple of KU, to the last row's own position or the
+// table's end.
 template <int KU>
 __device__ __forceinline__ void tile_keys(const AttendArgs& a, const KvSeq& q, int row0, int rows,
                                           int& lo, int& hi) {
   const int t0 = token_of(a, row0), t1 = token_of(a, row0 + rows - 1);
-  const int base = q.kv_len - q.q_len;
-  hi = base + t1 + 1;
+  hi = min(q.base + t1 + 1, q.end);
   lo = 0;
-  if (a.window > 0 && base + t0 + 1 - a.window > 0) lo = (base + t0 + 1 - a.window) / KU * KU;
+  if (a.window > 0 && q.base + t0 + 1 - a.window > 0)
+    lo = min(q.base + t0 + 1 - a.window, max(q.end - 1, 0)) / KU * KU;
   if (hi <= lo) hi = lo + 1;  // nothing is seen: one unit, all of it masked
 }
 template <int KU, int TR>
@@ -270,7 +271,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
   for (int s0 = 0; s0 < n; s0 += small ? 64 : THREADS) {
     const int s = s0 + (small ? lane : tid);
     int units = 0;
-    KvSeq q{0, 0, 0};
+    KvSeq q{0, 0, 0, 0};
     if (s < n) q = kv_seq(a.kv, s);
     const int tiles = (q.q_len * a.group + TR - 1) / TR;
 #pragma unroll
@@ -278,7 +279,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
       if (t < tiles) units += tile_units<KU, TR>(a, q, t);
     for (unsigned long long more = __ballot(tiles > FEW); more; more &= more - 1) {
       const int src = __builtin_ctzll(more);
-      const KvSeq u{__shfl(q.q0, src), __shfl(q.q_len, src), __shfl(q.kv_len, src)};
+      const KvSeq u{0, __shfl(q.q_len, src), __shfl(q.base, src), __shfl(q.end, src)};
       const int tu = __shfl(tiles, src);
       int part = 0;
       for (int t = FEW + lane; t < tu; t += 64) part += tile_units<KU, TR>(a, u, t);
@@ -292,7 +293,7 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
       if (lane >= d) sum += z;
     }
     if (preT && small) {
-      longest = tiles > 0 ? (q.kv_len + KU - 1) / KU : 0;
+      longest = tiles > 0 ? (q.end + KU - 1) / KU : 0;
       int st = tiles * a.kv.H;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -383,7 +384,8 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, 
     p.q = kv_seq(a.kv, p.seq);
     p.q.q0 = uni(p.q.q0);
     p.q.q_len = uni(p.q.q_len);
-    p.q.kv_len = uni(p.q.kv_len);
+    p.q.base = uni(p.q.base);
+    p.q.end = uni(p.q.end);
     const uint32_t th = (uint32_t)(p.q.q_len * a.group + TR - 1) / (uint32_t)TR;
     const uint32_t rem = (uint32_t)(c.tile - uni(preT[p.seq]));
     p.head = (int)(rem / th);
@@ -402,7 +404,8 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, 
   p.q = kv_seq(a.kv, c.seq);
   p.q.q0 = uni(p.q.q0);
   p.q.q_len = uni(p.q.q_len);
-  p.q.kv_len = uni(p.q.kv_len);
+  p.q.base = uni(p.q.base);
+  p.q.end = uni(p.q.end);
   const int before = uni(pre[c.seq]);
   const uint32_t hu = (uint32_t)(uni(pre[c.seq + 1]) - before) / (uint32_t)a.kv.H;
   p.head = (int)((uint32_t)(c.pos - before) / hu);
@@ -699,9 +702,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // ---- queries: operand B of the first product, column = row of the tile
     const int row = p.row0 + min(col, p.rows - 1);
     const int tq = token_of(a, row);
-    const int pos = p.q.kv_len - p.q.q_len + tq;
-    const int posmin = p.q.kv_len - p.q.q_len + token_of(a, p.row0);
-    const int posmax = p.q.kv_len - p.q.q_len + token_of(a, p.row0 + p.rows - 1);
+    const int pos = p.q.base + tq;
+    const int posmin = p.q.base + token_of(a, p.row0);
+    const int posmax = p.q.base + token_of(a, p.row0 + p.rows - 1);
     const int win = a.window > 0 ? a.window : 0x40000000;
     u32x4 qf[S::NQ];
     {
@@ -1155,7 +1158,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   while (next_piece<KU, TR>(a, sh.pre, c, p, sh.preT)) {
     const int wrow0 = p.row0 + wave * 32;
     const int wrows = min(32, p.rows - wave * 32);   // <= 0: no rows of its own
-    const int base = p.q.kv_len - p.q.q_len;
+    const int base = p.q.base;
     const int row = min(wrow0 + col, p.row0 + p.rows - 1);
     const int tq = token_of(a, row);
     const int pos = base + tq;
@@ -1190,7 +1193,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
         sh.ids[w][i % NIDS] = id;
       }
-      any_bad = __syncthreads_or(bad);
+      // (of rows past the table every tile is taken as one with absent pages)
+      any_bad = __syncthreads_or(bad || bmax >= p.q.end);
     };
     // ---- loads of one tile; lane = token for the page lookups
     u32x4 stk[Q8 ? LPW : 1], stv[Q8 ? LPW : 1], vsc[Q8 ? LPW : 1];

@@ -33,7 +33,7 @@ __device__ __forceinline__ int kv_find_seq(const KvView& v, int w, int lane, KvS
   int base = 0;
   for (int stride = v.n_seqs > 64 ? 64 : 1;; stride = 1) {
     const int s = base + lane * stride;
-    KvSeq mine{0, 0, 0};
+    KvSeq mine{0, 0, 0, 0};
     bool le = false;
     if (s < v.n_seqs) {
       mine = kv_seq(v, s);
@@ -45,7 +45,8 @@ __device__ __forceinline__ int kv_find_seq(const KvView& v, int w, int lane, KvS
     if (stride == 1) {
       q.q0 = __builtin_amdgcn_readlane(mine.q0, at);
       q.q_len = __builtin_amdgcn_readlane(mine.q_len, at);
-      q.kv_len = __builtin_amdgcn_readlane(mine.kv_len, at);
+      q.base = __builtin_amdgcn_readlane(mine.base, at);
+      q.end = __builtin_amdgcn_readlane(mine.end, at);
       return base;
     }
   }
@@ -62,13 +63,15 @@ template <int E, int D>
 __device__ __forceinline__ bool kv_group(const KvView& v, int w, int h, int lane, Group& g) {
   KvSeq q;
   const int s = kv_find_seq<E>(v, w, lane, q);
-  const int p0 = q.kv_len > q.q_len ? q.kv_len - q.q_len : 0;  // rows before position 0 have no place
+  // rows before position 0 and past the table have no place
+  const int p0 = q.base > 0 ? q.base : 0;
+  const int p1 = q.base + q.q_len < q.end ? q.base + q.q_len : q.end;
   const int first = p0 / E;
   const int pos = (first + (w - (q.q0 / E + 2 * s))) * E;
-  if (w < q.q0 / E + 2 * s || pos >= q.kv_len || q.q_len == 0) return false;
+  if (w < q.q0 / E + 2 * s || pos >= p1 || p0 >= p1) return false;
   g.lo = p0 > pos ? p0 - pos : 0;
-  g.hi = q.kv_len - pos < E ? q.kv_len - pos : E;
-  g.row = q.q0 + (pos + g.lo - (q.kv_len - q.q_len));
+  g.hi = p1 - pos < E ? p1 - pos : E;
+  g.row = q.q0 + (pos + g.lo - q.base);
   const int b = (int)kv_div(v, (uint32_t)pos);
   const int slot = pos - b * v.T;
   const int32_t* t = v.table + ((int64_t)s * 2 * v.H + h) * v.nb + b;

@@ -56,22 +56,26 @@ inline void div_init(int32_t d, uint32_t& m, int32_t& s) {
   s = k - 1;
 }
 
-// Rows of one sequence's new tokens and their first position, with everything
-// that comes from device memory held inside the buffers: q rows inside
-// [0, n_tokens], the cache inside the table's row.
+// Rows of one sequence's new tokens, their positions, and its cached tokens, with
+// everything that comes from device memory held inside the buffers: rows inside
+// [0, n_tokens], cached tokens inside the table's row.  Positions follow the lengths
+// as they are given (the first row's is kv_len - q_len, and what rows before row 0
+// there are), so that cutting rows or tokens off moves none of the others.
 struct KvSeq {
-  int32_t q0, q_len, kv_len;   // position of new token t: kv_len - q_len + t
+  int32_t q0, q_len;   // rows q0 .. q0 + q_len - 1
+  int32_t base;        // position of row q0, held inside +-2^29 (no token is there)
+  int32_t end;         // cached tokens that the table has place for
 };
 __host__ __device__ inline KvSeq kv_seq(const KvView& v, int s) {
   KvSeq r;
-  const int64_t cap = (int64_t)v.nb * v.T;
-  int a = v.q_start[s], b = v.q_start[s + 1], n = v.kv_len[s];
-  a = a < 0 ? 0 : (a > v.n_tokens ? v.n_tokens : a);
-  b = b < a ? a : (b > v.n_tokens ? v.n_tokens : b);
-  n = n < 0 ? 0 : n;
-  r.q0 = a;
-  r.q_len = b - a;
-  r.kv_len = (int64_t)n > cap ? (int32_t)cap : n;
+  const int64_t cap = (int64_t)v.nb * v.T, far = (int64_t)1 << 29;
+  const int a = v.q_start[s], b = v.q_start[s + 1], n = v.kv_len[s] < 0 ? 0 : v.kv_len[s];
+  r.q0 = a < 0 ? 0 : (a > v.n_tokens ? v.n_tokens : a);
+  const int e = b < r.q0 ? r.q0 : (b > v.n_tokens ? v.n_tokens : b);
+  r.q_len = e - r.q0;
+  const int64_t base = (int64_t)n - b + r.q0;   // n - (b - a) + (q0 - a)
+  r.base = (int32_t)(base < -far ? -far : (base > far ? far : base));
+  r.end = (int64_t)n > cap ? (int32_t)cap : n;
   return r;
 }
 

@@ -435,9 +435,11 @@ typedef struct {
  * cached tokens, its new ones included and last: new token t is at position
  * kv_len[s] - q_len + t.  table [n_seqs][2][n_kv_heads][max_blocks]: page ids of
  * the sequence's K (0) and V (1) blocks of T tokens.  All three are read on the
- * device and never trusted: rows outside [0, n_tokens] and positions past the
- * table's max_blocks * T are cut off, and tokens whose K or V page id lies
- * outside [0, n_pages) (e.g. -1: given back, or never there) are absent.
+ * device and never trusted: rows outside [0, n_tokens) do not exist and positions
+ * past the table's max_blocks * T have no place (what is left keeps its positions:
+ * they follow kv_len and q_start as given, a negative kv_len as 0), and tokens whose
+ * K or V page id lies outside [0, n_pages) (e.g. -1: given back, or never there) are
+ * absent.
  * max_q_len: the longest q_len (it chooses among kernels; a wrong one changes no
  * more than the rounding and the time). */
 typedef struct {
@@ -460,13 +462,14 @@ lora_status lora_kv_layout(const lora_pool* pool, const lora_kv_desc* kv, int32_
  * FP8: a row x of one token and head gets the smallest exponent e in [-126,
  * 127] with 448 * 2^e >= max |x| over its finite elements, and the codes
  * e4m3(x * 2^-e), nearest even; elements that are not finite become NaN codes.
- * Tokens at negative positions and in absent pages are dropped.  No page may
+ * Tokens at negative positions, past the table and in absent pages are dropped.  No page may
  * be named twice by the tokens written. */
 lora_status lora_kv_write(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                           const void* k_dev, const void* v_dev, int64_t ld, void* stream);
 /* The reverse: the cached rows of the batch's tokens (the last q_len of each
  * sequence) into k, v, act_dtype; FP8 values c * 2^e are rounded once.  Rows of
- * absent pages become zero, rows of tokens at negative positions are left. */
+ * absent pages become zero, rows of tokens at negative positions or past the table
+ * are left. */
 lora_status lora_kv_read(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                          void* k_dev, void* v_dev, int64_t ld, void* stream);
 /* Bytes of caller-owned workspace of lora_kv_attend for this batch's max_q_len:

@@ -104,3 +104,120 @@ def test_weights_of_long_work_have_one_term(act, kv):
         _, vd = c.fill()
         q, kd = whole_scores(c, 8)
         check_terms(c, q, kd, vd, act, 1, rows=[[0, 31, 32, 99], [0, 1, 59]])
+
+
+# ---------------------------------------------------------------------------------------------
+# lengths past the table and rows past the call's tokens: nothing moves
+# ---------------------------------------------------------------------------------------------
+# q_start, n_tokens, kv_len of one sequence over a table of 64 tokens -> (first kept row, its position)
+CUT = [
+    ([0, 1], 1, 65, (0, 64)),                # one token past the table
+    ([0, 5], 5, 66, (0, 61)),                # the last of five, too
+    ([0, 3], 3, 67, (0, 64)),                # all of them
+    ([0, 40], 40, 90, (0, 50)),
+    ([0, 2], 2, 2 ** 31 - 1, (0, 2 ** 31 - 3)),
+    ([0, 10], 8, 40, (0, 30)),               # rows past the call's tokens
+    ([0, 30], 20, 80, (0, 50)),              # both
+    ([-2, 5], 5, 40, (0, 35)),               # rows before the first
+    ([-2 ** 31, 5], 5, 40, (0, 35)),
+    ([0, 2 ** 31 - 1], 6, 2 ** 31 - 1, (0, 0)),
+    ([3, 9], 7, 64, (3, 58)),
+    ([0, 6], 6, -7, (0, -6)),                # a length below none is none
+]
+
+
+def kept(q_start, n, kv_len, first):
+    """Rows of the call's tensors that belong to the sequence and their positions."""
+    rows = np.arange(first[0], min(n, max(q_start[1], first[0])))
+    return rows, first[1] + rows - first[0]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("q_start,n,kv_len,first", CUT)
+def test_write_and_read_past_the_table_and_the_tokens(kv, q_start, n, kv_len, first):
+    page = 4096 if kv == "bf16" else 2048
+    with Case("bf16", kv, page, 2, 128, [0], [64], seed=40, extra_blocks=0) as c:
+        assert c.T == 32 and c.full_table.shape[3] == 2
+        c.fill()
+        before, scales = c.pages.clone(), None if c.scales is None else c.scales.clone()
+        k = torch.randn((n, 2, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        v = torch.randn((n, 2, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        b = L.KvBatch(i32(q_start), i32([kv_len]), c.table, n, n)
+        rows, pos = kept(q_start, n, kv_len, first)
+        has = (pos >= 0) & (pos < 64)
+        L.lora_kv_write(c.cache, b, k, v)
+        ko, vo = torch.full_like(k, 9.0), torch.full_like(v, 9.0)
+        L.lora_kv_read(c.cache, b, ko, vo)
+        # the whole cache, the rows' places among it
+        ka, va = torch.empty_like(c.k), torch.empty_like(c.v)
+        L.lora_kv_read(c.cache, L.KvBatch(i32([0, 64]), c.kvl, c.table, 64, 64), ka, va)
+        torch.cuda.synchronize()
+        for new, old, out, whole in ((k, c.k, ko, ka), (v, c.v, vo, va)):
+            stored = (lambda x: torch.from_numpy(dequant(*quant(host(x)))).to(torch.float32).to(x.dtype).cuda()) if c.fp8 \
+                else (lambda x: x)
+            want = stored(old).clone()
+            want[pos[has]] = stored(new)[rows[has]]
+            assert torch.equal(whole, want)
+            kept_rows = torch.zeros(n, dtype=torch.bool)
+            kept_rows[rows[has]] = True
+            assert torch.equal(out[rows[has]], stored(new)[rows[has]])
+            assert torch.all(out[~kept_rows.cuda()] == 9.0)      # rows without a place are left
+        if not has.any():
+            assert torch.equal(c.pages, before) and (scales is None or torch.equal(c.scales, scales))
+
+
+# few rows, tiles of 128 rows, tiles of 256 (a long table, of which one sequence uses the first blocks)
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("group,n,q_start,kv_len", [
+    (1, 1, [0, 1], 129), (4, 4, [0, 4], 130), (2, 6, [0, 8], 131), (2, 5, [-3, 5], 100), (1, 2, [0, 2], 2 ** 31 - 1),
+    (4, 50, [0, 50], 140), (4, 40, [0, 60], 120), (4, 40, [0, 60], 150), (4, 40, [-5, 40], 110), (4, 30, [0, 30], 10 ** 9),
+])
+def test_attend_past_the_table_and_the_tokens(kv, window, group, n, q_start, kv_len):
+    # pages of 40 (FP8: 80) tokens: the table's end lies inside a tile of keys
+    cap = 120 if kv == "bf16" else 160
+    with Case("bf16", kv, 5120, 1, 128, [0], [cap], seed=41, extra_blocks=0) as c:
+        log("[case] past the table %s group %d rows %d %s kv_len %d window %d" % (kv, group, n, q_start, kv_len, window))
+        kd, vd = c.fill()
+        assert c.full_table.shape[3] * c.T == cap
+        q = torch.randn((n, group, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        b = L.KvBatch(i32(q_start), i32([kv_len]), c.table, n, n)
+        out, lse = attend(c, q, 0.1, window, batch=b)
+        torch.cuda.synchronize()
+        pos = kv_len - (q_start[1] - q_start[0]) + (np.arange(n) - q_start[0])
+        see = visible(pos, cap, window)
+        agree(host(out), host(lse), formula(host(q), kd[0], vd[0], see, 0.1), "bf16", 2, "bf16", cap)
+
+
+@pytest.mark.parametrize("kv", ["f16", "fp8"])
+def test_attend_wide_past_the_table(kv):
+    # 8 waves: the first sequence ends inside its table, the second's lengths pass it
+    act, G, n = "f16", 8, [100, 90]
+    with wide_case(act, kv, 4096, 128, 1, G, n, [300, 200], seed=42) as c:
+        nb = c.full_table.shape[3]
+        cap = nb * c.T
+        # the second sequence repeats its blocks over the whole table: the keys are those 200's over and over
+        used = -(-200 // c.T)
+        reps = -(-nb // (used - 1))
+        c.table[1] = c.table[1, :, :, :used - 1].repeat(1, 1, reps)[:, :, :nb]
+        kd, vd = c.fill()
+        lens = [300, cap + 7]
+        b = L.KvBatch(c.q_start, i32(lens), c.table, sum(n), 100)
+        q = torch.randn((sum(n), G, 128), device="cuda", generator=c.gen).to(TD[act])
+        q[100:, :, :] = 0   # all keys alike: the mean of the values
+        out, lse = attend(c, q, 0.1, 0, batch=b)
+        torch.cuda.synchronize()
+        see = visible(300 - 100 + np.arange(100), 300)
+        agree(host(out[:100]), host(lse[:100]), formula(host(q[:100]), kd[0], vd[0], see, 0.1), "f16", 1, act, 300)
+        m = (used - 1) * c.T
+        whole, rest = divmod(cap, m)
+        vs = vd[1][:m, 0]
+        pos = cap + 7 - 90 + np.arange(90)
+        for i in (0, 1, 82, 83, 84, 89):
+            keys = min(pos[i] + 1, cap)
+            whole, rest = divmod(keys, m)
+            want = (whole * vs.sum(0) + vs[:rest].sum(0)) / keys
+            # equal weights are powers of two: only the sums and the output round
+            tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + (keys + 64) * 2.0 ** -24 * np.abs(vs).mean(0)
+            assert np.all(np.abs(host(out[100 + i]) - want) <= tol), i
+            assert np.all(np.abs(host(lse[100 + i]) - np.log(keys)) <= 2.0 ** -21 * np.log(keys) + 2.0 ** -21)
