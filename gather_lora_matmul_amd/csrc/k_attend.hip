@@ -118,7 +118,7 @@ __device__ __forceinline__ void p_operand(const float* p, u32x4& hi, u32x4& lo) 
 // and no others (0 * inf is not 0 in a matrix product).  For tiles that some row
 // does not see whole: v loses them, and for each class (+inf, -inf, NaN) an
 // indicator takes their place in a product with the visibility of the tokens,
-// whose result says which rows get that value.
+// whose result says which rows get that value.  (Tiles seen whole: settle.)
 template <typename T>
 __device__ __forceinline__ uint32_t class_bits(const u32x4& u, int cls) {
   constexpr uint32_t kInf = std::is_same<T, bf16_t>::value ? 0x7f80u : 0x7c00u;
@@ -496,6 +496,72 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 
+// What an infinity or NaN in V does to a row that sees its token: the result's element
+// is that value, whatever its weight (NaN where they differ).  The products of tiles
+// that all rows see whole, and factors that round to 0 later, make NaN of some (0 *
+// inf: of a weight or a second term that has rounded to 0), but never hide one: an
+// element is finite only if all that its row saw of V was.  So the elements of a
+// piece that are not finite are settled after its results are stored, by a look at
+// their column of V: bound by the reads of it, and nothing where all is finite.
+// FP8 has NaN only, and needs none of this.
+template <typename A, int D>
+__device__ __forceinline__ uint32_t seen_classes(const KvView& kv, const int32_t* ktab, const int32_t* vtab,
+                                                 int lo, int hi, int d) {
+  uint32_t found = 0;   // +inf, -inf, NaN
+#pragma unroll 1
+  for (int t = lo & ~7; t <= hi && found < 3; t += 8) {
+    const int b = (int)kv_div(kv, (uint32_t)t);
+    if (b >= kv.nb) break;
+    const int kp = ktab[b], vp = vtab[b];
+    if ((unsigned)kp >= (unsigned)kv.n_pages || (unsigned)vp >= (unsigned)kv.n_pages) continue;
+    const u32x4 u = ldv(kv.pages + (int64_t)vp * kv.page_bytes + ((int64_t)((t - b * kv.T) / 8) * D + d) * 16);
+    const uint32_t see = run_bits<8>(t, lo, hi);
+#pragma unroll
+    for (int cls = 0; cls < 3; ++cls) found |= (class_bits<A>(u, cls) & see) ? 1u << cls : 0u;
+  }
+  return found;
+}
+// The elements of `mask`, of a row that sees the tokens lo .. hi of the piece: element
+// `bit` is number dim(bit) of the head's, which put(d, value) stores.
+template <typename A, int D, typename Mask, typename Dim, typename Put>
+__device__ __forceinline__ void settle(const KvView& kv, const int32_t* ktab, const int32_t* vtab, int lo, int hi,
+                                       Mask mask, Dim dim, Put put) {
+#pragma unroll 1
+  for (; mask; mask &= mask - 1) {
+    const int d = dim(__builtin_ctzll(mask));
+    const uint32_t c = seen_classes<A, D>(kv, ktab, vtab, max(lo, 0), hi, d);
+    if (c) put(d, class_value(c == 1 ? 0 : (c == 2 ? 1 : 2)));
+  }
+}
+// Bits of the values that are not finite.
+template <typename V, int N, int E = sizeof(V) / sizeof(float)>
+__device__ __forceinline__ uint64_t odd_ones(const V (&o)[N]) {
+  uint64_t bits = 0;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < E; ++i) bits |= (uint64_t)!(fabsf(o[n][i]) < INFINITY) << (n * E + i);
+  return bits;
+}
+// NaN if one of the values is not finite, else 0.
+template <typename V, int N, int E = sizeof(V) / sizeof(float)>
+__device__ __forceinline__ float residue(const V (&o)[N]) {
+  float z = 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < E; ++i) z = __builtin_fmaf(o[n][i], 0.f, z);
+  return z;
+}
+// o w of a part, for a weight above 0 that may have rounded to 0: what is not finite stays.
+__device__ __forceinline__ f32x4 weigh(const f32x4& o, float w) {
+  f32x4 x = o * w;
+  if (w == 0.f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fabsf(o[i]) < INFINITY ? 0.f : o[i];
+  return x;
+}
+
 // ---- the joining launch ----------------------------------------------------------
 // RB rows a block: weights of the parts by their maxima, then a
 // weighted sum, D / 4 lanes a part and several parts at a time.  Bound by the reads
@@ -532,7 +598,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
         const float2 ml = parts.ml[at];
         const float w = exp2f(ml.x - Mu);  // an empty part: exp2(-inf) = 0
         sum += w * ml.y;
-        acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
+        acc += weigh(*reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4), w);
       }
 #pragma unroll
     for (int x = LR; x < RW; x <<= 1) {
@@ -626,7 +692,7 @@ __global__ __launch_bounds__(256) void k_attend_join_list(AttendArgs a, int G) {
         const float2 ml = parts.ml[at];
         const float w = exp2f(ml.x - Mu);
         sum += w * ml.y;
-        acc += w * *reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4);
+        acc += weigh(*reinterpret_cast<const f32x4*>(parts.o + at * D + li * 4), w);
       }
     if (P > 1) {
       sh_acc[gi][li] = acc;
@@ -942,6 +1008,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (g == 0) parts.ml[at] = float2{m, l};
         }
       }
+      if constexpr (!Q8) {
+        if (__builtin_expect(__ballot(residue(o) != 0.f) != 0, 0) && col < p.rows && l < INFINITY) {
+          const bool whole = p.begins && p.ends;
+          const int head = p.head * a.group + row - tq * a.group;
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D;
+          float* part = parts.o + (((int64_t)c.block * 2 + slot) * TR + col) * D;
+          settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), whole && l == 0.f ? 0 : odd_ones(o),
+                       [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); },
+                       [&](int d, float x) {
+                         if (whole) out[d] = (uint16_t)pack2<A>(x, x);
+                         else part[d] = x;
+                       });
+        }
+      }
       if (n_piece == 0 && speaker) describe(desc, c, &p);
       ++n_piece;
       continue;
@@ -983,6 +1063,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int64_t at = ((int64_t)c.block * 2 + slot) * TR + r;
         *reinterpret_cast<f32x4*>(parts.o + at * D + d) = acc;
         if (d == 0) parts.ml[at] = float2{M, sum};
+      }
+      if constexpr (!Q8) {
+        const f32x4 got[1] = {acc};
+        if (__builtin_expect(residue(got) != 0.f, 0) && sum < INFINITY) {
+          const int rr = p.row0 + r, t = token_of(a, rr), head = p.head * a.group + rr - t * a.group;
+          const int at = p.q.base + t;
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + t) * a.out_ld + (int64_t)head * D;
+          float* part = parts.o + (((int64_t)c.block * 2 + slot) * TR + r) * D;
+          settle<A, D>(kv, ktab, vtab, max(at - win + 1, p.key0), min(at, p.key1 - 1), odd_ones(got),
+                       [&](int bit) { return d + bit; },
+                       [&](int e, float x) {
+                         if (whole) out[e] = (uint16_t)pack2<A>(x, x);
+                         else part[e] = x;
+                       });
+        }
       }
     }
     if (n_piece == 0 && speaker) describe(desc, c, &p);
@@ -1555,6 +1650,19 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
             *reinterpret_cast<f32x4*>(parts.o + at * D + n * 32 + b * 8 + hi * 4) =
                 f32x4{o[n][4 * b] * up, o[n][4 * b + 1] * up, o[n][4 * b + 2] * up, o[n][4 * b + 3] * up};
         if (hi == 0) parts.ml[at] = float2{m, l};
+      }
+    }
+    if constexpr (!Q8) {
+      if (__builtin_expect(__ballot(residue(o) != 0.f) != 0, 0) && col < wrows && l < INFINITY) {
+        const int head = p.head * a.group + row - tq * a.group;
+        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D;
+        float* part = parts.o + (((int64_t)c.block * 2 + (n_piece == 0 ? 0 : 1)) * TR + wave * 32 + col) * D;
+        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), whole && l == 0.f ? 0 : odd_ones(o),
+                     [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); },
+                     [&](int d, float x) {
+                       if (whole) out[d] = (uint16_t)pack2<A>(x, x);
+                       else part[d] = x;
+                     });
       }
     }
     if (p.first >= 0) {

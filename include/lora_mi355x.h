@@ -489,7 +489,9 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11): where there
  * are 512 rows a head and sequence on average, and full tables (or the window) would
  * give every compute unit 24 tiles of 256 rows and 64 keys.  One rounding at the store.  A token that sees none gets zeros.  What is
- * not seen has no influence, whatever it holds.  lse (optional, NULL)
+ * not seen has no influence, whatever it holds; a value of v that is not finite is that
+ * element's result in every row that sees its token, at any weight (NaN where several
+ * differ).  lse (optional, NULL)
  * [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j), -inf for none.  Rows
  * of out that belong to no sequence are not written.  LORA_E_UNSUPPORTED for
  * calls that could need 2^31 units of work (a tile of rows with 64 keys, if every

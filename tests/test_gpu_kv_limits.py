@@ -221,3 +221,92 @@ def test_attend_wide_past_the_table(kv):
             tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + (keys + 64) * 2.0 ** -24 * np.abs(vs).mean(0)
             assert np.all(np.abs(host(out[100 + i]) - want) <= tol), i
             assert np.all(np.abs(host(lse[100 + i]) - np.log(keys)) <= 2.0 ** -21 * np.log(keys) + 2.0 ** -21)
+
+
+# ---------------------------------------------------------------------------------------------
+# infinities in V, wherever their token lies
+# ---------------------------------------------------------------------------------------------
+def rewrite(c):
+    """The cache again from c.k, c.v; the dense copies of one sequence with it."""
+    m = c.kv_len[0]
+    L.lora_kv_write(c.cache, L.KvBatch(i32([0, m]), c.kvl, torch.from_numpy(c.full_table).cuda(), m, m), c.k, c.v)
+    c.kd, c.vd = [host(c.k)], [host(c.v)]
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("H,G,n", [(1, 1, 1), (1, 4, 4), (2, 2, 40), (600, 1, 1)])
+@pytest.mark.parametrize("window", [0, 130])
+def test_infinite_values_far_from_every_edge(act, H, G, n, window):
+    # tokens that every row sees, in tiles of keys that every row sees whole; weights down to 2^-40
+    many = H > 256   # sequences instead of heads: waves that work for themselves
+    S, H = (H, 1) if many else (1, H)
+    m = 150
+    with Case(act, act, 4096, H, 128, [n] * S, [m] * S, seed=43, extra_blocks=0) as c:
+        c.fill()
+        c.k[:, :, 0] = -4.0 * torch.rand(c.k.shape[:2], device="cuda", generator=c.gen).to(c.k.dtype)
+        c.k[m - 1::m, :, 0] = 0                       # the last token has the largest weight
+        for s in range(S):
+            at = s * m
+            c.v[at + 70, 0, 3] = float("inf")
+            c.v[at + 71, 0, 4] = -float("inf")
+            c.v[at + 40, 0, 5] = float("inf")
+            c.v[at + 90, 0, 5] = -float("inf")        # both: NaN
+            c.v[at + 60, 0, 6] = float("nan")
+        starts = np.arange(S + 1) * m
+        L.lora_kv_write(c.cache, L.KvBatch(i32(starts), c.kvl, torch.from_numpy(c.full_table).cuda(), S * m, m), c.k, c.v)
+        q = torch.randn((c.n, H * G, 128), device="cuda", generator=c.gen).to(TD[act])
+        q[:, :, 0] = 70.0
+        out, lse = attend(c, q, 0.1, window)
+        torch.cuda.synchronize()
+        few = n * G <= 16
+        for s in (range(S) if S < 3 else (0, 1, S // 2, S - 1)):
+            r = slice(s * n, s * n + n)
+            kd, vd = host(c.k[s * m:s * m + m]), host(c.v[s * m:s * m + m])
+            see = visible(m - n + np.arange(n), m, window)
+            agree(host(out[r]), host(lse[r]), formula(host(q[r]), kd, vd, see, 0.1), act, 2 if few else 1, act, m)
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_infinite_values_of_small_weights_in_long_caches(act, n):
+    # the weight of the infinite value is 2^-15 .. 2^-300 of the largest, which comes before it or
+    # long after it (other tiles, other blocks' parts): any weight above zero times infinity is infinite
+    m = 9000
+    for first in (False, True):
+        with Case(act, act, 8192, 1, 128, [n], [m], seed=44, extra_blocks=0) as c:
+            c.fill()
+            for drop in (15, 30, 140, 300):
+                c.k[:] = 0
+                top = 100 if first else m - 500
+                c.k[top, 0, 0] = 8.0
+                at = 5000 if first else 1000
+                c.v[:] = torch.randn(c.v.shape, device="cuda", generator=c.gen).to(c.v.dtype)
+                c.v[at, 0, 3] = float("inf")
+                c.v[at + 1, 0, 7] = -float("inf")
+                rewrite(c)
+                q = torch.zeros((n, 2, 128), device="cuda", dtype=TD[act])
+                q[:, :, 0] = drop / 8.0
+                out, lse = attend(c, q, float(np.log(2.0)))
+                torch.cuda.synchronize()
+                see = visible(m - n + np.arange(n), m)
+                agree(host(out), host(lse), formula(host(q), c.kd[0], c.vd[0], see, float(np.float32(np.log(2.0)))), act,
+                      2 if 2 * n <= 16 else 1, act, m, "drop %d" % drop)
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+def test_wide_infinite_values_far_from_every_edge(act):
+    n, lens = [90, 70], [700, 500]
+    with wide_case(act, act, 4096, 128, 1, 8, n, lens, seed=45) as c:
+        c.fill()
+        c.k[:, :, 0] = -4.0 * torch.rand(c.k.shape[:2], device="cuda", generator=c.gen).to(c.k.dtype)
+        for at, d, x in ((70, 3, "inf"), (330, 4, "-inf"), (200, 5, "inf"), (400, 5, "-inf"), (250, 6, "nan"),
+                         (700 + 100, 3, "-inf")):
+            c.v[at, 0, d] = float(x)
+        L.lora_kv_write(c.cache, L.KvBatch(i32([0, 700, 1200]), c.kvl, torch.from_numpy(c.full_table).cuda(), 1200, 700), c.k, c.v)
+        q = torch.randn((c.n, 8, 128), device="cuda", generator=c.gen).to(TD[act])
+        q[:, :, 0] = 70.0
+        out, lse = attend(c, q, 0.1)
+        torch.cuda.synchronize()
+        for s, (r, k) in enumerate(((slice(0, 90), slice(0, 700)), (slice(90, 160), slice(700, 1200)))):
+            see = visible(lens[s] - n[s] + np.arange(n[s]), lens[s])
+            agree(host(out[r]), host(lse[r]), formula(host(q[r]), host(c.k[k]), host(c.v[k]), see, 0.1), act, 1, act, lens[s])
