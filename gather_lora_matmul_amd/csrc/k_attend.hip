@@ -102,6 +102,15 @@ __device__ __forceinline__ u32x4 keep8(u32x4 u, uint32_t bits) {
 // 2^-16 of bf16, 2^-22 of f16): the results' error is that of fp32 weights.  Only the
 // tiles of 256 rows, bound by the matrix cores, take the first term alone.  The sums
 // take P unrounded: lse is an fp32 result.
+//   f16 has no numbers between 0 and 2^-24, and many small weights may be what a row's
+// result is made of.  There P is 2^7 exp(s - m): with a maximum that P passes by 2^8
+// at most it stays below 2^15, and is off by 2^-32 of a weight 1 at most, whatever its
+// size.  m - 7 takes the maximum's place in the exponent and in what is stored.
+template <typename T>
+__device__ __forceinline__ float origin(float m) {
+  const float x = m == -INFINITY ? 0.f : m;
+  return std::is_same<T, f16_t>::value ? x - 7.f : x;
+}
 template <typename T>
 __device__ __forceinline__ void p_operand(const float* p, u32x4& hi, u32x4& lo) {
   uint32_t h[4], l[4];
@@ -950,7 +959,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         for (int n = 0; n < ND; ++n) o[n] *= f;
         m = mn;
       }
-      const float mu = safe_max(m);
+      const float mu = origin<PT>(m);
       float pr[4 * NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -987,6 +996,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    if (std::is_same<PT, f16_t>::value) m -= 7.f;   // the exponents' origin
     if constexpr (SOLO) {
       const int slot = n_piece == 0 ? 0 : 1;
       if (col < p.rows) {
@@ -1445,7 +1455,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
         for (int n = 0; n < ND; ++n) o[n] *= f;
         m = mn;
       }
-      return safe_max(m);
+      return origin<A>(m);
     };
     // the loads have arrived, of every wave (a barrier alone does not wait for loads
     // that go to LDS), and what the next ones will overwrite is read
@@ -1623,6 +1633,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
+    if (std::is_same<A, f16_t>::value) m -= 7.f;   // the exponents' origin
     const bool whole = p.begins && p.ends;
     if (col < wrows) {
       if (whole) {

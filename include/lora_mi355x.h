@@ -486,7 +486,8 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  *   out_i = sum_j p_ij v_j,  p_i. = softmax of scale * q_i . k_j over those j
  * with fp32 scores, maxima and sums.  For the products with v, p goes in two 16-bit
  * terms (relative 2^-16 of bf16, 2^-22 of f16; bf16 for FP8 caches in calls of at
- * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11): where there
+ * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11; of f16 a weight
+ * of any size is off by 2^-32 of the largest more at most): where there
  * are 512 rows a head and sequence on average, and full tables (or the window) would
  * give every compute unit 24 tiles of 256 rows and 64 keys.  One rounding at the store.  A token that sees none gets zeros.  What is
  * not seen has no influence, whatever it holds; a value of v that is not finite is that

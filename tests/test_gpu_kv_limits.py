@@ -310,3 +310,35 @@ def test_wide_infinite_values_far_from_every_edge(act):
         for s, (r, k) in enumerate(((slice(0, 90), slice(0, 700)), (slice(90, 160), slice(700, 1200)))):
             see = visible(lens[s] - n[s] + np.arange(n[s]), lens[s])
             agree(host(out[r]), host(lse[r]), formula(host(q[r]), host(c.k[k]), host(c.v[k]), see, 0.1), act, 1, act, lens[s])
+
+
+# ---------------------------------------------------------------------------------------------
+# weights of every size
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("S,n", [(1024, 1), (512, 17), (32, 512)])   # few rows, tiles of 128 and of 256 rows
+@pytest.mark.parametrize("exponent", [-20, -26])
+def test_many_small_weights_beside_a_large_one(act, S, n, exponent):
+    # one key of weight 1 and 16000 of about 2^-20 or 2^-26, whose values are all that is left in half of
+    # the elements; many sequences over the same pages, so that a worker walks many keys in one piece
+    m = 16000
+    with Case(act, act, 8192, 1, 128, [1], [m], seed=46, extra_blocks=0) as c:
+        log("[case] small weights %s %d x %d, 2^%d" % (act, S, n, exponent))
+        c.fill()
+        c.k[:] = 0
+        c.k[:, 0, 0] = (1 + 0.05 * torch.rand(m, device="cuda", generator=c.gen)).to(c.k.dtype)
+        c.v[:] = (1 + torch.rand(c.v.shape, device="cuda", generator=c.gen)).to(c.v.dtype)
+        c.k[7, 0, 0] = 0
+        c.v[7, 0, :64] = 0
+        L.lora_kv_write(c.cache, L.KvBatch(i32([0, m]), c.kvl, c.table, m, m), c.k, c.v)
+        q = torch.zeros((S * n, 1, 128), device="cuda", dtype=TD[act])
+        q[:, 0, 0] = float(exponent)
+        scale = float(np.float32(np.log(2.0)))
+        b = L.KvBatch(i32(np.arange(S + 1) * n), i32([m] * S), c.table.repeat(S, 1, 1, 1), S * n, n)
+        out, lse = attend(c, q, scale, batch=b)
+        torch.cuda.synchronize()
+        rows = np.unique([0, n // 2, n - 1])
+        see = visible(m - n + rows, m)
+        want = formula(host(q)[rows], host(c.k), host(c.v), see, scale)
+        for s in (0, 1, S // 2, S - 1):
+            agree(host(out)[s * n + rows], host(lse)[s * n + rows], want, act, 2 if n < 512 else 1, act, m, "sequence %d" % s)
