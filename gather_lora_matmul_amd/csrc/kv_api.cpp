@@ -151,6 +151,9 @@ lora_status lora_kv_read(const lora_pool* p, const lora_kv_desc* d, const lora_k
   return kv_copy(p, d, b, k_dev, v_dev, ld, false, stream);
 }
 
+// What chooses among the kernels: a length of none is as wrong as any other, where there are tokens.
+static int32_t longest(const lora_kv_batch* b) { return b->max_q_len < 1 ? 1 : b->max_q_len; }
+
 static lora_status check_heads(const lora_kv_desc* d, int32_t n_q_heads, const lora_kv_batch* b) {
   if (n_q_heads < d->n_kv_heads || n_q_heads % d->n_kv_heads)
     return fail(LORA_E_ARG, "n_q_heads %d is no multiple of n_kv_heads %d", n_q_heads, d->n_kv_heads);
@@ -168,7 +171,7 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* p, const lora_kv_desc
   LORA_TRY(batch_sizes(b, T));
   if (!bytes) return fail(LORA_E_ARG, "null size");
   LORA_TRY(check_heads(d, n_q_heads, b));
-  *bytes = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len, b->n_seqs,
+  *bytes = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, longest(b), b->n_seqs,
                             d->n_kv_heads);
   return LORA_OK;
 }
@@ -185,14 +188,14 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   if (!(scale > 0.f) || !std::isfinite(scale * 2.8853900817779268f))   // (f16 over FP8 doubles it)
     return fail(LORA_E_ARG, "scale must be positive and finite");
   if (window < 0) return fail(LORA_E_ARG, "negative window");
-  if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_q_len == 0) return LORA_OK;
-  if (attend_units(a.kv, n_q_heads / d->n_kv_heads, b->max_q_len) > INT32_MAX)
+  if (b->n_seqs == 0 || b->n_tokens == 0) return LORA_OK;
+  if (attend_units(a.kv, n_q_heads / d->n_kv_heads, longest(b)) > INT32_MAX)
     return fail(LORA_E_UNSUPPORTED, "more than 2^31 units of work: split the call's tokens");
   const int64_t row = (int64_t)n_q_heads * d->head_dim;
   LORA_TRY(check_rows(q_dev, q_ld, row, "q"));
   LORA_TRY(check_rows(out_dev, out_ld, row, "out"));
   if ((uintptr_t)lse_dev & 3u) return fail(LORA_E_ARG, "lse not 4-byte aligned");
-  const size_t need = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, b->max_q_len, b->n_seqs,
+  const size_t need = attend_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, longest(b), b->n_seqs,
                                        d->n_kv_heads);
   if (!workspace_dev || ws_bytes < need)
     return fail(LORA_E_ARG, "workspace of %zu bytes, this call needs %zu (lora_kv_attend_workspace_size)",
@@ -207,7 +210,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   a.n_q_heads = n_q_heads;
   a.group = n_q_heads / d->n_kv_heads;
   div_init(a.group < 2 ? 2 : a.group, a.group_m, a.group_s);
-  a.max_q_len = b->max_q_len;
+  a.max_q_len = longest(b);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window > (1 << 28) ? 0 : window;   // no position is farther back; keeps differences in 32 bits
   a.ws = (char*)workspace_dev;

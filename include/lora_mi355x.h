@@ -440,8 +440,8 @@ typedef struct {
  * they follow kv_len and q_start as given, a negative kv_len as 0), and tokens whose
  * K or V page id lies outside [0, n_pages) (e.g. -1: given back, or never there) are
  * absent.
- * max_q_len: the longest q_len (it chooses among kernels; a wrong one changes no
- * more than the rounding and the time). */
+ * max_q_len: the longest q_len (it chooses among kernels; a wrong one, 0 too, changes
+ * no more than the rounding and the time). */
 typedef struct {
   int32_t n_seqs;          /* 0..1024                                            */
   int32_t n_tokens;        /* rows of the new tensors, 0..2^24                   */

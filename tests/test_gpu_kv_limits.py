@@ -342,3 +342,16 @@ def test_many_small_weights_beside_a_large_one(act, S, n, exponent):
         want = formula(host(q)[rows], host(c.k), host(c.v), see, scale)
         for s in (0, 1, S // 2, S - 1):
             agree(host(out)[s * n + rows], host(lse)[s * n + rows], want, act, 2 if n < 512 else 1, act, m, "sequence %d" % s)
+
+
+@pytest.mark.parametrize("group", [1, 32])
+def test_a_longest_length_of_none_is_only_a_wrong_one(group):
+    # max_q_len chooses among kernels: with none given the rows are computed all the same
+    with Case("bf16", "bf16", 4096, 1, 128, [3, 1], [70, 33], seed=49) as c:
+        kd, vd = c.fill()
+        q = torch.randn((4, group, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        out, lse = attend(c, q, 0.1, batch=c.batch(max_q=0))
+        torch.cuda.synchronize()
+        for s, (r, n, m) in enumerate(((slice(0, 3), 3, 70), (slice(3, 4), 1, 33))):
+            see = visible(m - n + np.arange(n), m)
+            agree(host(out[r]), host(lse[r]), formula(host(q[r]), kd[s], vd[s], see, 0.1), "bf16", 2, "bf16", m)
