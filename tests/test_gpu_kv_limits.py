@@ -355,3 +355,40 @@ def test_a_longest_length_of_none_is_only_a_wrong_one(group):
         for s, (r, n, m) in enumerate(((slice(0, 3), 3, 70), (slice(3, 4), 1, 33))):
             see = visible(m - n + np.arange(n), m)
             agree(host(out[r]), host(lse[r]), formula(host(q[r]), kd[s], vd[s], see, 0.1), "bf16", 2, "bf16", m)
+
+
+# ---------------------------------------------------------------------------------------------
+# tiles that go out whole
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("act,kv", [("bf16", "bf16"), ("f16", "fp8")])
+@pytest.mark.parametrize("rows,S,H,G,n,length", [(128, 35, 5, 4, 96, 1000), (256, 22, 5, 4, 150, 1800)])
+def test_whole_rounds_of_tiles_and_a_cut_rest(act, kv, rows, S, H, G, n, length):
+    # tiles about equally long, more than the workers are: whole rounds of them, then the others cut into ranges
+    # from the middle of a sequence's tiles on
+    q_len, kv_len = [n - (s % 3 == 1) for s in range(S)], [length + 7 * (s % 4) for s in range(S)]
+    with Case(act, kv, 8192, H, 128, q_len, kv_len, seed=51, extra_blocks=0) as c:
+        workers = torch.cuda.get_device_properties(0).multi_processor_count * (512 // rows) // 2
+        tiles = [-(-x * G // rows) for x in q_len]
+        # units of 64 keys of each tile, to its last row's position
+        units = [sum(-(-(m - x + (min((t + 1) * rows, x * G) - 1) // G + 1) // 64) for t in range(k))
+                 for x, m, k in zip(q_len, kv_len, tiles)]
+        T, longest = sum(tiles) * H, max(-(-m // 64) for m in kv_len)
+        whole = T // workers * workers
+        if whole == 0 or whole == T:
+            pytest.skip("made for 256 compute units")
+        assert S <= 64 and 8 * T * longest <= 9 * sum(units) * H          # the rule of whole tiles
+        assert (256 if sum(q_len) * G >= 512 * S else 128) == rows
+        first = int(np.searchsorted(np.cumsum(tiles) * H, whole, side="right"))   # sequence of the first cut tile
+        assert (whole - sum(tiles[:first]) * H) % tiles[first]
+        kd, vd = c.fill()
+        q = torch.randn((c.n, H * G, 128), device="cuda", generator=c.gen).to(TD[act])
+        out, lse = attend(c, q, 0.1)
+        again = attend(c, q, 0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+        off = np.concatenate([[0], np.cumsum(q_len)])
+        for s in sorted({0, first - 1, first, S - 1}):
+            r = np.arange(off[s], off[s + 1])[[0, 1, 31, 32, 63, 64, -2, -1]]
+            see = visible(kv_len[s] - q_len[s] + r - off[s], kv_len[s])
+            agree(host(out)[r], host(lse)[r], formula(host(q)[r], kd[s], vd[s], see, 0.1), act, 2 if rows == 128 else 1,
+                  act, kv_len[s], "sequence %d" % s)
