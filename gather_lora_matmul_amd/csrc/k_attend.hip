@@ -1229,8 +1229,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   constexpr int KL = D / E;                 // wave loads of K (and of V) of a tile
   constexpr int LPW = KL / NW;              // ... of a wave
   static_assert(KL % NW == 0, "loads divide over the waves");
-  // f16 over FP8: values at half their size, so that 448 * 2^8 fits; made good in
-  // the score's scale and in the output
+  // f16 over FP8: values at half their size, so that the 65536 = 256 * 2^8 that codes of f16
+  // rows may stand for fits; made good in the score's scale and in the output.  Halves of
+  // less than 2^-14 are f16's subnormals: codes of rows whose largest value is below
+  // 2^-6 may lose their last bits, 2^-24 at most, which is f16's own step there.
   constexpr int DOWN = Q8 && std::is_same<A, f16_t>::value ? 1 : 0;
   extern __shared__ __align__(16) char smem[];
   typename TT::Shared& sh = *reinterpret_cast<typename TT::Shared*>(smem);

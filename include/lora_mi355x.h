@@ -426,8 +426,10 @@ typedef struct {
   int32_t dtype;           /* lora_dtype of the cached elements                  */
   uint8_t* scales_dev;     /* FP8: [n_pages][T] exponent bytes by page id and
                               token slot (16-byte aligned, caller-owned); a
-                              code c of slot t stands for c * 2^(byte - 127).
-                              NULL otherwise                                     */
+                              code c of slot t stands for c * 2^(byte - 127),
+                              bytes 1 to 254 (f16 activations: to 135, and values
+                              up to 131008, which lora_kv_write keeps to: beyond
+                              them lora_kv_attend is not defined).  NULL otherwise */
 } lora_kv_desc;
 
 /* The sequences of one call.  Sequence s has q_start[s + 1] - q_start[s] new
@@ -487,7 +489,8 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * with fp32 scores, maxima and sums.  For the products with v, p goes in two 16-bit
  * terms (relative 2^-16 of bf16, 2^-22 of f16; bf16 for FP8 caches in calls of at
  * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11; of f16 a weight
- * of any size is off by 2^-32 of the largest more at most): where there
+ * of any size is off by 2^-32 of the largest more at most; with
+ * f16 activations and more than 32 rows a head FP8 values are off by 2^-24 at most): where there
  * are 512 rows a head and sequence on average, and full tables (or the window) would
  * give every compute unit 24 tiles of 256 rows and 64 keys.  One rounding at the store.  A token that sees none gets zeros.  What is
  * not seen has no influence, whatever it holds; a value of v that is not finite is that

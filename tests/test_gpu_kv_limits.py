@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
 
 import gather_lora_matmul_amd as L
 from gpu_helpers import log
-from kv_formula import agree, bound, formula, visible
+from kv_formula import UNIT, agree, bound, formula, visible
 from test_gpu_kv import TD, Case, attend, dequant, quant, wide_case
 
 
@@ -392,3 +392,34 @@ def test_whole_rounds_of_tiles_and_a_cut_rest(act, kv, rows, S, H, G, n, length)
             see = visible(kv_len[s] - q_len[s] + r - off[s], kv_len[s])
             agree(host(out)[r], host(lse)[r], formula(host(q)[r], kd[s], vd[s], see, 0.1), act, 2 if rows == 128 else 1,
                   act, kv_len[s], "sequence %d" % s)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("size", [65504.0, 63488.0, 2.0 ** -8, 2.0 ** -14, 2.0 ** -20])
+def test_fp8_caches_of_f16_rows_of_every_size(n, size):
+    # rows from f16's smallest numbers to its largest, whose codes may stand for 65536 (past f16).  In tiles
+    # K and V are f16 numbers at half their size: off by 2^-24 at most
+    m = 200
+    with Case("f16", "fp8", 4096, 1, 128, [n], [m], seed=50) as c:
+        c.fill()
+        g = lambda: torch.empty((m, 1, 128), device="cuda").uniform_(-1, 1, generator=c.gen)
+        for k_size in (1.0, size):
+            c.k = (g() * k_size).to(torch.float16)
+            c.v = (g() * size).to(torch.float16)
+            c.v[:, 0, 5] = size
+            L.lora_kv_write(c.cache, L.KvBatch(i32([0, m]), c.kvl, torch.from_numpy(c.full_table).cuda(), m, m), c.k, c.v)
+            kd, vd = dequant(*quant(host(c.k))), dequant(*quant(host(c.v)))
+            q = torch.empty((n, 2, 128), device="cuda").uniform_(-1, 1, generator=c.gen).to(torch.float16)
+            scale = 0.2 / k_size
+            out, lse = attend(c, q, scale)
+            torch.cuda.synchronize()
+            see = visible(m - n + np.arange(n), m)
+            out_, lse_, sz, al, err = formula(host(q), kd, vd, see, scale)
+            p_type, terms = ("bf16", 2) if n == 1 else ("f16", 1)
+            if n > 1:
+                err = err + scale * 2.0 ** -24 * np.abs(host(q)).sum(-1)
+                sz = sz + 2.0 ** -24 / UNIT["f16"]      # of V, whole: u of this is 2^-24
+            big = np.abs(out_) > 65504                     # rounds to infinity
+            o = np.where(big & np.isinf(host(out)), out_, host(out))
+            assert np.isinf(host(out)[np.abs(out_) >= 65520 * (1 + 2.0 ** -10)]).all()
+            agree(o, host(lse), (out_, lse_, sz, al, err), p_type, terms, "f16", m, "size %g k %g" % (size, k_size))
