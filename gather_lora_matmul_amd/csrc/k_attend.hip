@@ -29,6 +29,7 @@
 
 #include "kcommon.h"
 #include "kv.h"
+#include "per_device.h"
 
 namespace lora {
 
@@ -1725,9 +1726,15 @@ template <typename A, typename KV, int D, int NW>
 hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
   using TT = Tiles<A, KV, D, NW>;
   const size_t lds = sizeof(typename TT::Shared);
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D, NW>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (attr != hipSuccess) return attr;
+  static PerDevice limit;   // the kernel's LDS, more than a block gets unasked, is a setting of each device
+  int device = -1;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess)
+    e = limit.done(device, [&] {
+      return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D, NW>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    });
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW>), dim3(G), dim3(NW * 64), lds, s, a);
   // tiles of which none has many parts: four blocks each; else the list.  Measured
   // (us of a call, list / this): 32 sequences of 5 x 8 rows 86.7 / 84.6, 2 of 256 x
