@@ -24,6 +24,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -76,12 +77,37 @@ def algorithmic_bytes(wl, ids: np.ndarray, slices, elt_y: int, shared_x: bool = 
     return total
 
 
-def source_hash(files) -> str:
+def kernel_header(sources: str, header: str) -> str:
+    """The parts of the public header's text that the kernels' sources can depend on:
+    its constants and types, where the sources name them or one of their
+    enumerators.  Comments, prototypes and other entry points' types cannot change
+    a kernel."""
+    text = re.sub(r"/\*.*?\*/|//[^\n]*", " ", header, flags=re.S)
+    names = set(re.findall(r"\w+", re.sub(r"/\*.*?\*/|//[^\n]*", " ", sources, flags=re.S)))
+    parts = []
+    for line in re.findall(r"^[ \t]*#define[ \t]+\w+[ \t]+\S.*$", text, flags=re.M):
+        if line.split()[1] in names:
+            parts.append(" ".join(line.split()))
+    for body, name in re.findall(r"typedef\s+((?:struct|enum)\s*\w*\s*\{.*?\})\s*(\w+)\s*;", text, flags=re.S):
+        enumerators = re.findall(r"(\w+)\s*=", body) if body.startswith("enum") else []
+        if names & {name, *enumerators}:
+            parts.append(" ".join((body + name).split()))
+    return "\n".join(parts)
+
+
+def source_hash(files, header: str = None) -> str:
+    """Of the sources' bytes and what they take from the public header (or from `header`'s text)."""
     h = hashlib.sha256()
-    paths = [os.path.join(CSRC, f) for f in files] + [os.path.join(ROOT, "include", "lora_mi355x.h")]
-    for path in paths:
-        with open(path, "rb") as fh:
-            h.update(os.path.basename(path).encode() + fh.read())
+    sources = b""
+    for f in files:
+        with open(os.path.join(CSRC, f), "rb") as fh:
+            text = fh.read()
+        sources += text
+        h.update(f.encode() + text)
+    if header is None:
+        with open(os.path.join(ROOT, "include", "lora_mi355x.h")) as fh:
+            header = fh.read()
+    h.update(kernel_header(sources.decode(), header).encode())
     return h.hexdigest()[:16]
 
 
