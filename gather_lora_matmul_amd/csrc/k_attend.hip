@@ -511,57 +511,105 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f
 // that all rows see whole, and factors that round to 0 later, make NaN of some (0 *
 // inf: of a weight or a second term that has rounded to 0), but never hide one: an
 // element is finite only if all that its row saw of V was.  So the elements of a
-// piece that are not finite are settled after its results are stored, by a look at
-// their column of V: bound by the reads of it, and nothing where all is finite.
-// FP8 has NaN only, and needs none of this.
-template <typename A, int D>
-__device__ __forceinline__ uint32_t seen_classes(const KvView& kv, const int32_t* ktab, const int32_t* vtab,
-                                                 int lo, int hi, int d) {
-  uint32_t found = 0;   // +inf, -inf, NaN
-#pragma unroll 1
-  for (int t = lo & ~7; t <= hi && found < 3; t += 8) {
-    const int b = (int)kv_div(kv, (uint32_t)t);
-    if (b >= kv.nb) break;
-    const int kp = ktab[b], vp = vtab[b];
-    if ((unsigned)kp >= (unsigned)kv.n_pages || (unsigned)vp >= (unsigned)kv.n_pages) continue;
-    const u32x4 u = ldv(kv.pages + (int64_t)vp * kv.page_bytes + ((int64_t)((t - b * kv.T) / 8) * D + d) * 16);
-    const uint32_t see = run_bits<8>(t, lo, hi);
+// piece that are not finite are settled at its end by a look at their column of V,
+// and where all is finite nothing is looked at.  FP8 has NaN only, and needs none of this.
+template <typename A>
+__device__ __forceinline__ uint32_t classes_of(const u32x4& u, uint32_t see) {   // bits: +inf, -inf, NaN
+  uint32_t found = 0;
 #pragma unroll
-    for (int cls = 0; cls < 3; ++cls) found |= (class_bits<A>(u, cls) & see) ? 1u << cls : 0u;
-  }
+  for (int cls = 0; cls < 3; ++cls) found |= (class_bits<A>(u, cls) & see) ? 1u << cls : 0u;
   return found;
 }
-// The elements of `mask`, of a row that sees the tokens lo .. hi of the piece: element
-// `bit` is number dim(bit) of the head's, which put(d, value) stores.
-template <typename A, int D, typename Mask, typename Dim, typename Put>
-__device__ __forceinline__ void settle(const KvView& kv, const int32_t* ktab, const int32_t* vtab, int lo, int hi,
-                                       Mask mask, Dim dim, Put put) {
-#pragma unroll 1
-  for (; mask; mask &= mask - 1) {
-    const int d = dim(__builtin_ctzll(mask));
-    const uint32_t c = seen_classes<A, D>(kv, ktab, vtab, max(lo, 0), hi, d);
-    if (c) put(d, class_value(c == 1 ? 0 : (c == 2 ? 1 : 2)));
-  }
+// Eight tokens' values of the head's first element, from token t on (a multiple of 8), and
+// which of them lie in [lo, hi] and have pages.
+__device__ __forceinline__ const char* eight_values(const KvView& kv, const int32_t* ktab, const int32_t* vtab, int D,
+                                                    int t, int lo, int hi, uint32_t& see) {
+  const int b = (int)kv_div(kv, (uint32_t)t);
+  const bool in = t <= hi && b < kv.nb;
+  const int kp = in ? ktab[b] : -1, vp = in ? vtab[b] : -1;
+  const bool ok = (unsigned)kp < (unsigned)kv.n_pages && (unsigned)vp < (unsigned)kv.n_pages;
+  see = ok ? run_bits<8>(t, lo, hi) : 0u;
+  return kv.pages + (int64_t)(ok ? vp : 0) * kv.page_bytes + (int64_t)(ok ? (t - b * kv.T) / 8 : 0) * D * 16;
 }
-// Bits of the values that are not finite.
-template <typename V, int N, int E = sizeof(V) / sizeof(float)>
-__device__ __forceinline__ uint64_t odd_ones(const V (&o)[N]) {
-  uint64_t bits = 0;
+// The wave's results o of rows that see the tokens lo .. hi of a piece's keys each and
+// [all_lo, all_hi] in common (the same in all lanes): element i of o[n] is number
+// dim(n E + i) of the head's.  Only lanes with `mine` are settled (a row whose scores are
+// not finite is NaN).  The common tokens are walked once, all columns at a
+// time; the few others of a row (as many as the wave's rows are apart) by its lanes.
+template <typename A, int D, typename V, int N, typename Dim>
+__device__ __forceinline__ void settle(const KvView& kv, const int32_t* ktab, const int32_t* vtab, int lo, int hi,
+                                       int all_lo, int all_hi, bool mine, V (&o)[N], Dim dim) {
+  constexpr int E = sizeof(V) / sizeof(float), C = D / 64, U = 4;
+  const int lane = threadIdx.x & 63;
+  uint32_t found[C] = {};
+#pragma unroll 1
+  for (int t0 = all_lo & ~7; t0 <= all_hi; t0 += 8 * U) {
+    u32x4 u[U][C];
+    uint32_t see[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const char* src = eight_values(kv, ktab, vtab, D, t0 + 8 * j, all_lo, all_hi, see[j]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) u[j][c] = ldv(src + (c * 64 + lane) * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) found[c] |= classes_of<A>(u[j][c], see[j]);
+  }
+  unsigned long long column[3][C];   // of all columns, in every lane
+#pragma unroll
+  for (int cls = 0; cls < 3; ++cls)
+#pragma unroll
+    for (int c = 0; c < C; ++c) column[cls][c] = __ballot((found[c] >> cls) & 1u);
+  const bool common = all_lo <= all_hi;
+  uint64_t odd = 0, is[3] = {};
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 0; i < E; ++i) bits |= (uint64_t)!(fabsf(o[n][i]) < INFINITY) << (n * E + i);
-  return bits;
+    for (int i = 0; i < E; ++i) odd |= (uint64_t)(mine && !(fabsf(o[n][i]) < INFINITY)) << (n * E + i);
+#pragma unroll 1
+  for (uint64_t left = odd; left; left &= left - 1) {
+    const int bit = __builtin_ctzll(left), d = dim(bit);
+    uint32_t f = 0;
+#pragma unroll
+    for (int cls = 0; cls < 3; ++cls) {
+      unsigned long long w = column[cls][0];
+      if (C > 1 && d >= 64) w = column[cls][C - 1];
+      f |= (uint32_t)((w >> (d & 63)) & 1u) << cls;
+    }
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const int from = side ? (common ? max(all_hi + 1, lo) : hi + 1) : lo;
+      const int to = side ? hi : (common ? min(all_lo - 1, hi) : hi);
+#pragma unroll 1
+      for (int t = from & ~7; t <= to; t += 8) {
+        uint32_t see;
+        const char* src = eight_values(kv, ktab, vtab, D, t, from, to, see);
+        f |= classes_of<A>(ldv(src + d * 16), see);
+      }
+    }
+#pragma unroll
+    for (int cls = 0; cls < 3; ++cls)
+      is[cls] |= (uint64_t)(cls < 2 ? f == 1u << cls : f > 2) << bit;
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int cls = 0; cls < 3; ++cls)
+        if ((is[cls] >> (n * E + i)) & 1u) o[n][i] = class_value(cls);
 }
 // NaN if one of the values is not finite, else 0.
 template <typename V, int N, int E = sizeof(V) / sizeof(float)>
 __device__ __forceinline__ float residue(const V (&o)[N]) {
-  float z = 0.f;
+  float z[4] = {0.f, 0.f, 0.f, 0.f};   // (in four chains, none of which waits for another)
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 0; i < E; ++i) z = __builtin_fmaf(o[n][i], 0.f, z);
-  return z;
+    for (int i = 0; i < E; ++i) z[i & 3] = __builtin_fmaf(o[n][i], 0.f, z[i & 3]);
+  return (z[0] + z[1]) + (z[2] + z[3]);
 }
 // o w of a part, for a weight above 0 that may have rounded to 0: what is not finite stays.
 __device__ __forceinline__ f32x4 weigh(const f32x4& o, float w) {
@@ -998,6 +1046,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     if (std::is_same<PT, f16_t>::value) m -= 7.f;   // the exponents' origin
+    if constexpr (!Q8) {
+      const bool mine = residue(o) != 0.f && l < INFINITY;
+      if (__builtin_expect(__ballot(mine) != 0, 0))
+        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
+                     min(posmin, p.key1 - 1), mine, o, [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); });
+    }
     if constexpr (SOLO) {
       const int slot = n_piece == 0 ? 0 : 1;
       if (col < p.rows) {
@@ -1017,20 +1071,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int n = 0; n < ND; ++n) *reinterpret_cast<f32x4*>(parts.o + at * D + 16 * n + 4 * g) = o[n];
           if (g == 0) parts.ml[at] = float2{m, l};
-        }
-      }
-      if constexpr (!Q8) {
-        if (__builtin_expect(__ballot(residue(o) != 0.f) != 0, 0) && col < p.rows && l < INFINITY) {
-          const bool whole = p.begins && p.ends;
-          const int head = p.head * a.group + row - tq * a.group;
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D;
-          float* part = parts.o + (((int64_t)c.block * 2 + slot) * TR + col) * D;
-          settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), whole && l == 0.f ? 0 : odd_ones(o),
-                       [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); },
-                       [&](int d, float x) {
-                         if (whole) out[d] = (uint16_t)pack2<A>(x, x);
-                         else part[d] = x;
-                       });
         }
       }
       if (n_piece == 0 && speaker) describe(desc, c, &p);
@@ -1060,7 +1100,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       for (int w = 0; w < (SOLO ? 1 : 4); ++w) {
         const float f = exp2f(sh_ml[w][r][0] - Mu);
         sum += f * sh_ml[w][r][1];
-        acc += f * *reinterpret_cast<const f32x4*>(&sh_o[w][r][d]);
+        acc += weigh(*reinterpret_cast<const f32x4*>(&sh_o[w][r][d]), f);
       }
       if (whole) {
         const int rr = p.row0 + r, t = token_of(a, rr), head = p.head * a.group + rr - t * a.group;
@@ -1074,21 +1114,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int64_t at = ((int64_t)c.block * 2 + slot) * TR + r;
         *reinterpret_cast<f32x4*>(parts.o + at * D + d) = acc;
         if (d == 0) parts.ml[at] = float2{M, sum};
-      }
-      if constexpr (!Q8) {
-        const f32x4 got[1] = {acc};
-        if (__builtin_expect(residue(got) != 0.f, 0) && sum < INFINITY) {
-          const int rr = p.row0 + r, t = token_of(a, rr), head = p.head * a.group + rr - t * a.group;
-          const int at = p.q.base + t;
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + t) * a.out_ld + (int64_t)head * D;
-          float* part = parts.o + (((int64_t)c.block * 2 + slot) * TR + r) * D;
-          settle<A, D>(kv, ktab, vtab, max(at - win + 1, p.key0), min(at, p.key1 - 1), odd_ones(got),
-                       [&](int bit) { return d + bit; },
-                       [&](int e, float x) {
-                         if (whole) out[e] = (uint16_t)pack2<A>(x, x);
-                         else part[e] = x;
-                       });
-        }
       }
     }
     if (n_piece == 0 && speaker) describe(desc, c, &p);
@@ -1637,6 +1662,13 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     // ---- results: a lane has four consecutive elements of its query at a time
     l += __shfl_xor(l, 32);
     if (std::is_same<A, f16_t>::value) m -= 7.f;   // the exponents' origin
+    if constexpr (!Q8) {
+      const bool mine = residue(o) != 0.f && l < INFINITY;
+      if (__builtin_expect(__ballot(mine) != 0, 0))
+        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
+                     min(posmin, p.key1 - 1), mine, o,
+                     [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); });
+    }
     const bool whole = p.begins && p.ends;
     if (col < wrows) {
       if (whole) {
@@ -1664,19 +1696,6 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
             *reinterpret_cast<f32x4*>(parts.o + at * D + n * 32 + b * 8 + hi * 4) =
                 f32x4{o[n][4 * b] * up, o[n][4 * b + 1] * up, o[n][4 * b + 2] * up, o[n][4 * b + 3] * up};
         if (hi == 0) parts.ml[at] = float2{m, l};
-      }
-    }
-    if constexpr (!Q8) {
-      if (__builtin_expect(__ballot(residue(o) != 0.f) != 0, 0) && col < wrows && l < INFINITY) {
-        const int head = p.head * a.group + row - tq * a.group;
-        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(p.q.q0 + tq) * a.out_ld + (int64_t)head * D;
-        float* part = parts.o + (((int64_t)c.block * 2 + (n_piece == 0 ? 0 : 1)) * TR + wave * 32 + col) * D;
-        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), whole && l == 0.f ? 0 : odd_ones(o),
-                     [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); },
-                     [&](int d, float x) {
-                       if (whole) out[d] = (uint16_t)pack2<A>(x, x);
-                       else part[d] = x;
-                     });
       }
     }
     if (p.first >= 0) {

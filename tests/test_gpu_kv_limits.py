@@ -423,3 +423,27 @@ def test_fp8_caches_of_f16_rows_of_every_size(n, size):
             o = np.where(big & np.isinf(host(out)), out_, host(out))
             assert np.isinf(host(out)[np.abs(out_) >= 65520 * (1 + 2.0 ** -10)]).all()
             agree(o, host(lse), (out_, lse_, sz, al, err), p_type, terms, "f16", m, "size %g k %g" % (size, k_size))
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("n,G,wide", [(3, 4, False), (100, 1, False), (90, 8, True)])
+@pytest.mark.parametrize("window", [0, 250])
+def test_infinities_that_some_rows_see_beside_others(act, n, G, wide, window):
+    # in columns with an infinity that all rows see: opposite ones that the first or the last rows of a wave see
+    m = 400
+    base = m - n
+    make = wide_case if wide else (lambda a, k, p, D, H, g, ql, kl, **kw: Case(a, k, p, H, D, ql, kl, **kw))
+    with make(act, act, 4096, 128, 1, G, [n], [m], seed=52) as c:
+        c.fill()
+        early = max(base - window, 0) + (n + 1) // 2 if window else 20
+        for at, d, x in ((200, 3, "inf"), (base + (n + 1) // 2, 3, "-inf"), (200, 4, "-inf"), (early, 4, "inf"),
+                         (m - 1, 5, "inf"), (early, 6, "nan"), (230, 7, "inf"), (230, 8, "nan"), (base, 8, "inf")):
+            c.v[at, 0, d] = float(x)
+        rewrite(c)
+        q = torch.randn((n, G, 128), device="cuda", generator=c.gen).to(TD[act])
+        out, lse = attend(c, q, 0.1, window)
+        torch.cuda.synchronize()
+        see = visible(base + np.arange(n), m, window)
+        agree(host(out), host(lse), formula(host(q), c.kd[0], c.vd[0], see, 0.1), act, 1 if wide else 2, act, m)
+        assert np.isinf(host(out)[:, :, 7]).all() and np.isnan(host(out)[:, :, 8]).all()
+        assert 0 < np.isnan(host(out)[:, 0, 3]).sum() < n and np.isinf(host(out)[0, :, 3]).all()
