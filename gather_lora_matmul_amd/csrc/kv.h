@@ -68,14 +68,15 @@ struct KvSeq {
 };
 __host__ __device__ inline KvSeq kv_seq(const KvView& v, int s) {
   KvSeq r;
-  const int64_t cap = (int64_t)v.nb * v.T, far = (int64_t)1 << 29;
+  const int cap = v.nb * v.T, far = 1 << 29;   // (cap <= 2^28, checked on the host)
   const int a = v.q_start[s], b = v.q_start[s + 1], n = v.kv_len[s] < 0 ? 0 : v.kv_len[s];
   r.q0 = a < 0 ? 0 : (a > v.n_tokens ? v.n_tokens : a);
   const int e = b < r.q0 ? r.q0 : (b > v.n_tokens ? v.n_tokens : b);
   r.q_len = e - r.q0;
-  const int64_t base = (int64_t)n - b + r.q0;   // n - (b - a) + (q0 - a)
-  r.base = (int32_t)(base < -far ? -far : (base > far ? far : base));
-  r.end = (int64_t)n > cap ? (int32_t)cap : n;
+  // n - (b - a) + (q0 - a); sums past 32 bits stay at their ends, beyond far
+  const int base = __builtin_elementwise_add_sat(__builtin_elementwise_sub_sat(n, b), r.q0);
+  r.base = base < -far ? -far : (base > far ? far : base);
+  r.end = n > cap ? cap : n;
   return r;
 }
 
