@@ -619,8 +619,8 @@ __device__ __forceinline__ float weight(float w) { return fmaxf(w, 0x1p-149f); }
 // ---- the joining launch ----------------------------------------------------------
 // RB rows a block: weights of the parts by their maxima, then a
 // weighted sum, D / 4 lanes a part and several parts at a time.  Bound by the reads
-// of the parts; each is a contiguous D * 4 bytes.  Measured 3.7 us (one token of 517,
-// 32 heads, 2.5 at the least) to 8 us (32 sequences of 40 rows, 8 heads).
+// of the parts; each is a contiguous D * 4 bytes.  Measured 3.1 us (one token of 517,
+// 32 heads, 2.3 at the least) to 8 us (32 sequences of 40 rows, 8 heads).
 template <typename A, int D, int TR, int RB>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, int G) {
   constexpr int LR = D / 4, PG = 256 / RB / LR;            // lanes of a part, parts at a time
@@ -780,9 +780,9 @@ __global__ __launch_bounds__(256) void k_attend_join_list(AttendArgs a, int G) {
 // for itself, its range of the units cut as the blocks' ones are: no wave waits
 // for another, and short sequences take their turns on 4 times as many workers.
 // Measured: 64 sequences of 20 to 2048 tokens, 32 heads of 128, bf16, 1.15 GB of K and
-// V, 214 us, 5.4 TB/s; 3 of 40001 to 131071 tokens, 8 heads for 64, FP8, 600 MB, 114 us,
-// 5.3 TB/s (a device copy of 1 GiB moves 4.8 TB/s, a sum reads 4.0); one of 517 tokens,
-// 32 heads, 9.3 us, of which two empty launches are 4.6.
+// V, 213 us, 5.4 TB/s; 3 of 40001 to 131071 tokens, 8 heads for 64, FP8, 600 MB, 115 us,
+// 5.2 TB/s (a device copy of 1 GiB moves 4.8 TB/s, a sum reads 4.0); one of 517 tokens,
+// 32 heads, 9.7 us, of which two empty launches are 4.6.
 template <typename A, typename KV, int D, bool SOLO>
 struct Skinny {
   static constexpr bool Q8 = is_quant<KV>();
@@ -1132,22 +1132,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // instructions a lane): only what overlaps is fast.  Two waves share a SIMD.
 //   Four waves (short work): two blocks share a CU, drifting apart because no barrier
 // ties them; a tile's products and its exponentials overlap within the second product
-// only.  A pair of wave tiles takes 5050 cycles (2048 over 16384 tokens, 64 heads on 8,
-// bf16: 1091 us, 945 TFLOP/s).
+// only.  P goes in two 16-bit terms: the results are as near as fp32 weights make them,
+// and the matrix cores wait for loads anyway (measured in turn, one term / two: 32 x 5 over
+// 900 to 4100 tokens, 64 heads on 8, 86.3 / 88.4 us; 4 x 128 over 2000 70.2 / 82.0; 16 x 300
+// over 300 of 32 heads on 32 68.2 / 72.3; 15 heads of 64 in a window of 1000, 1 to 255 new
+// tokens each, 59.1 / 65.0).  2048 over 16384 tokens, 64 heads on 8, bf16, takes 1490 us.
 //   Eight waves (long work): a step weaves the exponentials of one tile with its second
-// product and the first product of the next tile, and spreads the loads among them
-// (4390 cycles, 949 us, 1086 TFLOP/s: a matrix product of 8192^3 runs at 1236).  The
-// loads to LDS arrive at 53 bytes a cycle and CU, and issuing a tile's at once stops a
-// wave for 600 to 1300 cycles; 256 rows halve them a row.  Weaving alone (four waves:
-// 1055 us) and more rows alone (1079) give less, and both cost the short calls.
-//   Four waves take P in two 16-bit terms: their results are then as near as fp32 weights
-// make them, and their matrix cores wait for loads (with one term: 32 x 5 over 900 to
-// 4100 tokens, 64 heads on 8, 86.3 us against 88.4 with two, FP8 92.0 against 100.2; 4 x
-// 128 over 2000 70.2 against 82.0, 16 x 300 over 300 of 32 heads on 32 68.2 against 72.3,
-// the mixed batch of 15 heads of 64 in a window of 1000 59.1 against 65.0).  Eight waves
-// take one, because the matrix cores bound them: of the calls above 2048 over 16384 takes
-// 1011 us with one term and 1493 with two, and what one term costs is that an output's
-// error grows from its own rounding's to 1.4 times that.
+// product and the first product of the next tile, and spreads the loads among them (4390
+// cycles a pair of wave tiles; that chunk 950 to 1000 us by the card's clock, 1030 to 1086
+// TFLOP/s: a matrix product of 8192^3 runs at 1236).  The loads to LDS arrive at 53 bytes a
+// cycle and CU, and issuing a tile's at once stops a wave for 600 to 1300 cycles; 256 rows
+// halve them a row.  P goes in one term here, because the matrix cores bound the kernel:
+// with two the chunk takes 1493 us against 1011 in turn, and what one costs is that an
+// output's error grows from its own rounding's to 1.4 times that.
 __device__ __forceinline__ void load_lds16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -1705,18 +1702,19 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // Rows of a head of the longest sequence choose the kernel for all of a batch.
 // One tile of 16 of them, or of FP8 caches two (the tiles of 128 rows convert every code
 // for whatever rows there are).  Measured, us by k_attend_rows / k_attend_tiles, new
-// tokens of 64 query heads on 8 unless said: 16 rows, bf16, 2 over 500 11.0 / 14.7, 2
-// over 30000 32.0 / 37.8, 32 x 2 over 2000 51.8 / 50.2; 32 rows, bf16, 4 over 500 12.1 /
-// 14.8, 4 over 30000 47.5 / 39.2, 64 x 32 over 500 of 32 heads on 32 215 / 116; 32 rows,
-// FP8, 12.9 / 15.3, 31.4 / 39.2, 101 / 125; 40 and 48 rows, FP8, 5 over 30000 39.8 /
-// 43.4, 32 x 5 over 2000 85 / 58, 32 x 6 87 / 59.
+// tokens of 64 query heads on 8 unless said: 16 rows, bf16, 2 over 500 11.3 / 15.5, 2
+// over 30000 32.2 / 40.1, 32 x 2 over 2000 52.4 / 52.8; 32 rows, bf16, 4 over 500 11.7 /
+// 15.6, 4 over 30000 47.1 / 41.6, 32 x 4 over 2000 47.3 / 54.0, 64 x 32 over 500 of 32
+// heads on 32 207 / 121; 32 rows, FP8, 12.7 / 15.6, 32.2 / 40.2, 94.8 / 115 (the last as of
+// bf16); 40 and 48 rows, FP8, 5 over 30000 40.1 / 44.5, 32 x 5 over 2000 84.3 / 61.6, 32 x 6
+// 85.1 / 62.4.
 inline bool few_rows(bool fp8, int32_t group, int32_t max_q_len) {
   return (int64_t)max_q_len * group <= (fp8 ? 32 : 16);
 }
 inline int blocks_of(int n_cu) { return std::min(2 * n_cu / 8 * 8, 1024); }
 
 // Every wave for itself once there are two (sequence, head) pairs a block.  Measured, us
-// by blocks / by waves: 64 sequences of 16 tokens, 32 heads, 22 / 10, of 20 to 2048 250 /
+// by blocks / by waves: 64 sequences of 16 tokens, 32 heads, 19 / 12, of 20 to 2048 233 /
 // 214; with fewer pairs a wave's range ends inside its tiles and the parts cost more.
 inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_seqs * H >= 2 * blocks_of(n_cu); }
 
@@ -1724,11 +1722,11 @@ inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_
 // average and a block gets 24 units or more, as far as the host can tell: if the caches
 // are as long as their tables (or the window).  Measured, us of a call with four / eight
 // waves, 64 query heads on 8 unless said, bf16 (FP8), by new tokens over keys: 2048 over
-// 16384 1091 / 949 (1208 / 967), the same in a window of 1000 115 / 98, 2 x 256 over 4096
-// 105 / 102 (120 / 104), 4000 over 4000 of 32 heads on 32 206 / 197, 1000 over 30000 of 8
-// on 1 164 / 153; and below the line 4 x 128 over 2000 69 / 72, 512 over 512 48 / 56, 4096
-// over 4096 of 8 on 1 109 / 128, 32 x 5 over 4096 84 / 100, 16 x 300 over 300 of 32 on
-// 32 65 / 76.
+// 16384 1490 / 958 (1485 / 984), the same in a window of 1000 142 / 100 (145 / 100), 2 x 256
+// over 4096 126 / 99 (128 / 106), 512 over 4096 123 / 98, 4000 over 4000 of 32 heads on 32
+// 255 / 198, 1000 over 30000 of 8 on 1 205 / 151; and below the line 4 x 128 over 2000 81 /
+// 72, 512 over 512 50 / 57, 1000 over 1000 of 32 on 32 54 / 55, 4096 over 4096 of 8 on 1 119 /
+// 131, 32 x 5 over 4096 115 / 117 (112 / 130), 16 x 300 over 300 of 32 on 32 69 / 80.
 inline bool wide_tiles(const AttendArgs& a, int blocks) {
   const int64_t rows = (int64_t)a.kv.n_tokens * a.group;
   if (rows < 512 * (int64_t)a.kv.n_seqs) return false;
@@ -1752,9 +1750,9 @@ hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW>), dim3(G), dim3(NW * 64), lds, s, a);
   // tiles of which none has many parts: four blocks each; else the list.  Measured
-  // (us of a call, list / this): 32 sequences of 5 x 8 rows 86.7 / 84.6, 2 of 256 x
-  // 8 rows over 4096 tokens 110 / 104, 64 x 4 rows of 8 heads over 2000 tokens 28.8
-  // / 34.0, 100 x 8 rows of one head over 30000 tokens 43.9 / 118
+  // (us of a call, list / this): 32 sequences of 5 x 8 rows over 2500 tokens 78.4 / 76.1,
+  // 2 of 256 x 8 rows over 4096 130 / 126, 64 x 4 rows of 8 heads over 2000 33.6 / 83.6,
+  // 100 x 8 rows of one head over 30000 49.5 / 123
   const int64_t tiles = a.kv.H * std::max<int64_t>(a.kv.n_seqs, (int64_t)a.kv.n_tokens * a.group / TT::TR);
   if (2 * tiles >= G) {
     constexpr int RB = 256 / (D / 4);

@@ -8,10 +8,10 @@
 // its pieces written 16 bytes (FP8: 8) a lane, and a wave's lanes cover whole
 // 128-byte lines on both sides, save the tokens at a sequence's ends.  Measured (a
 // device copy of 1 GiB moves 4.8 TB/s): write of 32 requests of 32 to 600 tokens, 40
-// heads of 128, bf16 into FP8, 313 MB, 79 us, 4.0 TB/s; read of 16 requests of 200 to
-// 3000 tokens, 32 heads, FP8 to f16, 565 MB, 123 us, 4.6 TB/s; one token each of 64
-// requests written, 5.5 us, and 4001 tokens of 8 heads read, 33 MB, 8.1 us, are mostly
-// the launch.
+// heads of 128, bf16 into FP8, 313 MB, 79 us, 4.0 TB/s, the same into bf16, 416 MB,
+// 97 us, 4.3 TB/s; read of 16 requests of 200 to 3000 tokens, 32 heads, FP8 to f16, 565
+// MB, 123 us, 4.6 TB/s; one token each of 64 requests written, 5.5 us, and 4001 tokens of
+// 8 heads read, 33 MB, 8.1 us, are mostly the launch.
 #include "kcommon.h"
 #include "kv.h"
 

@@ -15,7 +15,7 @@
 // the token.  Enough sequences, or few probabilities, are one launch with a block
 // of 16 waves a sequence; else the regions' sums are a launch over the whole chip
 // and the scan is a second one.  Measured: one sequence of 4 drafted tokens, 32000
-// probabilities, f32, 7.3 us (a launch and three dependent rounds of loads); 128 of
+// probabilities, f32, 7.4 us (a launch and three dependent rounds of loads); 128 of
 // none to 7, 131071 probabilities, 108 MB, 25.5 us, 4.2 TB/s.
 #include "kcommon.h"
 #include "kv.h"
@@ -333,10 +333,10 @@ __global__ __launch_bounds__(512) void k_verify_pick(VerifyArgs a, const uint64_
 }
 
 // One launch where a block a sequence is enough to read the rows.  Measured on
-// MI355X, us of one launch / of two, by sequences, f32 with drafts: 32000
-// probabilities 6.7 / 8.5 (1), 8.7 / 8.4 (16), 9.5 / 10.1 (128); 131071 15.4 / 8.2
-// (1), 21.6 / 16.5 (64), 22.9 / 23.2 (128), 35.7 / 40.0 (256); 262144 26.8 / 8.3
-// (1), 44.3 / 38.4 (128), 72 / 82 (256).
+// MI355X, us of a call by one launch / by two, by sequences of 4 drafted tokens, f32 with
+// the draft's probabilities: 32000 probabilities 7.6 / 7.8 (1), 8.7 / 8.3 (16), 10.7 /
+// 12.4 (128); 131071 16.3 / 7.5 (1), 21.8 / 16.6 (64), 28.9 / 26.9 (128), 46.6 / 49.6
+// (256); 262144 30.8 / 7.4 (1), 56.2 / 46.1 (128), 83 / 86 (256).
 bool one_launch(const VerifyArgs& a) { return a.vocab <= 32768 || a.n_seqs >= 192; }
 
 template <typename T>

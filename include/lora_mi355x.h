@@ -464,8 +464,8 @@ lora_status lora_kv_layout(const lora_pool* pool, const lora_kv_desc* kv, int32_
  * FP8: a row x of one token and head gets the smallest exponent e in [-126,
  * 127] with 448 * 2^e >= max |x| over its finite elements, and the codes
  * e4m3(x * 2^-e), nearest even; elements that are not finite become NaN codes.
- * Tokens at negative positions, past the table and in absent pages are dropped.  No page may
- * be named twice by the tokens written. */
+ * Tokens at negative positions, past the table and in absent pages are dropped.  No
+ * page may be named twice by the tokens written. */
 lora_status lora_kv_write(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                           const void* k_dev, const void* v_dev, int64_t ld, void* stream);
 /* The reverse: the cached rows of the batch's tokens (the last q_len of each
@@ -486,24 +486,25 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * h / (n_q_heads / n_kv_heads).  The token at position i sees the present tokens
  * j with j <= i and, if window > 0, j > i - window:
  *   out_i = sum_j p_ij v_j,  p_i. = softmax of scale * q_i . k_j over those j
- * with fp32 scores, maxima and sums.  For the products with v, p goes in two 16-bit
- * terms (relative 2^-16 of bf16, 2^-22 of f16; bf16 for FP8 caches in calls of at
- * most 32 rows a head), in long work in one of act_dtype (2^-8, 2^-11; of f16 a weight
- * of any size is off by 2^-32 of the largest more at most; with
- * f16 activations and more than 32 rows a head FP8 values are off by 2^-24 at most): where there
- * are 512 rows a head and sequence on average, and full tables (or the window) would
- * give every compute unit 24 tiles of 256 rows and 64 keys.  One rounding at the store.  A token that sees none gets zeros.  What is
- * not seen has no influence, whatever it holds; a value of v that is not finite is that
- * element's result in every row that sees its token, at any weight (NaN where several
- * differ).  lse (optional, NULL)
- * [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j), -inf for none.  Rows
- * of out that belong to no sequence are not written.  LORA_E_UNSUPPORTED for
- * calls that could need 2^31 units of work (a tile of rows with 64 keys, if every
- * cache filled its table); overlapping rows of a q_start that does not ascend are
- * undefined, and nothing at all if they make that many.  Stream-ordered, no host
- * wait, no allocation (graph-capturable); workspace_dev: 256-byte aligned, at
- * least lora_kv_attend_workspace_size bytes, no initial contents; calls that
- * share one must not overlap.  Runs of one batch give the same bits. */
+ * with fp32 scores, maxima and sums and one rounding at the store.  For the products
+ * with v, p goes in two 16-bit terms of act_dtype (relative 2^-16 of bf16, 2^-22 of
+ * f16), over FP8 caches with at most 32 rows a head of bf16.  In long work it goes in
+ * one (2^-8, 2^-11): where there are 512 rows a head and sequence on average, and full
+ * tables (or the window) would give every compute unit 24 tiles of 256 rows and 64
+ * keys.  A weight in f16 is off by 2^-32 of the largest more at most, whatever its
+ * size, and with f16 activations and more than 32 rows a head FP8 values are off by
+ * 2^-24 at most.
+ * A token that sees none gets zeros.  What is not seen has no influence, whatever it
+ * holds; a value of v that is not finite is that element's result in every row that
+ * sees its token, at any weight (NaN where several differ).  Windows past 2^28 count as
+ * none.  lse (optional, NULL) [n_tokens][n_q_heads]: ln sum_j exp(scale * q_i . k_j),
+ * -inf for none.  Rows of out that belong to no sequence are not written.
+ * LORA_E_UNSUPPORTED for calls that could need 2^31 units of work (a tile of rows with
+ * 64 keys, if every cache filled its table); overlapping rows of a q_start that does
+ * not ascend are undefined, and nothing at all if they make that many.  Stream-ordered,
+ * no host wait, no allocation (graph-capturable); workspace_dev: 256-byte aligned, at
+ * least lora_kv_attend_workspace_size bytes, no initial contents; calls that share one
+ * must not overlap.  Runs of one batch give the same bits. */
 lora_status lora_kv_attend(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                            const void* q_dev, int64_t q_ld, int32_t n_q_heads, float scale,
                            int32_t window, void* out_dev, int64_t out_ld, float* lse_dev,
