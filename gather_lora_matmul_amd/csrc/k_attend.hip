@@ -118,7 +118,17 @@ __device__ __forceinline__ void p_operand(const float* p, u32x4& hi, u32x4& lo) 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[i] = pack2<T>(p[2 * i], p[2 * i + 1]);
-    l[i] = pack2<T>(p[2 * i] - bits_to_f<T>(h[i] & 0xffffu), p[2 * i + 1] - bits_to_f<T>(h[i] >> 16));
+    if constexpr (std::is_same<T, f16_t>::value) {
+      // p - h in one instruction a value, which takes h as it lies in its half (the compiler
+      // left alone rounds each half once more by itself and converts it back)
+      float less = -1.f;
+      asm("" : "+v"(h[i]));
+      asm("" : "+v"(less));
+      const f16x2_t v = __builtin_bit_cast(f16x2_t, h[i]);
+      l[i] = pack2<T>(__builtin_fmaf((float)v[0], less, p[2 * i]), __builtin_fmaf((float)v[1], less, p[2 * i + 1]));
+    } else {
+      l[i] = pack2<T>(p[2 * i] - bits_to_f<T>(h[i] & 0xffffu), p[2 * i + 1] - bits_to_f<T>(h[i] >> 16));
+    }
   }
   hi = u32x4{h[0], h[1], h[2], h[3]};
   lo = u32x4{l[0], l[1], l[2], l[3]};
@@ -1136,7 +1146,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // and the matrix cores wait for loads anyway (measured in turn, one term / two: 32 x 5 over
 // 900 to 4100 tokens, 64 heads on 8, 86.3 / 88.4 us; 4 x 128 over 2000 70.2 / 82.0; 16 x 300
 // over 300 of 32 heads on 32 68.2 / 72.3; 15 heads of 64 in a window of 1000, 1 to 255 new
-// tokens each, 59.1 / 65.0).  2048 over 16384 tokens, 64 heads on 8, bf16, takes 1490 us.
+// tokens each, 59.1 / 65.6).  2048 over 16384 tokens, 64 heads on 8, bf16, takes 1490 us.
 //   Eight waves (long work): a step weaves the exponentials of one tile with its second
 // product and the first product of the next tile, and spreads the loads among them (4390
 // cycles a pair of wave tiles; that chunk 950 to 1000 us by the card's clock, 1030 to 1086
