@@ -730,7 +730,8 @@ def lora_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window:
                    workspace=None, stream=None):
     """out = attention of q [n_tokens][n_q_heads][head_dim] over the cache; lse
     (optional): float32 [n_tokens][n_q_heads]; workspace: a device tensor of
-    lora_kv_attend_workspace_size bytes."""
+    lora_kv_attend_workspace_size bytes.  Any whole number is a window: 0, and
+    what passes 2^28, none; below 0 it is refused."""
     prepare_kv_attend(cache, batch, q, out, scale, window, lse, workspace)(stream)
 
 
@@ -847,7 +848,7 @@ def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, wind
     wp, wb = _ws(workspace)
     return PreparedCall(_lib.lora_kv_attend,
                         (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, q_ld, heads,
-                         float(scale), int(window), op, out_ld, _dev_ptr(lse), wp, wb),
+                         float(scale), max(-1, min(int(window), 2 ** 31 - 1)), op, out_ld, _dev_ptr(lse), wp, wb),
                         "lora_kv_attend", (cache, batch, q, out, lse, workspace))
 
 

@@ -447,3 +447,16 @@ def test_infinities_that_some_rows_see_beside_others(act, n, G, wide, window):
         agree(host(out), host(lse), formula(host(q), c.kd[0], c.vd[0], see, 0.1), act, 1 if wide else 2, act, m)
         assert np.isinf(host(out)[:, :, 7]).all() and np.isnan(host(out)[:, :, 8]).all()
         assert 0 < np.isnan(host(out)[:, 0, 3]).sum() < n and np.isinf(host(out)[0, :, 3]).all()
+
+
+def test_windows_past_32_bits_are_none():
+    with Case("bf16", "bf16", 4096, 1, 128, [2], [70], seed=53) as c:
+        c.fill()
+        q = torch.randn((2, 2, 128), device="cuda", generator=c.gen).to(TD["bf16"])
+        want, lse = attend(c, q, 0.1)
+        for window in (10 ** 12, 2 ** 63 - 1, 2 ** 32 + 5, 2 ** 31):
+            got, ls = attend(c, q, 0.1, window)
+            assert torch.equal(got, want) and torch.equal(ls, lse)
+        for window in (-1, -2 ** 31 - 1, -2 ** 32 + 5):
+            with pytest.raises(L.LoraError, match="window"):
+                attend(c, q, 0.1, window)
