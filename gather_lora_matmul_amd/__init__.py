@@ -90,7 +90,7 @@ class KvBatchDesc(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
                 ("max_q_len", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
                 ("q_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
-                ("table_dev", ctypes.c_void_p)]
+                ("table_dev", ctypes.c_void_p), ("two_terms", ctypes.c_int32)]
 
 
 class VerifyDesc(ctypes.Structure):
@@ -664,9 +664,10 @@ class KvBatch:
     """The sequences of one call (lora_kv_batch): int32 device tensors q_start
     [n_seqs + 1], kv_len [n_seqs] and table [n_seqs][2][n_kv_heads][max_blocks],
     read by the calls that use it (kept alive here).  Their contents may change
-    between calls; n_tokens and max_q_len are bounds."""
+    between calls; n_tokens and max_q_len are bounds.  two_terms: lora_kv_attend
+    takes the weights in two 16-bit terms in long work too."""
 
-    def __init__(self, q_start, kv_len, table, n_tokens: int, max_q_len: int):
+    def __init__(self, q_start, kv_len, table, n_tokens: int, max_q_len: int, two_terms: bool = False):
         import torch
         for t, what in ((q_start, "q_start"), (kv_len, "kv_len"), (table, "table")):
             if t.dtype != torch.int32:
@@ -678,7 +679,7 @@ class KvBatch:
             raise ValueError("table: shape %s, expected [%d][2][n_kv_heads][max_blocks]" % (tuple(table.shape), n))
         self.q_start, self.kv_len, self.table = q_start, kv_len, table
         self.desc = KvBatchDesc(n, int(n_tokens), int(max_q_len), int(table.shape[3]), _dev_ptr(q_start),
-                                _dev_ptr(kv_len), _dev_ptr(table))
+                                _dev_ptr(kv_len), _dev_ptr(table), int(bool(two_terms)))
 
 
 def _kv_rows(cache: KvCache, batch: KvBatch, t, what: str, heads: Optional[int] = None):

@@ -1154,7 +1154,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // cycle and CU, and issuing a tile's at once stops a wave for 600 to 1300 cycles; 256 rows
 // halve them a row.  P goes in one term here, because the matrix cores bound the kernel:
 // with two the chunk takes 1493 us against 1011 in turn, and what one costs is that an
-// output's error grows from its own rounding's to 1.4 times that.
+// output's error grows from its own rounding's to 1.4 times that.  A caller who wants two
+// gets four waves, which take as long.
 __device__ __forceinline__ void load_lds16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -1739,7 +1740,7 @@ inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_
 // 131, 32 x 5 over 4096 115 / 117 (112 / 130), 16 x 300 over 300 of 32 on 32 69 / 80.
 inline bool wide_tiles(const AttendArgs& a, int blocks) {
   const int64_t rows = (int64_t)a.kv.n_tokens * a.group;
-  if (rows < 512 * (int64_t)a.kv.n_seqs) return false;
+  if (a.two_terms || rows < 512 * (int64_t)a.kv.n_seqs) return false;
   int64_t keys = (int64_t)a.kv.nb * a.kv.T - a.max_q_len / 2;
   if (a.window > 0) keys = std::min<int64_t>(keys, a.window);
   return rows / 256 * a.kv.H * (keys / 64) >= 24 * (int64_t)blocks;

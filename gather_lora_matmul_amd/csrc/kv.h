@@ -103,6 +103,7 @@ struct AttendArgs {
   uint32_t group_m;        // by it (if it is not 1)
   int32_t group_s;
   int32_t max_q_len;
+  bool two_terms;          // of the weights, in long work too
   float scale_log2;        // scale * log2(e)
   int32_t window;          // 0: none
   char* ws;

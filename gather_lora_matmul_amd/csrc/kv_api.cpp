@@ -211,6 +211,7 @@ lora_status lora_kv_attend(const lora_pool* p, const lora_kv_desc* d, const lora
   a.group = n_q_heads / d->n_kv_heads;
   div_init(a.group < 2 ? 2 : a.group, a.group_m, a.group_s);
   a.max_q_len = longest(b);
+  a.two_terms = b->two_terms != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window > (1 << 28) ? 0 : window;   // no position is farther back; keeps differences in 32 bits
   a.ws = (char*)workspace_dev;

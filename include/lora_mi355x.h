@@ -452,6 +452,8 @@ typedef struct {
   const int32_t* q_start_dev;  /* [n_seqs + 1], ascending                        */
   const int32_t* kv_len_dev;   /* [n_seqs]                                       */
   const int32_t* table_dev;
+  int32_t two_terms;       /* lora_kv_attend: not 0 takes the weights in two terms in
+                              long work too                                      */
 } lora_kv_batch;
 
 /* Tokens of a page (T), pages of one block of T tokens (2 n_kv_heads) and bytes
@@ -489,7 +491,7 @@ lora_status lora_kv_attend_workspace_size(const lora_pool* pool, const lora_kv_d
  * with fp32 scores, maxima and sums and one rounding at the store.  For the products
  * with v, p goes in two 16-bit terms of act_dtype (relative 2^-16 of bf16, 2^-22 of
  * f16), over FP8 caches with at most 32 rows a head of bf16.  In long work it goes in
- * one (2^-8, 2^-11): where there are 512 rows a head and sequence on average, and full
+ * one (2^-8, 2^-11; two_terms: as elsewhere, for up to half as much time again): where there are 512 rows a head and sequence on average, and full
  * tables (or the window) would give every compute unit 24 tiles of 256 rows and 64
  * keys.  A weight in f16 is off by 2^-32 of the largest more at most, whatever its
  * size, and with f16 activations and more than 32 rows a head FP8 values are off by

@@ -52,9 +52,9 @@ def whole_scores(c, n_heads, spread=2):
     return q.to(TD[c.act]), [host(x) for x in c.k.split(c.kv_len)]
 
 
-def check_terms(c, q, kd, vd, p_type, terms, rows=None):
+def check_terms(c, q, kd, vd, p_type, terms, rows=None, batch=None):
     """The kernel's results within the bound of `terms`, which weights of one term are not within."""
-    out, lse = attend(c, q, 0.25)
+    out, lse = attend(c, q, 0.25, batch=batch)
     torch.cuda.synchronize()
     worst, at = 0.0, 0
     for s, (n, m) in enumerate(zip(c.q_len, c.kv_len)):
@@ -104,6 +104,20 @@ def test_weights_of_long_work_have_one_term(act, kv):
         _, vd = c.fill()
         q, kd = whole_scores(c, 8)
         check_terms(c, q, kd, vd, act, 1, rows=[[0, 31, 32, 99], [0, 1, 59]])
+
+
+@pytest.mark.parametrize("act,kv", [("f16", "f16"), ("bf16", "bf16"), ("f16", "fp8"), ("bf16", "fp8")])
+def test_weights_of_long_work_have_two_terms_for_those_who_ask(act, kv):
+    q_len, kv_len = [100, 60], [140, 99]
+    with wide_case(act, kv, 4096, 128, 1, 8, q_len, kv_len, seed=49) as c:
+        log("[case] terms, wide with two %s/%s" % (act, kv))
+        _, vd = c.fill()
+        q, kd = whole_scores(c, 8)
+        b = L.KvBatch(c.q_start, c.kvl, c.table, c.n, max(q_len), two_terms=True)
+        check_terms(c, q, kd, vd, act, 2, rows=[[0, 31, 32, 99], [0, 1, 59]], batch=b)
+        one, _ = attend(c, q, 0.25)
+        two, _ = attend(c, q, 0.25, batch=b)
+        assert not torch.equal(one, two)
 
 
 # ---------------------------------------------------------------------------------------------
