@@ -49,6 +49,7 @@ __device__ __forceinline__ float prob(const void* base, int64_t i) {
 struct VerifySeq {
   int q0, k;        // first row, drafted tokens (-1: no rows)
   int first;        // accepted tokens
+  int rows;         // all of the sequence's, which are k + 1 unless its drafts are not there
   int64_t drow;     // draft row of the first drafted token
 };
 
@@ -68,7 +69,8 @@ __device__ __forceinline__ VerifySeq accept(const VerifyArgs& a, int s) {
   int b, e;
   rows_of(a, s, b, e);
   r.q0 = b;
-  r.k = e - b - 1;
+  r.rows = e - b;
+  r.k = r.rows - 1;
   // each sequence with rows before this one has one row that is no draft's
   r.drow = (int64_t)b;
   for (int i0 = 0; i0 < s; i0 += THREADS) {
@@ -275,7 +277,7 @@ __device__ __forceinline__ void finish(const VerifyArgs& a, int s, const VerifyS
     __syncthreads();
     tok = *sh;
   }
-  for (int t = tid; t <= (r.k > 0 ? r.k : 0); t += THREADS)
+  for (int t = tid; t < r.rows; t += THREADS)
     a.tokens[r.q0 + t] = t < r.first ? a.drafted[r.drow + t] : (t == r.first ? tok : -1);
   if (tid == 0) a.n_out[s] = r.first + 1;
 }

@@ -547,7 +547,8 @@ lora_status lora_spec_verify_workspace_size(int32_t n_seqs, int32_t vocab, size_
  * floor(2^44 p_v) after the last one or when all of those are 0: the smallest v
  * with w_0 + .. + w_v > floor(total * floor(2^31 u) / 2^31).  All weights 0: -1.
  * Whole-number sums: the token depends on no order or split.  An id outside
- * [0, vocab) is refused.  Stream-ordered, no wait, no allocation; workspace_dev
+ * [0, vocab) is refused; a sequence whose drafted rows would lie outside the n_drafts
+ * gets one token, of its first row.  Stream-ordered, no wait, no allocation; workspace_dev
  * 16-byte aligned, no initial contents, not shared by calls that overlap. */
 lora_status lora_spec_verify(const lora_verify_desc* desc, void* workspace_dev, size_t ws_bytes,
                              void* stream);
