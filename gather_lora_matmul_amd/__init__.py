@@ -45,6 +45,9 @@ EXPORTS = (
     "lora_store_destroy", "lora_store_add", "lora_store_ensure", "lora_store_get_stats",
     "lora_kv_layout", "lora_kv_write", "lora_kv_read", "lora_kv_attend_workspace_size",
     "lora_kv_attend", "lora_spec_verify_workspace_size", "lora_spec_verify",
+    "lora_kv_tree_build", "lora_kv_attend_tree", "lora_spec_verify_tree_workspace_size", "lora_spec_verify_tree",
+    "lora_kv_weigh_workspace_size", "lora_kv_weigh", "lora_kv_select_workspace_size", "lora_kv_select",
+    "lora_kv_compact",
 )
 
 
@@ -102,6 +105,22 @@ class VerifyDesc(ctypes.Structure):
                 ("target_dev", ctypes.c_void_p), ("draft_dev", ctypes.c_void_p),
                 ("u_accept_dev", ctypes.c_void_p), ("u_sample_dev", ctypes.c_void_p),
                 ("tokens_dev", ctypes.c_void_p), ("n_out_dev", ctypes.c_void_p)]
+
+
+class KvTreeDesc(ctypes.Structure):
+    _fields_ = [("words", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("seen_dev", ctypes.c_void_p), ("depth_dev", ctypes.c_void_p)]
+
+
+class TreeVerifyDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("path_ld", ctypes.c_int32), ("reserved", ctypes.c_int32), ("target_ld", ctypes.c_int64),
+                ("q_start_dev", ctypes.c_void_p), ("parent_dev", ctypes.c_void_p),
+                ("drafted_dev", ctypes.c_void_p), ("target_dev", ctypes.c_void_p),
+                ("u_accept_dev", ctypes.c_void_p), ("u_sample_dev", ctypes.c_void_p),
+                ("tokens_dev", ctypes.c_void_p), ("path_dev", ctypes.c_void_p),
+                ("n_out_dev", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -168,6 +187,15 @@ def _load() -> ctypes.CDLL:
         "lora_kv_attend": [V, KV, KB, V, I64, I32, F, I32, V, I64, V, V, SZ, V],
         "lora_spec_verify_workspace_size": [I32, I32, ctypes.POINTER(SZ)],
         "lora_spec_verify": [ctypes.POINTER(VerifyDesc), V, SZ, V],
+        "lora_kv_tree_build": [I32, I32, V, V, I32, I32, V, V, V],
+        "lora_kv_attend_tree": [V, KV, KB, ctypes.POINTER(KvTreeDesc), V, I64, I32, F, I32, V, I64, V, V, SZ, V],
+        "lora_spec_verify_tree_workspace_size": [I32, I32, ctypes.POINTER(SZ)],
+        "lora_spec_verify_tree": [ctypes.POINTER(TreeVerifyDesc), V, SZ, V],
+        "lora_kv_weigh_workspace_size": [V, KV, KB, I32, ctypes.POINTER(SZ)],
+        "lora_kv_weigh": [V, KV, KB, V, I64, I32, F, I32, V, F, V, V, I64, V, SZ, V],
+        "lora_kv_select_workspace_size": [V, KV, KB, ctypes.POINTER(SZ)],
+        "lora_kv_select": [V, KV, KB, V, I64, I32, I32, I32, V, I64, V, V, SZ, V],
+        "lora_kv_compact": [V, KV, KB, V, I32, I64, V, I32, V, I64, V],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -752,6 +780,94 @@ def lora_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tokens
 
 
 # ----------------------------------------------------------------------------
+# trees of drafted tokens
+# ----------------------------------------------------------------------------
+class KvTree:
+    """What the tokens of trees see (lora_kv_tree): int64 device tensor seen
+    [n_tokens][words] (bit u % 64 of word u / 64: new token u) and, where there is a
+    window, int32 depth [n_tokens]; read by the calls that use it (kept alive here).
+    lora_kv_tree_build writes both."""
+
+    def __init__(self, seen, depth=None):
+        import torch
+        if seen.dtype != torch.int64 or seen.dim() != 2 or not 1 <= seen.shape[1] <= 16:
+            raise TypeError("seen: expected an int64 tensor [n_tokens][1..16], got %s %s" % (seen.dtype, tuple(seen.shape)))
+        if depth is not None:
+            if depth.dtype != torch.int32:
+                raise TypeError("depth: dtype %s, expected int32" % depth.dtype)
+            _check_tensor(depth, "depth", None, int(seen.shape[0]))
+        self.seen, self.depth = seen, depth
+        self.desc = KvTreeDesc(int(seen.shape[1]), 0, _dev_ptr(seen), _dev_ptr(depth))
+
+
+def lora_kv_tree_build(q_start, parent, seen, depth, window: int = 0, stream=None):
+    """seen [n_tokens][words] and depth [n_tokens] of trees with the parents parent
+    [n_tokens]; q_start [n_seqs + 1]."""
+    prepare_kv_tree_build(q_start, parent, seen, depth, window)(stream)
+
+
+def lora_kv_attend_tree(cache: KvCache, batch: KvBatch, tree: KvTree, q, out, scale: float, window: int = 0,
+                        lse=None, workspace=None, stream=None):
+    """lora_kv_attend of tokens that see what was cached before them and the new
+    tokens of their rows of `tree`; the same workspace."""
+    prepare_kv_attend_tree(cache, batch, tree, q, out, scale, window, lse, workspace)(stream)
+
+
+def lora_spec_verify_tree_workspace_size(n_seqs: int, vocab: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_spec_verify_tree_workspace_size(int(n_seqs), int(vocab), ctypes.byref(out)),
+           "lora_spec_verify_tree_workspace_size")
+    return int(out.value)
+
+
+def lora_spec_verify_tree(q_start, parent, drafted, target, u_accept, u_sample, tokens, path, n_out, workspace,
+                          stream=None):
+    """Verify trees: q_start [n_seqs + 1]; parent, drafted and u_accept [n_tokens];
+    target [n_tokens][vocab]; u_sample [n_seqs]; writes tokens and path [n_seqs][most]
+    and n_out [n_seqs]."""
+    prepare_spec_verify_tree(q_start, parent, drafted, target, u_accept, u_sample, tokens, path, n_out,
+                             workspace)(stream)
+
+
+# ----------------------------------------------------------------------------
+# eviction from the KV cache
+# ----------------------------------------------------------------------------
+def lora_kv_weigh_workspace_size(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_kv_weigh_workspace_size(cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc),
+                                             int(n_q_heads), ctypes.byref(out)), "lora_kv_weigh_workspace_size")
+    return int(out.value)
+
+
+def lora_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, scale: float, window: int = 0,
+                  decay: float = 1.0, before=None, workspace=None, stream=None):
+    """weights [n_seqs][n_kv_heads][n] (float32, by position) = decay * before + the
+    attention that the cached tokens get from q [n_tokens][n_q_heads][head_dim], whose
+    attention left lse [n_tokens][n_q_heads].  before: None or like weights (or weights)."""
+    prepare_kv_weigh(cache, batch, q, lse, weights, scale, window, decay, before, workspace)(stream)
+
+
+def lora_kv_select_workspace_size(cache: KvCache, batch: KvBatch) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_kv_select_workspace_size(cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc),
+                                              ctypes.byref(out)), "lora_kv_select_workspace_size")
+    return int(out.value)
+
+
+def lora_kv_select(cache: KvCache, batch: KvBatch, weights, budget: int, keep, n_keep, sinks: int = 0,
+                   recent: int = 0, workspace=None, stream=None):
+    """keep [n_seqs][n_kv_heads][>= budget] and n_keep [n_seqs] (int32): the positions of the
+    tokens that stay, by weights [n_seqs][n_kv_heads][n]."""
+    prepare_kv_select(cache, batch, weights, budget, keep, n_keep, sinks, recent, workspace)(stream)
+
+
+def lora_kv_compact(cache: KvCache, batch: KvBatch, keep, n_keep, from_new: bool = False, weights=None, stream=None):
+    """Move the tokens that stay together, in place: keep [n_seqs][1 or n_kv_heads][most] (or
+    [n_seqs][most]) as of lora_kv_select, or with from_new the path of lora_spec_verify_tree."""
+    prepare_kv_compact(cache, batch, keep, n_keep, from_new, weights)(stream)
+
+
+# ----------------------------------------------------------------------------
 # prepared calls: arguments checked and marshalled once
 # ----------------------------------------------------------------------------
 class PreparedCall:
@@ -837,8 +953,7 @@ def prepare_kv_read(cache: KvCache, batch: KvBatch, k, v) -> PreparedCall:
                         (cache, batch, k, v))
 
 
-def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window: int = 0, lse=None,
-                      workspace=None) -> PreparedCall:
+def _attend_args(cache: KvCache, batch: KvBatch, q, out, scale, window, lse, workspace):
     if batch.table.shape[2] != cache.desc.n_kv_heads:
         raise ValueError("table: %d heads, the cache has %d" % (batch.table.shape[2], cache.desc.n_kv_heads))
     qp, q_ld = _kv_rows(cache, batch, q, "q")
@@ -847,10 +962,113 @@ def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, wind
     if lse is not None:
         _check_tensor(lse, "lse", 0, batch.desc.n_tokens * heads)
     wp, wb = _ws(workspace)
-    return PreparedCall(_lib.lora_kv_attend,
-                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, q_ld, heads,
-                         float(scale), max(-1, min(int(window), 2 ** 31 - 1)), op, out_ld, _dev_ptr(lse), wp, wb),
+    return (qp, q_ld, heads, float(scale), _window(window), op, out_ld, _dev_ptr(lse), wp, wb)
+
+
+def _window(window) -> int:
+    return max(-1, min(int(window), 2 ** 31 - 1))
+
+
+def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window: int = 0, lse=None,
+                      workspace=None) -> PreparedCall:
+    args = _attend_args(cache, batch, q, out, scale, window, lse, workspace)
+    return PreparedCall(_lib.lora_kv_attend, (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc)) + args,
                         "lora_kv_attend", (cache, batch, q, out, lse, workspace))
+
+
+def prepare_kv_attend_tree(cache: KvCache, batch: KvBatch, tree: KvTree, q, out, scale: float, window: int = 0,
+                           lse=None, workspace=None) -> PreparedCall:
+    args = _attend_args(cache, batch, q, out, scale, window, lse, workspace)
+    if tree.seen.shape[0] < batch.desc.n_tokens:
+        raise ValueError("seen: %d rows for %d tokens" % (tree.seen.shape[0], batch.desc.n_tokens))
+    return PreparedCall(_lib.lora_kv_attend_tree,
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), ctypes.byref(tree.desc)) + args,
+                        "lora_kv_attend_tree", (cache, batch, tree, q, out, lse, workspace))
+
+
+def _check_int32(t, what: str, need: int):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError("%s: dtype %s, expected int32" % (what, t.dtype))
+    _check_tensor(t, what, None, need)
+
+
+def prepare_kv_tree_build(q_start, parent, seen, depth, window: int = 0) -> PreparedCall:
+    n = int(parent.numel())
+    tree = KvTree(seen, depth)
+    _check_int32(q_start, "q_start", 1)
+    _check_int32(parent, "parent", 0)
+    _check_int32(depth, "depth", n)
+    if seen.shape[0] < n:
+        raise ValueError("seen: %d rows for %d tokens" % (seen.shape[0], n))
+    return PreparedCall(_lib.lora_kv_tree_build,
+                        (int(q_start.numel()) - 1, n, _dev_ptr(q_start), _dev_ptr(parent), tree.desc.words,
+                         _window(window), tree.desc.seen_dev, tree.desc.depth_dev),
+                        "lora_kv_tree_build", (q_start, parent, seen, depth))
+
+
+def _token_weights(cache: KvCache, batch: KvBatch, t, what: str):
+    """(pointer, entries of a head) of a float32 [n_seqs][n_kv_heads][n] tensor."""
+    _check_tensor(t, what, 0, 0)
+    if t.dim() != 3 or t.shape[0] != batch.desc.n_seqs or t.shape[1] != cache.desc.n_kv_heads:
+        raise ValueError("%s: shape %s, expected [%d][%d][n]" % (what, tuple(t.shape), batch.desc.n_seqs,
+                                                                cache.desc.n_kv_heads))
+    return _dev_ptr(t), int(t.shape[2])
+
+
+def _check_table(cache: KvCache, batch: KvBatch):
+    if batch.table.shape[2] != cache.desc.n_kv_heads:
+        raise ValueError("table: %d heads, the cache has %d" % (batch.table.shape[2], cache.desc.n_kv_heads))
+
+
+def prepare_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, scale: float, window: int = 0,
+                     decay: float = 1.0, before=None, workspace=None) -> PreparedCall:
+    _check_table(cache, batch)
+    qp, q_ld = _kv_rows(cache, batch, q, "q")
+    heads = int(q.shape[1])
+    _check_tensor(lse, "lse", 0, batch.desc.n_tokens * heads)
+    wt, w_ld = _token_weights(cache, batch, weights, "weights")
+    old = None
+    if before is not None:
+        old, ld = _token_weights(cache, batch, before, "before")
+        if ld != w_ld:
+            raise ValueError("before: %d entries a head, weights has %d" % (ld, w_ld))
+    wp, wb = _ws(workspace)
+    return PreparedCall(_lib.lora_kv_weigh,
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, q_ld, heads, float(scale),
+                         _window(window), _dev_ptr(lse), float(decay), old, wt, w_ld, wp, wb),
+                        "lora_kv_weigh", (cache, batch, q, lse, weights, before, workspace))
+
+
+def prepare_kv_select(cache: KvCache, batch: KvBatch, weights, budget: int, keep, n_keep, sinks: int = 0,
+                      recent: int = 0, workspace=None) -> PreparedCall:
+    _check_table(cache, batch)
+    wt, w_ld = _token_weights(cache, batch, weights, "weights")
+    _check_int32(keep, "keep", 0)
+    _check_int32(n_keep, "n_keep", batch.desc.n_seqs)
+    if keep.dim() != 3 or keep.shape[0] != batch.desc.n_seqs or keep.shape[1] != cache.desc.n_kv_heads:
+        raise ValueError("keep: shape %s, expected [%d][%d][n]" % (tuple(keep.shape), batch.desc.n_seqs,
+                                                                  cache.desc.n_kv_heads))
+    wp, wb = _ws(workspace)
+    return PreparedCall(_lib.lora_kv_select,
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), wt, w_ld, int(budget),
+                         int(sinks), int(recent), _dev_ptr(keep), int(keep.shape[2]), _dev_ptr(n_keep), wp, wb),
+                        "lora_kv_select", (cache, batch, weights, keep, n_keep, workspace))
+
+
+def prepare_kv_compact(cache: KvCache, batch: KvBatch, keep, n_keep, from_new: bool = False,
+                       weights=None) -> PreparedCall:
+    _check_table(cache, batch)
+    _check_int32(keep, "keep", 0)
+    _check_int32(n_keep, "n_keep", batch.desc.n_seqs)
+    if keep.dim() not in (2, 3) or keep.shape[0] != batch.desc.n_seqs:
+        raise ValueError("keep: shape %s, expected [%d][1 or n_kv_heads][n]" % (tuple(keep.shape), batch.desc.n_seqs))
+    wt, w_ld = (None, 0) if weights is None else _token_weights(cache, batch, weights, "weights")
+    return PreparedCall(_lib.lora_kv_compact,
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), _dev_ptr(keep),
+                         1 if keep.dim() == 2 else int(keep.shape[1]), int(keep.shape[-1]), _dev_ptr(n_keep),
+                         int(bool(from_new)), wt, w_ld),
+                        "lora_kv_compact", (cache, batch, keep, n_keep, weights))
 
 
 def prepare_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out,
@@ -885,6 +1103,38 @@ def prepare_spec_verify(q_start, drafted, target, draft, u_accept, u_sample, tok
     wp, wb = _ws(workspace)
     return PreparedCall(_lib.lora_spec_verify, (ctypes.byref(d), wp, wb), "lora_spec_verify",
                         (d, q_start, drafted, target, draft, u_accept, u_sample, tokens, n_out, workspace))
+
+
+def _probability_rows(target):
+    """(dtype code, rows, vocab, elements between rows) of a [n_tokens][vocab] tensor."""
+    import torch
+    code = {torch.float32: LORA_F32, torch.float16: LORA_F16, torch.bfloat16: LORA_BF16}
+    if target.dtype not in code:
+        raise TypeError("target: dtype %s" % target.dtype)
+    if target.dim() != 2 or target.stride(1) != 1 or not target.is_cuda:
+        raise ValueError("target: expected a device tensor [n_tokens][vocab] with contiguous rows")
+    n, vocab = (int(x) for x in target.shape)
+    return code[target.dtype], n, vocab, int(target.stride(0)) if n > 1 else vocab
+
+
+def prepare_spec_verify_tree(q_start, parent, drafted, target, u_accept, u_sample, tokens, path, n_out,
+                             workspace) -> PreparedCall:
+    code, n, vocab, ld = _probability_rows(target)
+    n_seqs = int(u_sample.numel())
+    if tokens.dim() != 2 or tuple(tokens.shape) != tuple(path.shape) or tokens.shape[0] != n_seqs:
+        raise ValueError("tokens and path: shapes %s and %s, expected [%d][most]" % (
+            tuple(tokens.shape), tuple(path.shape), n_seqs))
+    for t, what, need in ((q_start, "q_start", n_seqs + 1), (parent, "parent", n), (drafted, "drafted", n),
+                          (tokens, "tokens", 0), (path, "path", 0), (n_out, "n_out", n_seqs)):
+        _check_int32(t, what, need)
+    _check_tensor(u_accept, "u_accept", 0, n)
+    _check_tensor(u_sample, "u_sample", 0, n_seqs)
+    d = TreeVerifyDesc(n_seqs, n, vocab, code, int(tokens.shape[1]), 0, ld, _dev_ptr(q_start), _dev_ptr(parent),
+                       _dev_ptr(drafted), target.data_ptr(), _dev_ptr(u_accept), _dev_ptr(u_sample), _dev_ptr(tokens),
+                       _dev_ptr(path), _dev_ptr(n_out))
+    wp, wb = _ws(workspace)
+    return PreparedCall(_lib.lora_spec_verify_tree, (ctypes.byref(d), wp, wb), "lora_spec_verify_tree",
+                        (d, q_start, parent, drafted, target, u_accept, u_sample, tokens, path, n_out, workspace))
 
 
 # ----------------------------------------------------------------------------

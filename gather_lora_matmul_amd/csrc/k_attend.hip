@@ -28,60 +28,14 @@
 #include <type_traits>
 
 #include "kcommon.h"
-#include "kv.h"
+#include "kvtiles.h"
 #include "per_device.h"
 
 namespace lora {
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ u32x4 ldv(const void* p) { return *reinterpret_cast<const u32x4*>(p); }
-
 constexpr float kLn2 = 0.69314718055994530942f;
-
-template <typename T>
-__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, f32x4 c) {
-  if constexpr (std::is_same<T, bf16_t>::value)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-template <typename T>
-__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, f32x16 c) {
-  if constexpr (std::is_same<T, bf16_t>::value)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-// Eight FP8 codes (two words) -> eight 16-bit values, exact.
-template <typename T>
-__device__ __forceinline__ u32x4 fp8_to16(uint32_t w0, uint32_t w1) {
-  u32x4 r;
-  if constexpr (std::is_same<T, bf16_t>::value) {
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true));
-  } else {
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true));
-  }
-  return r;
-}
 
 // 2^(byte - 127), less `down` (0 or 1) in the exponent.
 __device__ __forceinline__ float scale_of(uint32_t byte, int down) {
@@ -171,12 +125,6 @@ __device__ __forceinline__ uint32_t nan_codes(const u32x4& u) {
   constexpr uint32_t kM = 0x7f7f7f7fu, kO = 0x01010101u;
   return (((u.x & kM) + kO) | ((u.y & kM) + kO) | ((u.z & kM) + kO) | ((u.w & kM) + kO)) & 0x80808080u;
 }
-// Bits of the N tokens from k0 on that lie in [lo, up].
-template <int N>
-__device__ __forceinline__ uint32_t run_bits(int k0, int lo, int up) {
-  const int x = min(max(lo - k0, 0), N), y = min(max(up - k0 + 1, 0), N);
-  return ((1u << y) - 1u) & ~((1u << x) - 1u);
-}
 // Not zero if one of eight values is not finite: adding one to an exponent of all
 // ones carries into the sign's place.
 template <typename T>
@@ -215,27 +163,27 @@ struct PartDesc {        // a tile whose last of several parts a block has
   int32_t share;         // groups of lanes of the joining launch that a row gets
 };
 
-__device__ __forceinline__ int token_of(const AttendArgs& a, int row) {  // row / group
-  return a.group == 1 ? row : (int)(__umulhi((uint32_t)row, a.group_m) >> a.group_s);
-}
-// A value that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// The arguments say whether rows see the tokens up to their own (AttendArgs) or those of
+// their own tree (TreeArgs): each is a kernel of its own.
+template <class AA>
+constexpr bool is_tree = std::is_same<AA, TreeArgs>::value;
 
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
 // row's window, down to a multiple of KU, to the last row's own position or the
-// table's end.
-template <int KU>
-__device__ __forceinline__ void tile_keys(const AttendArgs& a, const KvSeq& q, int row0, int rows,
+// table's end.  Rows of a tree: from the window of a token of depth 0 to the last new token.
+template <int KU, class AA>
+__device__ __forceinline__ void tile_keys(const AA& a, const KvSeq& q, int row0, int rows,
                                           int& lo, int& hi) {
-  const int t0 = token_of(a, row0), t1 = token_of(a, row0 + rows - 1);
+  const int t0 = is_tree<AA> ? 0 : token_of(a, row0);
+  const int t1 = is_tree<AA> ? q.q_len - 1 : token_of(a, row0 + rows - 1);
   hi = min(q.base + t1 + 1, q.end);
   lo = 0;
   if (a.window > 0 && q.base + t0 + 1 - a.window > 0)
     lo = min(q.base + t0 + 1 - a.window, max(q.end - 1, 0)) / KU * KU;
   if (hi <= lo) hi = lo + 1;  // nothing is seen: one unit, all of it masked
 }
-template <int KU, int TR>
-__device__ __forceinline__ int tile_units(const AttendArgs& a, const KvSeq& q, int tile) {
+template <int KU, int TR, class AA>
+__device__ __forceinline__ int tile_units(const AA& a, const KvSeq& q, int tile) {
   const int row0 = tile * TR, rows = min(TR, q.q_len * a.group - row0);
   if (rows <= 0) return 0;
   int lo, hi;
@@ -277,8 +225,8 @@ struct Cut {               // ("block": the worker, which may be a wave)
 // the workers of one XCD: they walk the same keys at the same time, which ranges cut
 // anywhere do not, and find them in their L2 (a chunk of 2048 tokens over 16384, 8
 // heads: 54 % of the L2's reads missed without it).
-template <int KU, int TR, int THREADS>
-__device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, int workers, int i,
+template <int KU, int TR, int THREADS, class AA>
+__device__ __forceinline__ void cut_work(const AA& a, int* pre, Cut& c, int workers, int i,
                                          int* preT = nullptr) {
   const int n = a.kv.n_seqs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -395,8 +343,8 @@ __device__ __forceinline__ void cut_work(const AttendArgs& a, int* pre, Cut& c, 
 
 // The next piece of the range; advances c.  Sequences without units are passed.
 // Every wave computes it for itself, with all its lanes.
-template <int KU, int TR>
-__device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, Cut& c, Piece& p,
+template <int KU, int TR, class AA>
+__device__ __forceinline__ bool next_piece(const AA& a, const int* pre, Cut& c, Piece& p,
                                            const int* preT = nullptr) {
   if (preT && c.tile < c.tiles) {
     const int n = a.kv.n_seqs, lane = threadIdx.x & 63;
@@ -468,6 +416,44 @@ __device__ __forceinline__ bool next_piece(const AttendArgs& a, const int* pre, 
   p.first = p.begins ? c.block : c.block_of(p.start);
   c.pos += take;
   return true;
+}
+
+// What a row of a tree sees: of the tokens before the new ones those within the window of
+// its depth, of the new ones (u at base + u) those whose bits its row of `seen` has.  Both
+// are read where a tile is not seen whole by all rows, and held nowhere: the kernels have no
+// registers left for them.
+__device__ __forceinline__ int tree_depth(const TreeArgs& a, int row) {
+  return a.window > 0 ? min(max(a.depth[row], 0), 1 << 24) : 0;
+}
+// The first token of the window of row t of a sequence.
+__device__ __forceinline__ int tree_from(const TreeArgs& a, const KvSeq& q, int t) {
+  return a.window > 0 ? q.base + tree_depth(a, q.q0 + t) + 1 - a.window : -(1 << 30);
+}
+// Bits of the 64 tokens from k0 on that row t sees.
+__device__ __forceinline__ uint64_t tree_sees(const TreeArgs& a, const KvSeq& q, int t, int k0) {
+  auto below = [](int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); };   // bits 0 .. n - 1
+  const uint64_t* words = a.seen + (int64_t)(q.q0 + t) * a.words;
+  const int rel = k0 - q.base, off = rel & 63, w = rel >> 6;
+  const uint64_t x = (unsigned)w < (unsigned)a.words ? words[w] : 0ull;
+  const uint64_t y = off && (unsigned)(w + 1) < (unsigned)a.words ? words[w + 1] : 0ull;
+  uint64_t bits = below(-rel) & ~below(tree_from(a, q, t) - k0);
+  bits |= (x >> off) | (off ? y << (64 - off) : 0ull);
+  return bits & below(q.q_len - rel);
+}
+// Of the N <= 16 tokens from k0 on.
+template <int N>
+__device__ __forceinline__ uint32_t tree_sees_few(const TreeArgs& a, const KvSeq& q, int t, int k0) {
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(a.seen + (int64_t)(q.q0 + t) * a.words);
+  const int rel = k0 - q.base, w = rel >> 5;
+  const uint32_t x = (unsigned)w < 2u * (unsigned)a.words ? words[w] : 0u;
+  const uint32_t y = (unsigned)(w + 1) < 2u * (unsigned)a.words ? words[w + 1] : 0u;
+  const uint32_t bits = __builtin_amdgcn_alignbit(y, x, (uint32_t)rel & 31u);
+  return (bits & run_bits<N>(rel, 0, q.q_len - 1)) | run_bits<N>(k0, tree_from(a, q, t), q.base - 1);
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x = max(x, __shfl_xor(x, d));
+  return x;
 }
 
 // Partial results of a block: slot 0 its first piece, slot 1 its last one if
@@ -543,12 +529,13 @@ __device__ __forceinline__ const char* eight_values(const KvView& kv, const int3
 }
 // The wave's results o of rows that see the tokens lo .. hi of a piece's keys each and
 // [all_lo, all_hi] in common (the same in all lanes): element i of o[n] is number
-// dim(n E + i) of the head's.  Only lanes with `mine` are settled (a row whose scores are
+// dim(n E + i) of the head's; of those outside the common ones the lane's row sees the
+// eight from t on that eight(t) has bits of.  Only lanes with `mine` are settled (a row whose scores are
 // not finite is NaN).  The common tokens are walked once, all columns at a
 // time; the few others of a row (as many as the wave's rows are apart) by its lanes.
-template <typename A, int D, typename V, int N, typename Dim>
+template <typename A, int D, typename V, int N, typename Dim, typename Eight>
 __device__ __forceinline__ void settle(const KvView& kv, const int32_t* ktab, const int32_t* vtab, int lo, int hi,
-                                       int all_lo, int all_hi, bool mine, V (&o)[N], Dim dim) {
+                                       int all_lo, int all_hi, bool mine, V (&o)[N], Dim dim, Eight eight) {
   constexpr int E = sizeof(V) / sizeof(float), C = D / 64, U = 4;
   const int lane = threadIdx.x & 63;
   uint32_t found[C] = {};
@@ -596,7 +583,7 @@ __device__ __forceinline__ void settle(const KvView& kv, const int32_t* ktab, co
       for (int t = from & ~7; t <= to; t += 8) {
         uint32_t see;
         const char* src = eight_values(kv, ktab, vtab, D, t, from, to, see);
-        f |= classes_of<A>(ldv(src + d * 16), see);
+        f |= classes_of<A>(ldv(src + d * 16), see & eight(t));
       }
     }
 #pragma unroll
@@ -807,8 +794,8 @@ struct Skinny {
   using PT = typename std::conditional<Q8, bf16_t, A>::type;  // type of P and V in the second one
 };
 
-template <typename A, typename KV, int D, bool SOLO>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_rows(AttendArgs a) {
+template <typename A, typename KV, int D, bool SOLO, class AA>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_rows(AA a) {
   using S = Skinny<A, KV, D, SOLO>;
   using PT = typename S::PT;
   constexpr int E = S::E, KT = S::KT, KU = S::KU, TR = S::TR, NT = S::NT, NC = S::NC, ND = S::ND;
@@ -833,9 +820,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int row = p.row0 + min(col, p.rows - 1);
     const int tq = token_of(a, row);
     const int pos = p.q.base + tq;
-    const int posmin = p.q.base + token_of(a, p.row0);
-    const int posmax = p.q.base + token_of(a, p.row0 + p.rows - 1);
+    // (rows of a tree: all see the token before the new ones, and none is past the last new one)
+    const int posmin = is_tree<AA> ? p.q.base - 1 : p.q.base + token_of(a, p.row0);
+    const int posmax = is_tree<AA> ? p.q.base + p.q.q_len - 1 : p.q.base + token_of(a, p.row0 + p.rows - 1);
     const int win = a.window > 0 ? a.window : 0x40000000;
+    int deep = posmax;   // position of the deepest row: tokens from deep - win + 1 on are in every window
+    if constexpr (is_tree<AA>) deep = p.q.base + uni(wave_max(tree_depth(a, p.q.q0 + tq)));
     u32x4 qf[S::NQ];
     {
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(p.q.q0 + tq) * a.q_ld +
@@ -913,17 +903,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (; tile < p.key1; tile += KU) {
       const bool more = tile + KU < p.key1;
       const bool kbad = (unsigned)id.kp >= (unsigned)kv.n_pages, vbad = (unsigned)id.vp >= (unsigned)kv.n_pages;
-      const bool edge = tile + KT - 1 > posmin || tile <= posmax - win || __ballot(kbad || vbad);
+      const bool edge = tile + KT - 1 > posmin || tile <= deep - win || __ballot(kbad || vbad);
       uint32_t seen = 0xffffu;   // of the lane's tokens g E + e: seen by the lane's row
       if (edge) {
         // group g's K page is known to the lanes with col / 4 == g
         const unsigned long long kb = __ballot(kbad);
         const bool gone = vbad || ((kb >> (g * 4)) & 1);
         const int k0 = tile + g * E;
-        seen = gone ? 0u : run_bits<E>(k0, pos - win + 1, pos);
         // what no row sees is taken out of V (0 times what lies there need not be 0);
         // values that are not finite go to the rows that see them, then they leave V
-        const uint32_t live = gone ? 0u : run_bits<E>(k0, posmin - win + 1, min(posmax, p.key1 - 1));
+        uint32_t live;
+        if constexpr (is_tree<AA>) {
+          seen = gone ? 0u : tree_sees_few<E>(a, p.q, tq, k0);
+          live = seen;
+#pragma unroll
+          for (int x = 1; x < 16; x <<= 1) live |= (uint32_t)__shfl_xor((int)live, x);
+        } else {
+          seen = gone ? 0u : run_bits<E>(k0, pos - win + 1, pos);
+          live = gone ? 0u : run_bits<E>(k0, posmin - win + 1, min(posmax, p.key1 - 1));
+        }
         uint32_t odd = 0;
 #pragma unroll
         for (int n = 0; n < ND; ++n) {
@@ -1054,9 +1052,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if (std::is_same<PT, f16_t>::value) m -= 7.f;   // the exponents' origin
     if constexpr (!Q8) {
       const bool mine = residue(o) != 0.f && l < INFINITY;
-      if (__builtin_expect(__ballot(mine) != 0, 0))
-        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
-                     min(posmin, p.key1 - 1), mine, o, [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); });
+      if (__builtin_expect(__ballot(mine) != 0, 0)) {
+        const auto dim = [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); };
+        if constexpr (is_tree<AA>)
+          settle<A, D>(kv, ktab, vtab, max(tree_from(a, p.q, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, p.q, tq, t); });
+        else
+          settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [](int) { return 0xffu; });
+      }
     }
     if constexpr (SOLO) {
       const int slot = n_piece == 0 ? 0 : 1;
@@ -1156,11 +1160,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // with two the chunk takes 1493 us against 1011 in turn, and what one costs is that an
 // output's error grows from its own rounding's to 1.4 times that.  A caller who wants two
 // gets four waves, which take as long.
-__device__ __forceinline__ void load_lds16(const void* src, void* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
-
 // Eight FP8 codes times a power of two -> eight 16-bit values.
 template <typename T>
 __device__ __forceinline__ u32x4 fp8_to16s(uint32_t w0, uint32_t w1, float sc) {
@@ -1249,8 +1248,8 @@ struct Tiles {
   };
 };
 
-template <typename A, typename KV, int D, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_tiles(AttendArgs a) {
+template <typename A, typename KV, int D, int NW, class AA>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attend_tiles(AA a) {
   using TT = Tiles<A, KV, D, NW>;
   constexpr bool Q8 = is_quant<KV>();
   constexpr int TR = TT::TR, KU = TT::KU, NIDS = TT::NIDS;
@@ -1300,8 +1299,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const int tq = token_of(a, row);
     const int pos = base + tq;
     const int win = a.window > 0 ? a.window : 0x40000000;
-    const int posmin = base + token_of(a, wrow0);
-    const int posmax = base + token_of(a, wrow0 + max(wrows, 1) - 1);
+    // (rows of a tree: all see the token before the new ones, and none is past the last new one)
+    const int posmin = is_tree<AA> ? base - 1 : base + token_of(a, wrow0);
+    const int posmax = is_tree<AA> ? base + p.q.q_len - 1 : base + token_of(a, wrow0 + max(wrows, 1) - 1);
     u32x4 qf[NQ];
     {
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(p.q.q0 + tq) * a.q_ld +
@@ -1311,7 +1311,20 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
     const int32_t* ktab = kv.table + ((int64_t)p.seq * 2 * kv.H + p.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-    const int bmin = base + token_of(a, p.row0), bmax = base + token_of(a, p.row0 + p.rows - 1);
+    const int bmin = is_tree<AA> ? base - 1 : base + token_of(a, p.row0);
+    const int bmax = is_tree<AA> ? base + p.q.q_len - 1 : base + token_of(a, p.row0 + p.rows - 1);
+    // positions of the deepest rows of the block and of the wave
+    int bdeep = bmax, deep = posmax;
+    if constexpr (is_tree<AA>) {
+      bdeep = deep = base;
+      if (a.window > 0) {
+        const int t0 = token_of(a, p.row0), t1 = token_of(a, p.row0 + p.rows - 1);
+        int most = 0;
+        for (int t = t0 + lane; t <= t1; t += 64) most = max(most, tree_depth(a, p.q.q0 + t));
+        bdeep = base + uni(wave_max(most));
+        deep = base + uni(wave_max(tree_depth(a, p.q.q0 + tq)));
+      }
+    }
     // ---- page ids of the blocks from b0 on, in LDS (absent ones as they are).  Blocks
     // before the first row's window may be given back without any care
     const int vis0 = a.window > 0 ? bmin - a.window + 1 : 0;
@@ -1402,7 +1415,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     commit_k(0);
     commit_v(0);
     // tiles from clean0 to before clean1 are seen whole by all rows of the block, if their pages are there
-    const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bmax - a.window + 1 : 0;
+    const int clean1 = bmin - KU + 2, clean0 = a.window > 0 ? bdeep - a.window + 1 : 0;
     auto is_edge = [&](int tile) { return tile < clean0 || tile >= clean1 || any_bad; };
     auto sees = [&](int tile) {   // this wave's rows see something of it
       return wrows > 0 && tile <= posmax && tile + KU - 1 > posmin - win;
@@ -1410,7 +1423,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     // An edge tile's V before the products: tokens that no row of the block sees are
     // taken out in LDS (0 times what lies there need not be 0), and what is not finite
     // goes to the rows that see it.  Returns the tokens without pages.
-    auto clean = [&](int tile, int slot) {
+    auto clean = [&](int tile, int slot) __attribute__((always_inline)) {
       unsigned long long bad = 0;
       if (__builtin_expect(any_bad, 0)) {
         const int b = (int)kv_div(kv, (uint32_t)(tile + lane)) - b0;
@@ -1438,7 +1451,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
-            const u32x4 vis = ones8<A>(run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0));
+            uint32_t see;
+            if constexpr (is_tree<AA>) see = (uint32_t)(tree_sees(a, p.q, tq, tile) >> k0) & 0xffu;
+            else see = run_bits<8>(k0, pos - win + 1 - tile, pos - tile);
+            const u32x4 vis = ones8<A>(see & ~(uint32_t)(bad >> k0));
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
               const u32x4 v = sh.v[slot][2 * q + hi][n * 32 + col];
@@ -1458,11 +1474,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
       }
       return bad;
     };
-    auto mask = [&](f32x16(&s)[2], int tile, unsigned long long bad) {
+    auto mask = [&](f32x16(&s)[2], int tile, unsigned long long bad) __attribute__((always_inline)) {
+      uint64_t row = 0;
+      if constexpr (is_tree<AA>) row = tree_sees(a, p.q, tq, tile) & ~(uint64_t)bad;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
-        const uint32_t seen = run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
+        uint32_t seen;
+        if constexpr (is_tree<AA>) seen = (uint32_t)(row >> k0) & 0xffu;
+        else seen = run_bits<8>(k0, pos - win + 1 - tile, pos - tile) & ~(uint32_t)(bad >> k0);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
           if (!((seen >> r) & 1)) s[h >> 1][8 * (h & 1) + r] = -INFINITY;
@@ -1570,7 +1590,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
       // One tile, whose scores s the step before has computed; sn becomes the next tile's.
       // K is loaded two tiles ahead, V one.  The step before the first tile only does the
       // latter.
-      auto step = [&](auto parity, f32x16(&s)[2], f32x16(&sn)[2], const int tile, const bool before) {
+      auto step = [&](auto parity, f32x16(&s)[2], f32x16(&sn)[2], const int tile, const bool before)
+          __attribute__((always_inline)) {
         constexpr int par = decltype(parity)::value;
         const bool kmore = tile + 2 * KU < p.key1, vmore = !before && tile + KU < p.key1;
         arrived();
@@ -1668,10 +1689,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     if (std::is_same<A, f16_t>::value) m -= 7.f;   // the exponents' origin
     if constexpr (!Q8) {
       const bool mine = residue(o) != 0.f && l < INFINITY;
-      if (__builtin_expect(__ballot(mine) != 0, 0))
-        settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
-                     min(posmin, p.key1 - 1), mine, o,
-                     [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); });
+      if (__builtin_expect(__ballot(mine) != 0, 0)) {
+        const auto dim = [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); };
+        if constexpr (is_tree<AA>)
+          settle<A, D>(kv, ktab, vtab, max(tree_from(a, p.q, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, p.q, tq, t); });
+        else
+          settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [](int) { return 0xffu; });
+      }
     }
     const bool whole = p.begins && p.ends;
     if (col < wrows) {
@@ -1746,8 +1772,8 @@ inline bool wide_tiles(const AttendArgs& a, int blocks) {
   return rows / 256 * a.kv.H * (keys / 64) >= 24 * (int64_t)blocks;
 }
 
-template <typename A, typename KV, int D, int NW>
-hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
+template <typename A, typename KV, int D, int NW, class AA>
+hipError_t launch_tiles(const AA& a, int G, hipStream_t s) {
   using TT = Tiles<A, KV, D, NW>;
   const size_t lds = sizeof(typename TT::Shared);
   static PerDevice limit;   // the kernel's LDS, more than a block gets unasked, is a setting of each device
@@ -1755,11 +1781,11 @@ hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
   hipError_t e = hipGetDevice(&device);
   if (e == hipSuccess)
     e = limit.done(device, [&] {
-      return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D, NW>),
+      return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_tiles<A, KV, D, NW, AA>),
                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW>), dim3(G), dim3(NW * 64), lds, s, a);
+  hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW, AA>), dim3(G), dim3(NW * 64), lds, s, a);
   // tiles of which none has many parts: four blocks each; else the list.  Measured
   // (us of a call, list / this): 32 sequences of 5 x 8 rows over 2500 tokens 78.4 / 76.1,
   // 2 of 256 x 8 rows over 4096 130 / 126, 64 x 4 rows of 8 heads over 2000 33.6 / 83.6,
@@ -1776,29 +1802,36 @@ hipError_t launch_tiles(const AttendArgs& a, int G, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename A, typename KV, int D>
-hipError_t launch(const AttendArgs& a, hipStream_t s) {
+template <typename A, typename KV, int D, class AA>
+hipError_t launch(const AA& a, hipStream_t s) {
   const int64_t most = std::min<int64_t>((int64_t)a.max_q_len * a.group, 16);   // rows of a tile
   const bool few = few_rows(is_quant<KV>(), a.group, a.max_q_len);
   const int G = blocks_of(a.n_cu);
   if (few && solo_waves(a.kv.n_seqs, a.kv.H, a.n_cu)) {
-    hipLaunchKernelGGL((k_attend_rows<A, KV, D, true>), dim3(G), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attend_rows<A, KV, D, true, AA>), dim3(G), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(4 * G, (unsigned)most), dim3(256), 0, s, a, 4 * G);
   } else if (few) {
-    hipLaunchKernelGGL((k_attend_rows<A, KV, D, false>), dim3(G), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attend_rows<A, KV, D, false, AA>), dim3(G), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_attend_join<A, D, 16, 1>), dim3(G, (unsigned)most), dim3(256), 0, s, a, G);
   } else {
     // FP8 of 64 elements has too few loads in a tile for eight waves
     constexpr bool wide = D / ET<KV>::E % 8 == 0;
-    if (wide && wide_tiles(a, G / 16 * 8)) return launch_tiles<A, KV, D, wide ? 8 : 4>(a, G / 16 * 8, s);
-    return launch_tiles<A, KV, D, 4>(a, G, s);
+    if (wide && wide_tiles(a, G / 16 * 8)) return launch_tiles<A, KV, D, wide ? 8 : 4, AA>(a, G / 16 * 8, s);
+    return launch_tiles<A, KV, D, 4, AA>(a, G, s);
   }
   return hipGetLastError();
 }
 
-template <typename A, typename KV>
-hipError_t launch_d(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {
+template <typename A, typename KV, class AA>
+hipError_t launch_d(const KvTypes& ty, const AA& a, hipStream_t s) {
   return ty.D == 128 ? launch<A, KV, 128>(a, s) : launch<A, KV, 64>(a, s);
+}
+
+template <class AA>
+hipError_t launch_types(const KvTypes& ty, const AA& a, hipStream_t s) {
+  const bool q = ty.kv == LORA_FP8_E4M3;
+  if (ty.act == LORA_F16) return q ? launch_d<f16_t, fp8_t>(ty, a, s) : launch_d<f16_t, f16_t>(ty, a, s);
+  return q ? launch_d<bf16_t, fp8_t>(ty, a, s) : launch_d<bf16_t, bf16_t>(ty, a, s);
 }
 
 }  // namespace
@@ -1818,10 +1851,7 @@ int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len) {
   return tiles * v.H * ((int64_t)v.nb * v.T / KU + 2);
 }
 
-hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s) {
-  const bool q = ty.kv == LORA_FP8_E4M3;
-  if (ty.act == LORA_F16) return q ? launch_d<f16_t, fp8_t>(ty, a, s) : launch_d<f16_t, f16_t>(ty, a, s);
-  return q ? launch_d<bf16_t, fp8_t>(ty, a, s) : launch_d<bf16_t, bf16_t>(ty, a, s);
-}
+hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s) { return launch_types(ty, a, s); }
+hipError_t launch_attend_tree(const KvTypes& ty, const TreeArgs& a, hipStream_t s) { return launch_types(ty, a, s); }
 
 }  // namespace lora

@@ -198,11 +198,14 @@ __device__ __forceinline__ void sum_regions(const VerifyArgs& a, const VerifyRow
   }
 }
 
+// floor(total * part / 2^31)
+__device__ __forceinline__ uint64_t part_of(uint64_t total, uint64_t part) {
+  return (total >> 31) * part + (((total & 0x7fffffffull) * part) >> 31);
+}
 // From the regions' sums (LDS) to the token, by one wave: total, level, region,
 // token.  -2: all weights are 0.
-template <typename T, bool SELF>
-__device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows& w, int regions,
-                                    const uint64_t* sums) {
+template <typename F>
+__device__ __forceinline__ int pick_from(float u, int regions, const uint64_t* sums, F rest) {
   const int lane = threadIdx.x & 63;
   constexpr int N = kMaxRegions / 64;
   uint64_t own = 0, x[N];
@@ -215,10 +218,9 @@ __device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows
   const uint64_t end = wave_scan(own);
   const uint64_t total = __shfl(end, 63);
   if (total == 0) return -2;
-  float u = a.u_sample[s];
   u = u > 0.f ? (u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f) : 0.f;
   const uint64_t part = (uint64_t)(uint32_t)(u * 0x1p31f);
-  const uint64_t level = (total >> 31) * part + (((total & 0x7fffffffull) * part) >> 31);
+  const uint64_t level = part_of(total, part);
   // the lane, then its region, that pass the level (total > level, so there is one)
   const int src = __builtin_ctzll(__ballot(end > level));
   uint64_t before = end - own;
@@ -236,7 +238,7 @@ __device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows
   const int region = __shfl(lane * N + at, src);
   before = __shfl(before, src);
   float f[8];
-  region_rest<T, SELF>(w, region, a.vocab, f);
+  rest(region, f);
   uint64_t y[8], sum = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -254,6 +256,11 @@ __device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows
     if (c > level && tok == 7) tok = j;
   }
   return __shfl(region * kRegion + lane * 8 + tok, tl);
+}
+template <typename T, bool SELF>
+__device__ __forceinline__ int pick(const VerifyArgs& a, int s, const VerifyRows& w, int regions,
+                                    const uint64_t* sums) {
+  return pick_from(a.u_sample[s], regions, sums, [&](int region, float* f) { region_rest<T, SELF>(w, region, a.vocab, f); });
 }
 
 // The token and the outputs of one sequence, from the regions' sums in LDS.
@@ -354,7 +361,211 @@ hipError_t launch(const VerifyArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- trees -------------------------------------------------------------------------
+// At a node the children are tried in their order: with L the weight that those refused
+// before have left of 2^44, child c is accepted if floor(L floor(2^31 u) / 2^31) < w(c); a
+// refused one's token loses its weight.  The walk goes on at the accepted child; where
+// none is, the token is drawn from what is left of the node's row.
+struct TreeWalk {
+  int q0, n;        // first row, tokens (0: none)
+  int node, count;  // the last accepted token, tokens of the path
+  int refused;      // children of it that had a weight and lost it
+};
+struct TreeShared {
+  uint64_t w[kTreeTokens];    // weight of a token in its parent's row
+  float u[kTreeTokens];
+  int token[kTreeTokens];
+  int16_t up[kTreeTokens];
+  int16_t path[kTreeTokens];
+  int16_t gone[kTreeTokens];  // the refused ones
+  TreeWalk walk;
+};
+
+// The accepted path of one sequence, in every wave.  All of a block's threads call it.
+template <typename T, int THREADS>
+__device__ __forceinline__ TreeWalk walk_tree(const TreeVerifyArgs& a, int s, TreeShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  int b = a.q_start[s], e = a.q_start[s + 1];
+  b = b < 0 ? 0 : (b > a.n_tokens ? a.n_tokens : b);
+  e = e < b ? b : (e > a.n_tokens ? a.n_tokens : e);
+  const int n = min(e - b, kTreeTokens);
+  for (int t = tid; t < n; t += THREADS) {
+    const int p = t ? a.parent[b + t] : -1, tok = a.drafted[b + t];
+    const float u = a.u_accept[b + t];
+    uint64_t w = 0;
+    if (p >= 0 && p < t && (unsigned)tok < (unsigned)a.vocab) {
+      const Weight x = fixed44(prob<T>(a.target, (int64_t)(b + p) * a.target_ld + tok));
+      w = whole(x.hi, x.lo);
+    }
+    sh.up[t] = (int16_t)(p >= 0 && p < t ? p : -1);
+    sh.token[t] = tok;
+    sh.u[t] = u;
+    sh.w[t] = w;
+  }
+  __syncthreads();
+  if (tid < 64) {
+    TreeWalk r{b, n, 0, n > 0 ? 1 : 0, 0};
+    if (lane == 0) sh.path[0] = 0;
+    bool on = n > 0;
+    while (on && r.count < a.path_ld) {
+      on = false;
+      r.refused = 0;
+      uint64_t left = (uint64_t)1 << 44;
+      for (int t0 = (r.node + 1) & ~63; t0 < n && !on; t0 += 64) {
+        const int t = t0 + lane;
+        unsigned long long kids = __ballot(t < n && t > r.node && sh.up[t] == r.node);
+        for (; kids; kids &= kids - 1) {
+          const int k = t0 + __builtin_ctzll(kids), tok = sh.token[k];
+          uint64_t w = sh.w[k];
+          bool again = false;   // refused before: no weight left
+          for (int i = lane; i < r.refused; i += 64) again |= sh.token[sh.gone[i]] == tok;
+          if (__ballot(again)) w = 0;
+          float u = sh.u[k];
+          u = u > 0.f ? (u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f) : 0.f;
+          if (part_of(left, (uint64_t)(uint32_t)(u * 0x1p31f)) < w) {
+            if (lane == 0) sh.path[r.count] = (int16_t)k;
+            ++r.count;
+            r.node = k;
+            r.refused = 0;
+            on = true;
+            break;
+          }
+          left = left > w ? left - w : 0;
+          if (w) {
+            if (lane == 0) sh.gone[r.refused] = (int16_t)k;
+            __builtin_amdgcn_wave_barrier();
+            ++r.refused;
+          }
+        }
+      }
+    }
+    if (lane == 0) sh.walk = r;
+  }
+  __syncthreads();
+  return sh.walk;
+}
+template <typename T>
+__device__ __forceinline__ VerifyRows tree_row(const TreeVerifyArgs& a, const TreeWalk& r) {
+  VerifyRows w;
+  w.p = reinterpret_cast<const char*>(a.target) + (int64_t)(r.q0 + r.node) * a.target_ld * ET<T>::bytes;
+  w.q = nullptr;
+  w.drop = -1;
+  return w;
+}
+
+// The token and the outputs of one sequence, from the sums of its last row's regions in LDS.
+template <typename T, int THREADS>
+__device__ __forceinline__ void finish_tree(const TreeVerifyArgs& a, int s, const TreeWalk& r, const VerifyRows& w,
+                                            int regions, uint64_t* sums, const TreeShared& sh, int* out) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid < 64) {
+    // the refused tokens (each once) leave the sums, and the region that is looked at again
+    auto move = [&](bool back) {
+      for (int i = lane; i < r.refused; i += 64) {
+        const int k = sh.gone[i];
+        unsigned long long* at = reinterpret_cast<unsigned long long*>(sums + sh.token[k] / kRegion);
+        atomicAdd(at, back ? (unsigned long long)sh.w[k] : 0ull - (unsigned long long)sh.w[k]);
+      }
+      __builtin_amdgcn_wave_barrier();
+    };
+    move(false);
+    const float u = a.u_sample[s];
+    int tok = pick_from(u, regions, sums, [&](int region, float* f) {
+      region_rest<T, true>(w, region, a.vocab, f);
+      const int v = region * kRegion + lane * 8;
+      for (int i = 0; i < r.refused; ++i) {
+        const int d = sh.token[sh.gone[i]] - v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = j == d ? 0.f : f[j];
+      }
+    });
+    if (tok == -2) {   // nothing is left: the row as it is
+      move(true);
+      tok = pick_from(u, regions, sums, [&](int region, float* f) { region_rest<T, true>(w, region, a.vocab, f); });
+      if (tok == -2) tok = -1;
+    }
+    if (lane == 0) *out = tok;
+  }
+  __syncthreads();
+  const int tok = *out;
+  for (int i = tid; i < a.path_ld; i += THREADS) {
+    const int64_t at = (int64_t)s * a.path_ld + i;
+    a.path[at] = i < r.count ? sh.path[i] : -1;
+    a.tokens[at] = i + 1 < r.count ? sh.token[sh.path[i + 1]] : (i + 1 == r.count ? tok : -1);
+  }
+  if (tid == 0) a.n_out[s] = r.count;
+}
+template <int THREADS>
+__device__ __forceinline__ void idle_tree(const TreeVerifyArgs& a, int s) {
+  for (int i = threadIdx.x; i < a.path_ld; i += THREADS) a.tokens[(int64_t)s * a.path_ld + i] = a.path[(int64_t)s * a.path_ld + i] = -1;
+  if (threadIdx.x == 0) a.n_out[s] = 0;
+}
+template <typename T>
+__device__ __forceinline__ void tree_sums(const TreeVerifyArgs& a, const VerifyRows& w, int first, int step, int regions,
+                                          uint64_t* sums) {
+  VerifyArgs v{};
+  v.vocab = a.vocab;
+  sum_regions<T, true>(v, w, first, step, regions, sums);
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void k_tree_one(TreeVerifyArgs a, int regions) {
+  __shared__ uint64_t sums[kMaxRegions];
+  __shared__ TreeShared sh;
+  __shared__ int out;
+  const int s = blockIdx.x;
+  const TreeWalk r = walk_tree<T, 1024>(a, s, sh);
+  if (r.n == 0) return idle_tree<1024>(a, s);
+  const VerifyRows w = tree_row<T>(a, r);
+  tree_sums<T>(a, w, (int)threadIdx.x >> 6, 16, regions, sums);
+  __syncthreads();
+  finish_tree<T, 1024>(a, s, r, w, regions, sums, sh, &out);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void k_tree_sums(TreeVerifyArgs a, uint64_t* __restrict__ ws, int regions) {
+  __shared__ TreeShared sh;
+  const int s = blockIdx.y;
+  const TreeWalk r = walk_tree<T, 256>(a, s, sh);
+  if (r.n == 0) return;
+  const VerifyRows w = tree_row<T>(a, r);
+  tree_sums<T>(a, w, blockIdx.x * 4 + ((int)threadIdx.x >> 6), gridDim.x * 4, regions, ws + (size_t)s * regions);
+}
+template <typename T>
+__global__ __launch_bounds__(512) void k_tree_pick(TreeVerifyArgs a, const uint64_t* __restrict__ ws, int regions) {
+  __shared__ uint64_t sums[kMaxRegions];
+  __shared__ TreeShared sh;
+  __shared__ int out;
+  const int s = blockIdx.x, tid = threadIdx.x;
+  const TreeWalk r = walk_tree<T, 512>(a, s, sh);
+  if (r.n == 0) return idle_tree<512>(a, s);
+  if (tid < regions) sums[tid] = ws[(size_t)s * regions + tid];
+  __syncthreads();
+  finish_tree<T, 512>(a, s, r, tree_row<T>(a, r), regions, sums, sh, &out);
+}
+
+template <typename T>
+hipError_t launch_tree(const TreeVerifyArgs& a, hipStream_t s) {
+  const int regions = (a.vocab + kRegion - 1) / kRegion;
+  if (a.vocab <= 32768 || a.n_seqs >= 192) {
+    hipLaunchKernelGGL((k_tree_one<T>), dim3(a.n_seqs), dim3(1024), 0, s, a, regions);
+  } else {
+    uint64_t* ws = reinterpret_cast<uint64_t*>(a.ws);
+    hipLaunchKernelGGL((k_tree_sums<T>), dim3((regions + 7) / 8, a.n_seqs), dim3(256), 0, s, a, ws, regions);
+    hipLaunchKernelGGL((k_tree_pick<T>), dim3(a.n_seqs), dim3(512), 0, s, a, ws, regions);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
+
+size_t tree_verify_workspace(int32_t n_seqs, int32_t vocab) {
+  return (size_t)n_seqs * ((vocab + kRegion - 1) / kRegion) * sizeof(uint64_t);
+}
+
+hipError_t launch_tree_verify(const TreeVerifyArgs& a, hipStream_t s) {
+  if (a.dtype == LORA_F32) return launch_tree<float>(a, s);
+  return a.dtype == LORA_F16 ? launch_tree<f16_t>(a, s) : launch_tree<bf16_t>(a, s);
+}
 
 size_t verify_workspace(int32_t n_seqs, int32_t vocab) {
   return (size_t)n_seqs * seq_words((vocab + kRegion - 1) / kRegion) * sizeof(uint64_t);

@@ -109,11 +109,19 @@ struct AttendArgs {
   char* ws;
   int32_t n_cu;
 };
+// Rows that are tokens of trees: which of their sequence's new tokens they see, and how
+// deep they are.
+struct TreeArgs : AttendArgs {
+  const uint64_t* seen;    // [n_tokens][words]
+  const int32_t* depth;    // [n_tokens], read if there is a window
+  int32_t words;
+};
 size_t attend_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len, int32_t n_seqs,
                         int32_t H);
 // A bound of the units of work of a call, to stay below 2^31.
 int64_t attend_units(const KvView& v, int32_t group, int32_t max_q_len);
 hipError_t launch_attend(const KvTypes& ty, const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend_tree(const KvTypes& ty, const TreeArgs& a, hipStream_t s);
 
 struct VerifyArgs {
   int32_t n_seqs, n_tokens, n_drafts, vocab, dtype;
@@ -130,5 +138,85 @@ struct VerifyArgs {
 };
 size_t verify_workspace(int32_t n_seqs, int32_t vocab);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
+
+
+// Trees of drafted tokens.
+struct TreeBuildArgs {
+  int32_t n_seqs, n_tokens, words, window;
+  const int32_t* q_start;
+  const int32_t* parent;
+  uint64_t* seen;          // [n_tokens][words]
+  int32_t* depth;          // [n_tokens]
+};
+hipError_t launch_tree_build(const TreeBuildArgs& a, hipStream_t s);
+
+constexpr int kTreeTokens = 1024;   // tokens of a tree (16 words)
+
+struct TreeVerifyArgs {
+  int32_t n_seqs, n_tokens, vocab, dtype, path_ld;
+  int64_t target_ld;
+  const int32_t* q_start;
+  const int32_t* parent;
+  const int32_t* drafted;
+  const void* target;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* tokens;         // [n_seqs][path_ld]
+  int32_t* path;           // [n_seqs][path_ld]
+  int32_t* n_out;
+  char* ws;
+};
+size_t tree_verify_workspace(int32_t n_seqs, int32_t vocab);
+hipError_t launch_tree_verify(const TreeVerifyArgs& a, hipStream_t s);
+
+// The attention that cached tokens get.
+struct WeighArgs {
+  KvView kv;
+  const void* q;
+  int64_t q_ld;
+  const float* lse;        // [n_tokens][n_q_heads]
+  const float* before;     // [n_seqs][H][w_ld] or null
+  float* weights;
+  int64_t w_ld;
+  int32_t n_q_heads;
+  int32_t group;           // as in AttendArgs
+  uint32_t group_m;
+  int32_t group_s;
+  int32_t max_q_len;
+  float scale_log2;
+  float decay;
+  int32_t window;
+  char* ws;
+  int32_t n_cu;
+};
+size_t weigh_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len);
+int64_t weigh_units(const KvView& v);
+hipError_t launch_weigh(const KvTypes& ty, const WeighArgs& a, hipStream_t s);
+
+// Eviction: the tokens that stay, and their way to the front.
+struct SelectArgs {
+  KvView kv;
+  const float* weights;    // [n_seqs][H][w_ld]
+  int64_t w_ld;
+  int32_t budget, sinks, recent;
+  int32_t* keep;           // [n_seqs][H][keep_ld]
+  int64_t keep_ld;
+  int32_t* n_keep;         // [n_seqs]
+  char* ws;
+};
+size_t select_workspace(int32_t n_seqs, int32_t H);
+hipError_t launch_select(const SelectArgs& a, hipStream_t s);
+
+struct CompactArgs {
+  KvView kv;
+  const int32_t* keep;     // [n_seqs][keep_heads][keep_ld]
+  int64_t keep_ld;
+  int32_t keep_heads;      // 1 or H
+  const int32_t* n_keep;
+  bool from_new;           // numbers count from the first new token
+  float* weights;          // [n_seqs][H][w_ld] or null
+  int64_t w_ld;
+};
+hipError_t launch_compact(const KvTypes& ty, const CompactArgs& a, hipStream_t s);
 
 }  // namespace lora

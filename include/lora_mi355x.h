@@ -25,10 +25,10 @@
  *   - Pointers named *_dev are device pointers (HBM), *_host are host pointers.
  *     The caller owns every buffer it passes in; the library never frees them.
  *   - `stream` is a hipStream_t (NULL: the null stream).  Compute entry points
- *     (lora_bgmv_*, lora_sgmv_*, lora_apply, lora_kv_write / read / attend,
- *     lora_spec_verify) are stream-ordered: they neither allocate memory nor
- *     wait for the device.  Set-up calls (pool creation,
- *     upload, evict, page-table build, plan create/build/prepare) may do both.
+ *     (lora_bgmv_*, lora_sgmv_*, lora_apply, lora_kv_*, lora_spec_verify*) are
+ *     stream-ordered: they neither allocate memory nor wait for the device.
+ *     Set-up calls (pool creation, upload, evict, page-table build, plan
+ *     create/build/prepare) may do both.
  *   - x rows are d_in elements of the pool's activation dtype (act_dtype:
  *     the page dtype, except 16-bit activations on FP8 pools), y rows d_out
  *     elements of y_dtype (act_dtype or LORA_F32), both dense row-major,
@@ -552,6 +552,144 @@ lora_status lora_spec_verify_workspace_size(int32_t n_seqs, int32_t vocab, size_
  * 16-byte aligned, no initial contents, not shared by calls that overlap. */
 lora_status lora_spec_verify(const lora_verify_desc* desc, void* workspace_dev, size_t ws_bytes,
                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Trees of drafted tokens: a step proposes several continuations of a sequence at
+ * once, which share what they have in common; one pass of the target looks at all
+ * of them, one path is accepted, and its tokens move together in the cache.
+ *
+ * The new tokens of a sequence are numbered 0, 1, .. in the order of their rows;
+ * token t is written to the cache at kv_len - q_len + t (lora_kv_write as ever).
+ * parent [n_tokens]: the number of a token's parent, below its own; a token whose
+ * parent is not (e.g. -1) is a root.  A token of depth d (roots: 0) stands at
+ * position kv_len - q_len + d of the text, which is what rotary embeddings and
+ * windows go by.
+ * ------------------------------------------------------------------------- */
+/* What the tokens of trees see of their sequence's new ones: bit u % 64 of word
+ * u / 64 of a row stands for new token u.  Bits of tokens that the sequence has
+ * not are not looked at; new tokens from 64 * words on are seen by none. */
+typedef struct {
+  int32_t words;             /* 64-bit words of a row, 1..16                     */
+  int32_t reserved;
+  const uint64_t* seen_dev;  /* [n_tokens][words], 8-byte aligned                */
+  const int32_t* depth_dev;  /* [n_tokens]; without a window it may be NULL      */
+} lora_kv_tree;
+
+/* Rows of a lora_kv_tree from the parents: every token sees itself and its
+ * ancestors, with window > 0 those less than window above it.  seen [n_tokens]
+ * [words] and depth [n_tokens] are written; tokens from 64 * words on get empty
+ * rows and depth 0, rows that belong to no sequence are left.  The time grows with the
+ * depth (a chain of 1024 tokens takes 43 us).  Stream-ordered,
+ * no allocation.  n_seqs 0..1024, n_tokens 0..2^24. */
+lora_status lora_kv_tree_build(int32_t n_seqs, int32_t n_tokens, const int32_t* q_start_dev,
+                               const int32_t* parent_dev, int32_t words, int32_t window,
+                               uint64_t* seen_dev, int32_t* depth_dev, void* stream);
+/* lora_kv_attend for tokens of trees: a token of depth d sees the present tokens j <
+ * kv_len - q_len that were cached before the new ones (if window > 0, those with j >
+ * kv_len - q_len + d - window), and the new tokens that its row of seen has, in
+ * any order, itself only if its bit is there.  A chain's rows give what
+ * lora_kv_attend gives.  Depths below 0 count as 0.  Everything else, the
+ * workspace and its size (lora_kv_attend_workspace_size) too, is as there. */
+lora_status lora_kv_attend_tree(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                                const lora_kv_tree* tree, const void* q_dev, int64_t q_ld,
+                                int32_t n_q_heads, float scale, int32_t window, void* out_dev,
+                                int64_t out_ld, float* lse_dev, void* workspace_dev, size_t ws_bytes,
+                                void* stream);
+
+/* Verification of a tree.  Token 0 of a sequence is the last one that stands; the
+ * others are drafted, each as a continuation of its parent, and row t of target
+ * has the target's probabilities after token t.  A sequence's tokens from 1024 on
+ * are not looked at. */
+typedef struct {
+  int32_t n_seqs;              /* 0..65535                                        */
+  int32_t n_tokens;            /* rows                                            */
+  int32_t vocab;               /* 1..2^18                                         */
+  int32_t dtype;               /* of target: LORA_F32, F16 or BF16                */
+  int32_t path_ld;             /* entries of a sequence in tokens and path, >= 1: a
+                                  path takes no more than path_ld - 1 drafted tokens */
+  int32_t reserved;
+  int64_t target_ld;           /* elements between rows, >= vocab                 */
+  const int32_t* q_start_dev;  /* [n_seqs + 1]                                    */
+  const int32_t* parent_dev;   /* [n_tokens]                                      */
+  const int32_t* drafted_dev;  /* [n_tokens] token ids (of tokens 0: not looked at) */
+  const void* target_dev;      /* [n_tokens][target_ld] probabilities             */
+  const float* u_accept_dev;   /* [n_tokens] uniform numbers in [0, 1)            */
+  const float* u_sample_dev;   /* [n_seqs]                                        */
+  int32_t* tokens_dev;         /* [n_seqs][path_ld] out: the accepted drafted tokens, then
+                                  the new one, then -1                            */
+  int32_t* path_dev;           /* [n_seqs][path_ld] out: the numbers of the tokens that stand,
+                                  0 first, then -1                                */
+  int32_t* n_out_dev;          /* [n_seqs] out: tokens that stand = tokens given out
+                                  (no rows: 0)                                    */
+} lora_tree_verify_desc;
+
+lora_status lora_spec_verify_tree_workspace_size(int32_t n_seqs, int32_t vocab, size_t* bytes);
+/* From token 0 on, the children of the token reached are tried in their order.  With
+ * the weights w_v = floor(2^44 p_v) of its row (p clamped to [0, 1], NaN: 0), child c
+ * with token id d is accepted if floor(L floor(2^31 u_c) / 2^31) < w_d, L being 2^44
+ * less the weights of the ones refused before it (at least 0); a refused one's id loses its weight, so
+ * that children of one id are refused with the first of them, as are ids outside [0,
+ * vocab).  The walk goes on from an accepted child.  Where none is accepted (or
+ * there are none, or path_ld is reached), the next token is drawn with the weights that are left: the
+ * smallest v with w_0 + .. + w_v > floor(total floor(2^31 u_sample) / 2^31); if none
+ * is left, with those of the row as it is; all 0: -1.  For rows that sum to 1 the
+ * tokens given out are distributed as the target's, for drafted tokens that were
+ * chosen without chance (the likeliest ones).  Whole-number sums: the result depends on no
+ * order or split.  Stream-ordered, no wait, no allocation; workspace_dev 16-byte
+ * aligned, no initial contents, not shared by calls that overlap. */
+lora_status lora_spec_verify_tree(const lora_tree_verify_desc* desc, void* workspace_dev, size_t ws_bytes,
+                                  void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction: the attention that cached tokens get, the tokens that stay, and their
+ * way to the front of their sequence's pages, whose last blocks the caller then
+ * gives back (lora_pool_free_pages).
+ * ------------------------------------------------------------------------- */
+/* weights [n_seqs][n_kv_heads][w_ld], fp32, by position: for every cached token j <
+ * kv_len (and < w_ld) of every sequence of the batch
+ *   weights_j = decay before_j + sum_i exp(scale q_i . k_j - lse_i)
+ * over the rows i (new tokens and query heads of the kv head) that see j as in
+ * lora_kv_attend, whose lse of the same q, scale and window is given
+ * [n_tokens][n_q_heads].  New tokens and calls with before_dev == NULL have nothing from before (nor is before read for
+ * decay 0); absent tokens get 0.  before has the layout of weights and may be weights itself.  Scores,
+ * exponentials (of lse's own accuracy) and sums are fp32; keys that a row does not
+ * see do not touch its terms, whatever they hold.  Entries from kv_len on are left.
+ * Runs of one batch give the same bits.  decay in [0, 1].  LORA_E_UNSUPPORTED for calls
+ * that could need 2^31 tiles of 32 tokens.  Stream-ordered, no wait, no allocation; workspace as
+ * for lora_kv_attend (size 0: none is needed). */
+lora_status lora_kv_weigh_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
+                                         const lora_kv_batch* batch, int32_t n_q_heads, size_t* bytes);
+lora_status lora_kv_weigh(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                          const void* q_dev, int64_t q_ld, int32_t n_q_heads, float scale,
+                          int32_t window, const float* lse_dev, float decay, const float* before_dev,
+                          float* weights_dev, int64_t w_ld, void* workspace_dev, size_t ws_bytes,
+                          void* stream);
+/* The tokens of every sequence and kv head that stay: the first `sinks`, the last
+ * `recent` (sinks + recent <= budget), then those of largest weight, of equal ones the
+ * first (NaN: below all others); absent tokens and those from w_ld on are never among them.  n_keep [n_seqs] =
+ * min(budget, the fewest present tokens of a head), keep [n_seqs][n_kv_heads][keep_ld]
+ * (keep_ld >= budget): their positions, ascending; entries from n_keep on are left.
+ * q_start and the batch's tokens play no part.  The same workspace rules as above. */
+lora_status lora_kv_select_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
+                                          const lora_kv_batch* batch, size_t* bytes);
+lora_status lora_kv_select(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                           const float* weights_dev, int64_t w_ld, int32_t budget, int32_t sinks,
+                           int32_t recent, int32_t* keep_dev, int64_t keep_ld, int32_t* n_keep_dev,
+                           void* workspace_dev, size_t ws_bytes, void* stream);
+/* In every sequence and head, place first + i gets the token first + keep[i], i < n_keep
+ * [n_seqs] (and < keep_ld): K, V, FP8 scales and, if weights_dev is not NULL, weights.  first is
+ * 0, or with from_new the first new token's position (kv_len - q_len); keep [n_seqs]
+ * [keep_heads][keep_ld], keep_heads 1 (one list for all heads, e.g. the path of
+ * lora_spec_verify_tree) or n_kv_heads (lora_kv_select).  A list ascends strictly; of one that
+ * does not it is undefined which tokens its places get.  Moves happen in place, so no page
+ * may be shared by two places of the call.  A place keeps what it has where the number names no
+ * cached token or one of the two has no page; nothing else is touched, the places behind
+ * included.  kv_len is not changed: the caller's next one is first + n_keep.  Stream-ordered,
+ * no wait, no allocation. */
+lora_status lora_kv_compact(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
+                            const int32_t* keep_dev, int32_t keep_heads, int64_t keep_ld,
+                            const int32_t* n_keep_dev, int32_t from_new, float* weights_dev,
+                            int64_t w_ld, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Debug / verification of the page-table resolution done inside the kernels.
