@@ -156,24 +156,18 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
 }
 
 // ---- compact -----------------------------------------------------------------------
-// Place i of a (sequence, head) gets token keep[i] >= i, in place.  A wave owns a column (a
-// 16-byte piece of K, 16 elements of V, the scale bytes or the weights) of one (sequence,
-// head) and goes through the list in order: what it reads for a step lies at or behind what
-// this step writes, and before that only earlier steps have written.
+// Place first + i of a (sequence, head) gets the token at first + keep[i] >= first + i, in
+// place.  Both pages' layouts hold 16 bytes of one token (K) or of E tokens (V), so that a
+// list that keeps every fifth token reads nearly every line of its pages: the bytes moved
+// are fewer than those that memory has to give.
+constexpr int64_t kNone = -1;
+
 struct Places {
   int n, first, end;   // entries of the list; position of place 0; tokens with a place in the table
   const int32_t* keep;
-  const int32_t* tab;
+  const int32_t* tab;  // K's page ids, then [H * nb] further V's
 };
-// Page and slot of a position; false: none.
-__device__ __forceinline__ bool page_of(const KvView& kv, const int32_t* tab, int pos, int end, int& page, int& slot) {
-  if (pos < 0 || pos >= end) return false;
-  const int b = (int)kv_div(kv, (uint32_t)pos);
-  slot = pos - b * kv.T;
-  page = tab[b];
-  return (unsigned)page < (unsigned)kv.n_pages;
-}
-__device__ __forceinline__ Places places_of(const CompactArgs& a, int s, int h, int which) {
+__device__ __forceinline__ Places places_of(const CompactArgs& a, int s, int h) {
   const KvView& kv = a.kv;
   const KvSeq q = kv_seq(kv, s);
   Places p;
@@ -182,95 +176,201 @@ __device__ __forceinline__ Places places_of(const CompactArgs& a, int s, int h, 
   p.n = (int)min((int64_t)max(uni(a.n_keep[s]), 0), a.keep_ld);
   p.n = min(p.n, p.end - p.first);
   p.keep = a.keep + ((int64_t)s * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_ld;
-  p.tab = kv.table + (((int64_t)s * 2 + which) * kv.H + h) * kv.nb;
+  p.tab = kv.table + ((int64_t)s * 2 * kv.H + h) * kv.nb;
   return p;
 }
-// The position that place i takes from; -1: none.
-__device__ __forceinline__ int source_of(const Places& p, int i) {
-  const int k = i < p.n ? p.keep[i] : -1;
-  return k >= 0 && k < p.end - p.first ? p.first + k : -1;
-}
-
-template <typename V>
-__device__ __forceinline__ void move_units(const KvView& kv, const Places& p, int lane, char* base, int64_t page_bytes,
-                                           int64_t column) {   // one unit V a token, at page, column + slot sizeof(V)
-  for (int i0 = 0; i0 < p.n; i0 += 64) {
-    const int i = i0 + lane, src = source_of(p, i), dst = p.first + i;
-    int sp = 0, ss = 0, dp = 0, ds = 0;
-    const bool ok = i < p.n && src != dst && page_of(kv, p.tab, src, p.end, sp, ss) && page_of(kv, p.tab, dst, p.end, dp, ds);
-    V v{};
-    if (ok) v = *reinterpret_cast<const V*>(base + sp * page_bytes + column + (int64_t)ss * sizeof(V));
-    if (ok) *reinterpret_cast<V*>(base + dp * page_bytes + column + (int64_t)ds * sizeof(V)) = v;
-  }
-}
-
+// Bytes of a token's K (which 0) or V rows in the pool's pages: of K its 16 bytes of piece
+// 0, of V its element 0.  kNone: it has no page.
 template <int E, int D>
-__device__ __forceinline__ void move_v(const KvView& kv, const Places& p, int lane, int column) {
+__device__ __forceinline__ int64_t token_at(const KvView& kv, const Places& p, int which, int pos) {
+  if (pos < 0 || pos >= p.end) return kNone;
+  const int b = (int)kv_div(kv, (uint32_t)pos), slot = pos - b * kv.T;
+  const int page = p.tab[(which ? (int64_t)kv.H * kv.nb : 0) + b];
+  if ((unsigned)page >= (unsigned)kv.n_pages) return kNone;
+  return (int64_t)page * kv.page_bytes + (which ? slot / E * (D * 16) + slot % E * (16 / E) : slot * 16);
+}
+// The scale byte of the token at `at` (K or V) in the pages.
+template <int E, int D>
+__device__ __forceinline__ int64_t scale_at(const KvView& kv, int which, int64_t at) {
+  const int64_t page = at / kv.page_bytes;
+  const int in = (int)(at - page * kv.page_bytes);
+  return page * kv.T + (which ? in / (D * 16) * E + in % 16 : in / 16);
+}
+
+// The list's entries in steps of N positions, resolved once for all of a block's columns:
+// slot x stands for position pos0 + x, pos0 a multiple of E.
+template <int N>
+struct Steps {
+  int64_t from[2][N], to[2][N];   // of K and V; from kNone: the place keeps what it has
+  int32_t w[N];                   // position that the weight comes from, -1: none
+};
+template <int E, int D, int N, int THREADS>
+__device__ __forceinline__ bool resolve(const CompactArgs& a, const Places& p, int pos0, Steps<N>& st) {
+  bool moves = false;
+  for (int x = threadIdx.x; x < N; x += THREADS) {
+    const int pos = pos0 + x, i = pos - p.first;
+    const int k = i >= 0 && i < p.n ? p.keep[i] : -1;
+    const int src = k >= 0 && k < p.end - p.first ? p.first + k : -1;
+    const bool move = src >= 0 && src != pos && pos >= 0;
+    moves |= move;
+    st.w[x] = move && src < a.w_ld ? src : -1;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int64_t f = src >= 0 ? token_at<E, D>(a.kv, p, which, src) : kNone;
+      const int64_t t = src >= 0 ? token_at<E, D>(a.kv, p, which, pos) : kNone;
+      st.from[which][x] = t == kNone ? kNone : f;
+      st.to[which][x] = t;
+    }
+  }
+  return __syncthreads_or(moves) != 0;
+}
+
+// E tokens' values of an element of V, gathered and in their places: what is in registers
+// between the reads and the writes.
+template <int E>
+struct Gathered {
   using B = typename std::conditional<E == 16, uint8_t, uint16_t>::type;
-  const int d = column * 16 + (lane & 15);
-  // four groups of E places at a time, aligned in the page
-  for (int pos0 = p.first / E * E; pos0 < p.first + p.n; pos0 += 4 * E) {
-    const int g0 = pos0 + (lane >> 4) * E;
-    int dp = 0, ds = 0;
-    const bool there = g0 < p.first + p.n && page_of(kv, p.tab, g0, p.end, dp, ds);
-    B v[E];
-    uint32_t have = 0, moved = 0;
+  uint32_t w[4];
+  uint32_t have;   // bits of the E tokens that have one
+};
+// Group x0 .. x0 + E - 1 of the step's positions, element d.
+template <int E, int N>
+__device__ __forceinline__ Gathered<E> gather_v(const char* pages, const Steps<N>& st, int x0, int d) {
+  using B = typename Gathered<E>::B;
+  B v[E];
+  Gathered<E> g;
+  g.have = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = g0 + e - p.first, src = there && i >= 0 ? source_of(p, i) : -1;
-      int sp = 0, ss = 0;
-      v[e] = 0;
-      if (src >= 0 && page_of(kv, p.tab, src, p.end, sp, ss)) {
-        v[e] = *reinterpret_cast<const B*>(kv.pages + (int64_t)sp * kv.page_bytes + ((int64_t)(ss / E) * D + d) * 16 +
-                                           (ss % E) * sizeof(B));
-        have |= 1u << e;
-        moved |= (uint32_t)(src != g0 + e) << e;
-      }
+  for (int e = 0; e < E; ++e) {
+    const int64_t f = st.from[1][x0 + e];
+    v[e] = 0;
+    if (f != kNone) {
+      v[e] = *reinterpret_cast<const B*>(pages + f + d * 16);
+      g.have |= 1u << e;
     }
-    char* dst = kv.pages + (int64_t)dp * kv.page_bytes + ((int64_t)(ds / E) * D + d) * 16;
-    if (have == (1u << E) - 1u && moved) {
-      uint32_t w[4] = {0, 0, 0, 0};
+  }
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e * (int)sizeof(B) / 4] |= (uint32_t)v[e] << (e * (int)sizeof(B) % 4 * 8);
-      *reinterpret_cast<u32x4*>(dst) = u32x4{w[0], w[1], w[2], w[3]};
-    } else {
+  for (int i = 0; i < 4; ++i) g.w[i] = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if ((moved >> e) & 1u) reinterpret_cast<B*>(dst)[e] = v[e];
-    }
+  for (int e = 0; e < E; ++e) g.w[e * (int)sizeof(B) / 4] |= (uint32_t)v[e] << (e * (int)sizeof(B) % 4 * 8);
+  return g;
+}
+template <int E, int N>
+__device__ __forceinline__ void place_v(char* pages, const Steps<N>& st, int x0, int d, const Gathered<E>& g) {
+  using B = typename Gathered<E>::B;
+  if (g.have == (1u << E) - 1u) {
+    *reinterpret_cast<u32x4*>(pages + st.to[1][x0] + d * 16) = u32x4{g.w[0], g.w[1], g.w[2], g.w[3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((g.have >> e) & 1u)
+        *reinterpret_cast<B*>(pages + st.to[1][x0 + e] + d * 16) = (B)(g.w[e * (int)sizeof(B) / 4] >> (e * (int)sizeof(B) % 4 * 8));
   }
 }
 
+// Lists of up to 64 - E entries (the path of a tree): a block moves everything of a
+// (sequence, head).  All is read before anything is written.
+template <int E, int D>
+__global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
+  constexpr int N = 64, KU = N * (D / E) / 256, VU = N / E * D / 256;
+  __shared__ Steps<N> st;
+  const KvView& kv = a.kv;
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+  const Places p = places_of(a, s, h);
+  const int pos0 = max(p.first, 0) / E * E;
+  if (p.n <= 0 || !resolve<E, D, N, 256>(a, p, pos0, st)) return;
+  const int x = tid & 63;
+  u32x4 k[KU];
+  Gathered<E> v[VU > 0 ? VU : 1];
+  uint8_t sc[2] = {0, 0};
+  float w = 0.f;
+#pragma unroll
+  for (int u = 0; u < KU; ++u)
+    if (st.from[0][x] != kNone) k[u] = ldv(kv.pages + st.from[0][x] + (int64_t)(u * 4 + (tid >> 6)) * kv.T * 16);
+#pragma unroll
+  for (int u = 0; u < VU; ++u) v[u] = gather_v<E>(kv.pages, st, (u * 256 + tid) / D * E, (u * 256 + tid) % D);
+  if (E == 16 && tid < 128 && st.from[tid >> 6][x] != kNone)
+    sc[0] = kv.scales[scale_at<E, D>(kv, tid >> 6, st.from[tid >> 6][x])];
+  float* weights = a.weights ? a.weights + ((int64_t)s * kv.H + h) * a.w_ld : nullptr;
+  if (weights && tid < N && st.w[tid] >= 0) w = weights[st.w[tid]];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < KU; ++u)
+    if (st.from[0][x] != kNone) *reinterpret_cast<u32x4*>(kv.pages + st.to[0][x] + (int64_t)(u * 4 + (tid >> 6)) * kv.T * 16) = k[u];
+#pragma unroll
+  for (int u = 0; u < VU; ++u) place_v<E>(kv.pages, st, (u * 256 + tid) / D * E, (u * 256 + tid) % D, v[u]);
+  if (E == 16 && tid < 128 && st.from[tid >> 6][x] != kNone)
+    kv.scales[scale_at<E, D>(kv, tid >> 6, st.to[tid >> 6][x])] = sc[0];
+  if (weights && tid < N && st.w[tid] >= 0) weights[pos0 + tid] = w;
+}
+
+// Lists of any length.  A wave owns a column (a 16-byte piece of K, 8 elements of V, the
+// scale bytes or the weights) of one (sequence, head) and goes through the list in order: what
+// it reads for a step lies at or behind what this step writes, and before that only earlier
+// steps have written.
 template <int E, int D>
 __global__ __launch_bounds__(256) void k_compact(CompactArgs a, int columns) {
-  constexpr int KC = D / E, VC = D / 16;
+  constexpr int N = 512, KC = D / E, VC = D / 8, U = 4, UV = 16 / E;
+  __shared__ Steps<N> st;
   const KvView& kv = a.kv;
   const int lane = threadIdx.x & 63, c = blockIdx.x * 4 + uni((int)threadIdx.x >> 6), h = blockIdx.y, s = blockIdx.z;
-  if (c >= columns) return;
-  if (c < KC) {
-    const Places p = places_of(a, s, h, 0);
-    move_units<u32x4>(kv, p, lane, kv.pages, kv.page_bytes, (int64_t)c * kv.T * 16);
-  } else if (c < KC + VC) {
-    const Places p = places_of(a, s, h, 1);
-    move_v<E, D>(kv, p, lane, c - KC);
-  } else if (E == 16 && c < KC + VC + 2) {
-    const Places p = places_of(a, s, h, c - KC - VC);
-    move_units<uint8_t>(kv, p, lane, reinterpret_cast<char*>(kv.scales), kv.T, 0);
-  } else {
-    const Places p = places_of(a, s, h, 0);
-    float* w = a.weights + ((int64_t)s * kv.H + h) * a.w_ld;
-    for (int i0 = 0; i0 < p.n; i0 += 64) {
-      const int i = i0 + lane, src = source_of(p, i), dst = p.first + i;
-      const bool ok = src >= 0 && src < a.w_ld && dst >= 0;
-      const float x = ok ? w[src] : 0.f;
-      if (ok && src != dst) w[dst] = x;
+  const Places p = places_of(a, s, h);
+  float* weights = a.weights ? a.weights + ((int64_t)s * kv.H + h) * a.w_ld : nullptr;
+  const int end = p.first + p.n;
+  for (int pos0 = max(p.first, 0) / E * E; pos0 < end; pos0 += N) {
+    if (resolve<E, D, N, 256>(a, p, pos0, st)) {
+      const int n = min(N, end - pos0);
+      if (c < KC) {
+        const int64_t column = (int64_t)c * kv.T * 16;
+        for (int x0 = 0; x0 < n; x0 += 64 * U) {
+          u32x4 v[U];
+          int64_t f[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            f[u] = x0 + 64 * u < n ? st.from[0][x0 + 64 * u + lane] : kNone;
+            if (f[u] != kNone) v[u] = ldv(kv.pages + f[u] + column);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (f[u] != kNone) *reinterpret_cast<u32x4*>(kv.pages + st.to[0][x0 + 64 * u + lane] + column) = v[u];
+        }
+      } else if (c < KC + VC) {
+        const int d = (c - KC) * 8 + (lane & 7);   // (8 elements are a line of 128 bytes)
+        for (int x0 = 0; x0 < n; x0 += 8 * UV * E) {
+          Gathered<E> v[UV];
+#pragma unroll
+          for (int u = 0; u < UV; ++u) v[u] = gather_v<E>(kv.pages, st, x0 + (u * 8 + (lane >> 3)) * E, d);
+#pragma unroll
+          for (int u = 0; u < UV; ++u) place_v<E>(kv.pages, st, x0 + (u * 8 + (lane >> 3)) * E, d, v[u]);
+        }
+      } else if (E == 16 && c < KC + VC + 2) {
+        const int which = c - KC - VC;
+        for (int x = lane; x < n; x += 64) {
+          const int64_t f = st.from[which][x];
+          uint8_t v = 0;
+          if (f != kNone) v = kv.scales[scale_at<E, D>(kv, which, f)];
+          if (f != kNone) kv.scales[scale_at<E, D>(kv, which, st.to[which][x])] = v;
+        }
+      } else if (c < columns) {
+        for (int x = lane; x < n; x += 64) {
+          const int f = st.w[x];
+          float v = 0.f;
+          if (f >= 0) v = weights[f];
+          if (f >= 0) weights[pos0 + x] = v;
+        }
+      }
     }
+    __syncthreads();   // the step's places have been read
   }
 }
 
 template <int E, int D>
 hipError_t compact(const CompactArgs& a, hipStream_t s) {
-  const int columns = D / E + D / 16 + (E == 16 ? 2 : 0) + (a.weights ? 1 : 0);
+  if (a.keep_ld <= 64 - E + 1) {
+    hipLaunchKernelGGL((k_compact_few<E, D>), dim3(a.kv.H, a.kv.n_seqs), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const int columns = D / E + D / 8 + (E == 16 ? 2 : 0) + (a.weights ? 1 : 0);
   hipLaunchKernelGGL((k_compact<E, D>), dim3((columns + 3) / 4, a.kv.H, a.kv.n_seqs), dim3(256), 0, s, a, columns);
   return hipGetLastError();
 }

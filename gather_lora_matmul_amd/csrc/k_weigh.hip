@@ -10,27 +10,36 @@
 #include <algorithm>
 
 #include "kvtiles.h"
+#include "per_device.h"
 
 namespace lora {
 
 namespace {
 
+#ifndef WR
+#define WR 2
+#define NB8 4
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Tiles of KT cached tokens of a (sequence, head), in that order of sequences.
 __device__ __forceinline__ int tokens_of(const WeighArgs& a, const KvSeq& q) {
   return (int)min((int64_t)q.end, a.w_ld);
 }
-// Prefix sums of the sequences' tiles in LDS (n_seqs + 1); returns all of them.
+// Prefix sums of the sequences' tiles in LDS (and, if wanted, the sequences); returns all.
 template <int KT, int THREADS>
-__device__ __forceinline__ int tile_sums(const WeighArgs& a, int* pre) {
+__device__ __forceinline__ int tile_sums(const WeighArgs& a, int* pre, KvSeq* seqs = nullptr) {
   const int n = a.kv.n_seqs, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   __shared__ int wsum[THREADS / 64];
   int run = 0;
   for (int s0 = 0; s0 < n; s0 += THREADS) {
     const int s = s0 + tid;
     int sum = 0;
-    if (s < n) sum = (tokens_of(a, kv_seq(a.kv, s)) + KT - 1) / KT * a.kv.H;
+    if (s < n) {
+      const KvSeq q = kv_seq(a.kv, s);
+      if (seqs) seqs[s] = q;
+      sum = (tokens_of(a, q) + KT - 1) / KT * a.kv.H;
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int z = __shfl_up(sum, d);
@@ -62,20 +71,26 @@ __device__ __forceinline__ int seq_of(const int* pre, int n, int u) {
   return lo;
 }
 
+// A (sequence, head) and a tile of it, the same in all lanes.
 struct Unit {
   int seq, head, tile;
+  int n;   // tokens of the sequence
   KvSeq q;
 };
+__device__ __forceinline__ void unit_seq(const WeighArgs& a, Unit& u, const KvSeq* seqs) {
+  u.q = seqs ? seqs[u.seq] : kv_seq(a.kv, u.seq);
+  u.q.q0 = uni(u.q.q0);
+  u.q.q_len = uni(u.q.q_len);
+  u.q.base = uni(u.q.base);
+  u.q.end = uni(u.q.end);
+  u.n = tokens_of(a, u.q);
+}
 template <int KT>
-__device__ __forceinline__ Unit unit_of(const WeighArgs& a, const int* pre, int u) {
+__device__ __forceinline__ Unit unit_of(const WeighArgs& a, const int* pre, int at, const KvSeq* seqs = nullptr) {
   Unit r;
-  r.seq = uni(seq_of(pre, a.kv.n_seqs, u));
-  r.q = kv_seq(a.kv, r.seq);
-  r.q.q0 = uni(r.q.q0);
-  r.q.q_len = uni(r.q.q_len);
-  r.q.base = uni(r.q.base);
-  r.q.end = uni(r.q.end);
-  const int tiles = (tokens_of(a, r.q) + KT - 1) / KT, rem = u - pre[r.seq];
+  r.seq = uni(seq_of(pre, a.kv.n_seqs, at));
+  unit_seq(a, r, seqs);
+  const int tiles = (r.n + KT - 1) / KT, rem = at - pre[r.seq];
   r.head = uni(rem / tiles);
   r.tile = uni((rem - r.head * tiles) * KT);
   return r;
@@ -87,125 +102,194 @@ __device__ __forceinline__ float old_weight(const WeighArgs& a, const Unit& u, i
 }
 
 // ---- up to 16 rows ---------------------------------------------------------------
-// A wave for itself: KT keys straight to registers, the rows in tiles of 16.
+// A wave for itself: KT keys straight to registers, the rows in tiles of 16.  Bound by the
+// reads of K: a wave's units are neighbours, the next one's keys are on their way while it
+// works on one, its page ids while it loads one.
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256) void k_weigh_rows(WeighArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WR, WR))) void k_weigh_rows(WeighArgs a) {
   constexpr bool Q8 = is_quant<KV>();
-  constexpr int E = ET<KV>::E, KT = 4 * E, NB = KT / 16, NC = D / (4 * E), NQ = D / 32;
+  constexpr int E = ET<KV>::E, NB = Q8 ? NB8 : 2, KT = 16 * NB, NC = D / (4 * E), NQ = D / 32;
   __shared__ int pre[kKvMaxSeqs + 1];
+  __shared__ KvSeq seqs[kKvMaxSeqs];
   const KvView& kv = a.kv;
-  const int units = tile_sums<KT, 256>(a, pre);
+  const int units = tile_sums<KT, 256>(a, pre, seqs);
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int workers = (int)gridDim.x * 4, worker = (int)blockIdx.x * 4 + uni(tid >> 6);
   const int from = (int)((int64_t)units * worker / workers), to = (int)((int64_t)units * (worker + 1) / workers);
-  for (int un = from; un < to; ++un) {
-    const Unit u = unit_of<KT>(a, pre, un);
-    const KvSeq& q = u.q;
+  if (from >= to) return;
+  const int win = a.window > 0 ? a.window : 0x40000000;
+  struct Ids {
+    int k[NB], v[NB];
+  };
+  struct Keys {
+    u32x4 k[NB][NC];
+    uint32_t scale[NB];
+    uint32_t there;   // of block b: bit b
+    float old;        // what the lane's token had before
+  };
+  auto find = [&](const Unit& u) {
     const int32_t* ktab = kv.table + ((int64_t)u.seq * 2 * kv.H + u.head) * kv.nb;
-    const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-    const int rows = q.q_len * a.group, n = tokens_of(a, q);
-    const int win = a.window > 0 ? a.window : 0x40000000;
-    u32x4 kf[NB][NC];
-    float f[NB], sum[NB];
-    bool there[NB];
+    Ids r;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int t = u.tile + 16 * b + col;
-      const int blk = (int)kv_div(kv, (uint32_t)t), slot = t - blk * kv.T;
-      const int kp = blk < kv.nb ? ktab[blk] : -1, vp = blk < kv.nb ? vtab[blk] : -1;
-      there[b] = (unsigned)kp < (unsigned)kv.n_pages && (unsigned)vp < (unsigned)kv.n_pages;
-      const int pg = there[b] ? kp : 0;
-      const char* src = kv.pages + (int64_t)pg * kv.page_bytes + (g * kv.T + (there[b] ? slot : 0)) * 16;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) kf[b][c] = ldv(src + c * 4 * kv.T * 16);
-      f[b] = a.scale_log2;
-      if (Q8) f[b] *= __uint_as_float((uint32_t)kv.scales[(int64_t)pg * kv.T + (there[b] ? slot : 0)] << 23);
-      sum[b] = 0.f;
+      const int blk = (int)kv_div(kv, (uint32_t)(u.tile + 16 * b + col));
+      r.k[b] = blk < kv.nb ? ktab[blk] : -1;
+      r.v[b] = blk < kv.nb ? ktab[(int64_t)kv.H * kv.nb + blk] : -1;
     }
-    // of the sequence's rows those of tokens [t0, t1) see something of the tile
-    const int t0 = max(u.tile - q.base, 0);
-    const int t1 = a.window > 0 ? min(q.q_len, u.tile + KT - 1 + a.window - q.base) : q.q_len;
-    for (int r0 = t0 * a.group; r0 < min(t1 * a.group, rows); r0 += 16) {
-      u32x4 qf[NQ];
-      {
-        const int row = min(r0 + col, rows - 1), t = token_of(a, row);
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(q.q0 + t) * a.q_ld +
-                              (int64_t)(u.head * a.group + row - t * a.group) * D;
+    return r;
+  };
+  auto load = [&](const Unit& u, const Ids& id) {
+    Keys r;
+    r.there = 0;
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) qf[i] = ldv(src + (Q8 ? (4 * (i >> 1) + g) * 16 + (i & 1) * 8 : (4 * i + g) * 8));
-      }
-      float ls[4];
-      int pos[4];
+    for (int b = 0; b < NB; ++b) {
+      const int t = u.tile + 16 * b + col, slot = t - (int)kv_div(kv, (uint32_t)t) * kv.T;
+      const bool ok = (unsigned)id.k[b] < (unsigned)kv.n_pages && (unsigned)id.v[b] < (unsigned)kv.n_pages;
+      r.there |= (uint32_t)ok << b;
+      const int pg = ok ? id.k[b] : 0, sl = ok ? slot : 0;
+      const char* src = kv.pages + (int64_t)pg * kv.page_bytes + (g * kv.T + sl) * 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 4 * g + i, r = min(row, rows - 1), t = token_of(a, r);
-        ls[i] = a.lse[(int64_t)(q.q0 + t) * a.n_q_heads + u.head * a.group + r - t * a.group] * kLog2e;
-        pos[i] = row < rows ? q.base + t : -0x40000000;
+      for (int c = 0; c < NC; ++c) r.k[b][c] = ldv(src + c * 4 * kv.T * 16);
+      r.scale[b] = Q8 ? kv.scales[(int64_t)pg * kv.T + sl] : 0u;
+    }
+    const int j = u.tile + 16 * g + col;
+    const int64_t at = ((int64_t)u.seq * kv.H + u.head) * a.w_ld;
+    r.old = g < NB && j < u.n ? old_weight(a, u, at, j) : 0.f;
+    return r;
+  };
+  auto next = [&](Unit& u) {   // the unit behind u
+    u.tile += KT;
+    if (u.tile < u.n) return;
+    u.tile = 0;
+    if (++u.head < kv.H) return;
+    u.head = 0;
+    do ++u.seq;
+    while (pre[u.seq + 1] == pre[u.seq]);
+    unit_seq(a, u, seqs);
+  };
+  u32x4 qf[NQ];
+  float ls[4];
+  int pos[4];
+  auto rows_at = [&](const Unit& u, int r0) {
+    const KvSeq& q = u.q;
+    const int rows = q.q_len * a.group;
+    {
+      const int row = min(r0 + col, rows - 1), t = token_of(a, row);
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(q.q0 + t) * a.q_ld +
+                            (int64_t)(u.head * a.group + row - t * a.group) * D;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) qf[i] = ldv(src + (Q8 ? (4 * (i >> 1) + g) * 16 + (i & 1) * 8 : (4 * i + g) * 8));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + 4 * g + i, r = min(row, rows - 1), t = token_of(a, r);
+      ls[i] = a.lse[(int64_t)(q.q0 + t) * a.n_q_heads + u.head * a.group + r - t * a.group] * kLog2e;
+      pos[i] = row < rows ? q.base + t : -0x40000000;
+    }
+  };
+  Unit u = unit_of<KT>(a, pre, from, seqs), un = u;
+  Keys key = load(u, find(u));
+  Ids idn{};
+  bool fresh = true;   // the rows in registers are not u's
+  if (from + 1 < to) {
+    next(un);
+    idn = find(un);
+  }
+  for (int i = from; i < to; ++i) {
+    const bool more = i + 1 < to;
+    const int rows = u.q.q_len * a.group;
+    if (fresh && rows > 0) rows_at(u, 0);
+    Keys kn;
+    Unit u2 = un;
+    if (more) {
+      kn = load(un, idn);
+      if (i + 2 < to) {
+        next(u2);
+        idn = find(u2);
       }
+    }
+    float sum[NB] = {};
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+      if (r0 > 0) rows_at(u, r0);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           if constexpr (Q8) {
-            s = mfma16<A>(qf[2 * c], fp8_to16<A>(kf[b][c].x, kf[b][c].y), s);
-            s = mfma16<A>(qf[2 * c + 1], fp8_to16<A>(kf[b][c].z, kf[b][c].w), s);
+            s = mfma16<A>(qf[2 * c], fp8_to16<A>(key.k[b][c].x, key.k[b][c].y), s);
+            s = mfma16<A>(qf[2 * c + 1], fp8_to16<A>(key.k[b][c].z, key.k[b][c].w), s);
           } else {
-            s = mfma16<A>(qf[c], kf[b][c], s);
+            s = mfma16<A>(qf[c], key.k[b][c], s);
           }
         }
         const int j = u.tile + 16 * b + col;
+        const float f = Q8 ? a.scale_log2 * __uint_as_float(key.scale[b] << 23) : a.scale_log2;
+        float part = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], f[b], -ls[i]));
-          sum[b] += j <= pos[i] && j > pos[i] - win ? p : 0.f;
+        for (int x = 0; x < 4; ++x) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], f, -ls[x]));
+          part += j <= pos[x] && j > pos[x] - win ? p : 0.f;
         }
+        sum[b] += part;
       }
     }
     // the lane groups' rows together; group g writes the 16 keys of block g
     float mine = 0.f;
-    bool ok = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float x = sum[b];
       x += __shfl_xor(x, 16);
       x += __shfl_xor(x, 32);
-      if (g == b) {
-        mine = x;
-        ok = there[b];
-      }
+      mine = g == b ? x : mine;
     }
     const int j = u.tile + 16 * g + col;
-    const int64_t at = ((int64_t)u.seq * kv.H + u.head) * a.w_ld;
-    if (g < NB && j < n) a.weights[at + j] = ok ? old_weight(a, u, at, j) + mine : 0.f;
+    if (g < NB && j < u.n)
+      a.weights[((int64_t)u.seq * kv.H + u.head) * a.w_ld + j] = (key.there >> g) & 1u ? key.old + mine : 0.f;
+    if (more) {
+      fresh = un.head != u.head || un.seq != u.seq || rows > 16;
+      key = kn;
+      u = un;
+      un = u2;
+    }
   }
 }
 
 // ---- more rows -------------------------------------------------------------------
 // A block's four waves have 64 keys each, in registers for all of the rows, which go
 // through LDS in tiles of 64 (two slots, one barrier a tile).
+// Rows in LDS, 64 of them in B blocks of 1 KB, each what one load brings: row r is number r / B
+// of block r % B, and a block begins 16 bytes further in the banks than the one before.  The
+// loads cover whole rows, a product's lanes read all banks alike, and all operands of a lane
+// are at constant distances from one address.
 template <int D>
 struct WeighShared {
-  u32x4 q[2][D / 8][64];
-  float lse[2][64];
+  static constexpr int P = D / 8, B = P, STEP = 1024 + 16, HALF = B * STEP;   // (64 rows of P pieces in 1 KB blocks: B = P)
+  static constexpr int RT = 128, SLOT = RT / 64 * HALF;
+  __align__(16) char q[2 * SLOT];
+  float lse[4][RT];        // of the tile before, this one and the two after
+  int pre[kKvMaxSeqs + 1];
+  static __device__ __forceinline__ int row_at(int r) { return r % B * STEP + r / B * (16 * P); }
 };
+
 template <typename A, typename KV, int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_weigh_tiles(WeighArgs a) {
   constexpr bool Q8 = is_quant<KV>();
-  constexpr int KT = 256, NQ = D / 16, RT = 64;
-  __shared__ int pre[kKvMaxSeqs + 1];
-  __shared__ __align__(16) WeighShared<D> sh;
+  using S = WeighShared<D>;
+  constexpr int KT = 256, NQ = D / 16, RT = S::RT, P = S::P, B = S::B;
+  extern __shared__ __align__(16) char smem[];
+  S& sh = *reinterpret_cast<S*>(smem);
   const KvView& kv = a.kv;
-  const int units = tile_sums<KT, 256>(a, pre);
+  const int units = tile_sums<KT, 256>(a, sh.pre);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, hi = lane >> 5;
   // an eighth of the units to each XCD: the tiles of one head, which read the same rows, share its L2
   const int per = (units + 7) / 8, x0 = min(((int)blockIdx.x & 7) * per, units), x1 = min(x0 + per, units);
   for (int un = x0 + ((int)blockIdx.x >> 3); un < x1; un += (int)gridDim.x >> 3) {
-    const Unit u = unit_of<KT>(a, pre, un);
+    const Unit u = unit_of<KT>(a, sh.pre, un);
     const KvSeq& q = u.q;
     const int32_t* ktab = kv.table + ((int64_t)u.seq * 2 * kv.H + u.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-    const int n = tokens_of(a, q), k0 = u.tile + wave * 64;
+    const int k0 = u.tile + wave * 64;
     const int win = a.window > 0 ? a.window : 0x40000000;
     u32x4 kf[2][NQ];
     float f[2], sum[2] = {0.f, 0.f};
@@ -234,79 +318,155 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int t0 = max(u.tile - q.base, 0);
     const int t1 = a.window > 0 ? min(q.q_len, u.tile + KT - 1 + a.window - q.base) : q.q_len;
     const int r0 = t0 * a.group, r1 = t1 * a.group;
-    auto row_of = [&](int r) { return min(r, r1 - 1); };
-    float next_lse = 0.f;
-    auto issue = [&](int rt, int slot) {   // rows rt .. rt + 63 to a slot; their lse to a register
+    // rows rt .. rt + RT - 1 to a slot, their lse to LDS.  A lane finds the place of a row of
+    // each 64, the loads take it from the lanes that have theirs
+    auto issue = [&](int rt, int n) {
+      float ls[RT / 64];
 #pragma unroll
-      for (int i = 0; i < D / 8 / 4; ++i) {
-        const int piece = wave + 4 * i, r = row_of(rt + lane), t = token_of(a, r);
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(q.q0 + t) * a.q_ld +
-                              (int64_t)(u.head * a.group + r - t * a.group) * D + piece * 8;
-        load_lds16(src, &sh.q[slot][piece][0]);
+      for (int h = 0; h < RT / 64; ++h) {
+        const int r = min(rt + 64 * h + lane, r1 - 1), t = token_of(a, r), in = u.head * a.group + r - t * a.group;
+        const int64_t at = (int64_t)(q.q0 + t) * a.q_ld + (int64_t)in * D;
+#pragma unroll
+        for (int i = 0; i < B / 4; ++i) {
+          const int b = wave + 4 * i, mine = b + B * (lane / P);   // the load's block, the lane's row
+          const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(mine * 4, (int)(uint32_t)at);
+          const int high = __builtin_amdgcn_ds_bpermute(mine * 4, (int)(at >> 32));
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + ((int64_t)high << 32 | lo) + lane % P * 8;
+          load_lds16(src, sh.q + (n & 1) * S::SLOT + h * S::HALF + b * S::STEP);
+        }
+        if (wave == 0) ls[h] = a.lse[(int64_t)(q.q0 + t) * a.n_q_heads + in] * kLog2e;
       }
-      if (tid < RT) {
-        const int r = row_of(rt + tid), t = token_of(a, r);
-        next_lse = a.lse[(int64_t)(q.q0 + t) * a.n_q_heads + u.head * a.group + r - t * a.group] * kLog2e;
-      }
+      if (wave == 0)
+#pragma unroll
+        for (int h = 0; h < RT / 64; ++h) sh.lse[n & 3][64 * h + lane] = ls[h];
     };
-    int slot = 0;
-    if (r0 < r1) {
-      issue(r0, 0);
-      if (tid < RT) sh.lse[0][tid] = next_lse;
-    }
-    for (int rt = r0; rt < r1; rt += RT, slot ^= 1) {
+    // One step: the exponentials of 32 rows' scores s (rows ra on) and the products of the
+    // 32 rows at `at`, woven, which keeps the matrix cores and the vector ALUs busy at the same
+    // time.  Operands are read four products ahead, of the step after this one too if its
+    // rows are there (then, at `after`), and that step's lse.
+    constexpr int R = 4, M = 2 * NQ, EACH = 32 / M;   // operands read ahead, products, exponentials to each
+    u32x4 fr[R];
+    f32x4 ls[4];
+    const char* const mine = sh.q + S::row_at(col) + hi * 16;
+    auto operand = [&](int at, int k) { return *reinterpret_cast<const u32x4*>(mine + at + k * 32); };
+    auto lse_of = [&](const float* lse, int b) { return *reinterpret_cast<const f32x4*>(lse + 8 * b + 4 * hi); };
+    auto step = [&](auto then, f32x16(&s)[2], f32x16(&sn)[2], int at, int after, const float* next_ls, int ra)
+        __attribute__((always_inline)) {
+      float part[2] = {0.f, 0.f};   // of 32 rows: the long sum's terms are of one size
+      const int rz = min(ra + 31, r1 - 1), pa = q.base + token_of(a, ra), pz = q.base + token_of(a, rz);
+      const bool edge = k0 + 63 > pa || k0 <= pz - win || ra + 31 >= r1;
+      auto product = [&](int m) __attribute__((always_inline)) {
+        const int k = m >> 1, c = m & 1;
+        sn[c] = mfma32<A>(fr[k % R], kf[c][k], k ? sn[c] : f32x16{});
+        if (!c) return;
+        if (k + R < NQ) fr[k % R] = operand(at, k + R);
+        else if (decltype(then)::value) fr[k % R] = operand(after, k + R - NQ);
+      };
+      if (__builtin_expect(edge, 0)) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) product(m);
+        float fe[2] = {f[0], f[1]};   // (unknown to the compiler, which would take the exponentials of both ways ahead of them)
+        asm volatile("" : "+v"(fe[0]), "+v"(fe[1]));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = ra + 8 * (i >> 2) + 4 * hi + (i & 3), pos = q.base + token_of(a, r);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int j = k0 + 32 * c + col;
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][i], fe[c], -ls[i >> 2][i & 3]));
+            part[c] += r < r1 && j <= pos && j > pos - win ? p : 0.f;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) ls[b] = lse_of(next_ls, b);
+      } else {
+        constexpr int L = 4;   // a sum follows its exponential by so many others
+        float y[L] = {};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          __builtin_amdgcn_sched_barrier(0);
+          const int i = e >> 1, c = e & 1;
+          const float x = __builtin_fmaf(s[c][i], f[c], -ls[i >> 2][i & 3]);
+          if (e % EACH == 0) product(e / EACH);
+          if (e >= L) {
+            part[c] += y[e % L];
+            asm volatile("" : "+v"(part[c]));   // (else the sums gather after the last product)
+          }
+          y[e % L] = __builtin_amdgcn_exp2f(x);
+          if (e % 8 == 7) ls[e / 8] = lse_of(next_ls, e / 8);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 0; e < L; ++e) part[e & 1] += y[e];
+      }
+      sum[0] += part[0];
+      sum[1] += part[1];
+    };
+    auto arrived = [&] {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
-      const bool more = rt + RT < r1;
-      if (more) issue(rt + RT, slot ^ 1);
-#pragma unroll 1
-      for (int rb = 0; rb < 2; ++rb) {
-        const int ra = rt + 32 * rb, rz = min(ra + 31, r1 - 1);
-        if (ra >= r1) break;
-        const int pa = q.base + token_of(a, ra), pz = q.base + token_of(a, rz);
-        if (k0 > pz || k0 + 63 <= pa - win) continue;   // nothing of the wave's keys is seen
-        f32x16 s[2] = {f32x16{}, f32x16{}};
+    };
+    auto begin = [&](int at) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          const u32x4 qf = sh.q[slot][2 * k + hi][32 * rb + col];
-          s[0] = mfma32<A>(qf, kf[0][k], s[0]);
-          s[1] = mfma32<A>(qf, kf[1][k], s[1]);
-        }
-        const bool edge = k0 + 63 > pa || k0 <= pz - win || ra + 31 >= r1;
+      for (int k = 0; k < R; ++k) fr[k] = operand(at, k);
+    };
+    if (r0 < r1) {
+      issue(r0, 0);
+      arrived();
+      if (r0 + RT < r1) issue(r0 + RT, 1);
+      f32x16 s0[2], s1[2];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const f32x4 ls = *reinterpret_cast<const f32x4*>(&sh.lse[slot][32 * rb + 8 * b + 4 * hi]);
+      for (int k = 0; k < NQ; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < 2; ++c) s0[c] = mfma32<A>(operand(0, k), kf[c][k], k ? s0[c] : f32x16{});
+      constexpr int HALF32 = 32 / B * 16 * P;   // distance of 32 rows
+      begin(HALF32);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][4 * b + i], f[c], -ls[i]));
-              if (edge) {
-                const int row = ra + 8 * b + 4 * hi + i, j = k0 + 32 * c + col;
-                const int pos = q.base + token_of(a, row);
-                p = row < r1 && j <= pos && j > pos - win ? p : 0.f;
-              }
-              sum[c] += p;
-            }
-        }
+      for (int b = 0; b < 4; ++b) ls[b] = lse_of(&sh.lse[0][0], b);
+      int n = 0;
+      for (int rt = r0; rt < r1; rt += RT, ++n) {
+        const int here = (n & 1) * S::SLOT, next = S::SLOT - here;
+        const float* lse = &sh.lse[n & 3][0];
+        step(std::true_type{}, s0, s1, here + HALF32, here + S::HALF, lse + 32, rt);
+        step(std::true_type{}, s1, s0, here + S::HALF, here + S::HALF + HALF32, lse + 64, rt + 32);
+        step(std::false_type{}, s0, s1, here + S::HALF + HALF32, 0, lse + 96, rt + 64);
+        arrived();   // the next tile; this one's slot has been read
+        if (rt + 2 * RT < r1) issue(rt + 2 * RT, n + 2);
+        begin(next);
+        step(std::true_type{}, s1, s0, next, next + HALF32, &sh.lse[(n + 1) & 3][0], rt + 96);
       }
-      if (more && tid < RT) sh.lse[slot ^ 1][tid] = next_lse;
     }
     __syncthreads();   // the slots have been read
 #pragma unroll
     for (int c = 0; c < 2; ++c) sum[c] += __shfl_xor(sum[c], 32);
     const int j = k0 + lane;
     const int64_t at = ((int64_t)u.seq * kv.H + u.head) * a.w_ld;
-    if (j < n) a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + (hi ? sum[1] : sum[0]) : 0.f;
+    if (j < u.n) a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + (hi ? sum[1] : sum[0]) : 0.f;
   }
+}
+
+template <typename A, typename KV, int D>
+hipError_t launch_tiles(const WeighArgs& a, hipStream_t s) {
+  const size_t lds = sizeof(WeighShared<D>);
+  static PerDevice limit;   // the kernel's LDS, more than a block gets unasked, is a setting of each device
+  int device = -1;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess)
+    e = limit.done(device, [&] {
+      return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_weigh_tiles<A, KV, D>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(2 * a.n_cu / 8 * 8), dim3(256), lds, s, a);
+  return hipGetLastError();
 }
 
 template <typename A, typename KV, int D>
 hipError_t launch(const WeighArgs& a, hipStream_t s) {
   if ((int64_t)a.max_q_len * a.group <= 16)
-    hipLaunchKernelGGL((k_weigh_rows<A, KV, D>), dim3(4 * a.n_cu), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_weigh_rows<A, KV, D>), dim3(WR * a.n_cu), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(2 * a.n_cu / 8 * 8), dim3(256), 0, s, a);
+    return launch_tiles<A, KV, D>(a, s);
   return hipGetLastError();
 }
 template <typename A, typename KV>
