@@ -1764,9 +1764,9 @@ inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_
 // 255 / 198, 1000 over 30000 of 8 on 1 205 / 151; and below the line 4 x 128 over 2000 81 /
 // 72, 512 over 512 50 / 57, 1000 over 1000 of 32 on 32 54 / 55, 4096 over 4096 of 8 on 1 119 /
 // 131, 32 x 5 over 4096 115 / 117 (112 / 130), 16 x 300 over 300 of 32 on 32 69 / 80.
-inline bool wide_tiles(const AttendArgs& a, int blocks) {
+inline bool wide_tiles(const AttendArgs& a, int blocks, int least) {
   const int64_t rows = (int64_t)a.kv.n_tokens * a.group;
-  if (a.two_terms || rows < 512 * (int64_t)a.kv.n_seqs) return false;
+  if (a.two_terms || rows < least * (int64_t)a.kv.n_seqs) return false;
   int64_t keys = (int64_t)a.kv.nb * a.kv.T - a.max_q_len / 2;
   if (a.window > 0) keys = std::min<int64_t>(keys, a.window);
   return rows / 256 * a.kv.H * (keys / 64) >= 24 * (int64_t)blocks;
@@ -1794,7 +1794,7 @@ hipError_t launch_tiles(const AA& a, int G, hipStream_t s) {
   if (2 * tiles >= G) {
     constexpr int RB = 256 / (D / 4);
     const int rows = (int)std::min<int64_t>((int64_t)a.max_q_len * a.group, TT::TR);
-    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, 4)),
+    hipLaunchKernelGGL((k_attend_join<A, D, TT::TR, RB>), dim3(G, (unsigned)std::min((rows + RB - 1) / RB, is_tree<AA> ? 16 : 4)),
                        dim3(256), 0, s, a, G);
   } else {
     hipLaunchKernelGGL((k_attend_join_list<A, D, TT::TR>), dim3(2 * G), dim3(256), 0, s, a, G);
@@ -1816,7 +1816,7 @@ hipError_t launch(const AA& a, hipStream_t s) {
   } else {
     // FP8 of 64 elements has too few loads in a tile for eight waves
     constexpr bool wide = D / ET<KV>::E % 8 == 0;
-    if (wide && wide_tiles(a, G / 16 * 8)) return launch_tiles<A, KV, D, wide ? 8 : 4, AA>(a, G / 16 * 8, s);
+    if (wide && wide_tiles(a, G / 16 * 8, is_tree<AA> ? 160 : 512)) return launch_tiles<A, KV, D, wide ? 8 : 4, AA>(a, G / 16 * 8, s);
     return launch_tiles<A, KV, D, 4, AA>(a, G, s);
   }
   return hipGetLastError();

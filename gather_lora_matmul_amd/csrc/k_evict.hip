@@ -16,143 +16,688 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   if ((b & 0x7fffffffu) > 0x7f800000u) return 1u;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ int select_tokens(const SelectArgs& a, int s) {
+  return (int)min((int64_t)kv_seq(a.kv, s).end, a.w_ld);
+}
+// The tokens of one (sequence, head).
 struct Ranks {
   const float* w;
   const int32_t *ktab, *vtab;
   int n, sinks, late;   // tokens; the first `sinks` and those from `late` on stay
   bool all;             // every token has pages
-  __device__ uint32_t of(const KvView& kv, int j, float x) const {
-    if (!all) {
-      const int b = (int)kv_div(kv, (uint32_t)j);
-      if ((unsigned)ktab[b] >= (unsigned)kv.n_pages || (unsigned)vtab[b] >= (unsigned)kv.n_pages) return 0u;
-    }
-    return j < sinks || j >= late ? 0xffffffffu : rank_of(x);
-  }
 };
-__device__ __forceinline__ int select_tokens(const SelectArgs& a, int s) {
-  return (int)min((int64_t)kv_seq(a.kv, s).end, a.w_ld);
-}
-
-// Tokens of a (sequence, head) that have pages.
-__global__ __launch_bounds__(256) void k_select_count(SelectArgs a, int32_t* __restrict__ counts) {
+__device__ __forceinline__ Ranks ranks_of(const SelectArgs& a, int s, int h) {
   const KvView& kv = a.kv;
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
-  const int n = select_tokens(a, s);
-  const int32_t* ktab = kv.table + ((int64_t)s * 2 * kv.H + h) * kv.nb;
-  const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
-  int c = 0;
-  for (int b = tid; (int64_t)b * kv.T < n; b += 256)
-    if ((unsigned)ktab[b] < (unsigned)kv.n_pages && (unsigned)vtab[b] < (unsigned)kv.n_pages) c += min(kv.T, n - b * kv.T);
-  __shared__ int part[4];
-#pragma unroll
-  for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d);
-  if ((tid & 63) == 0) part[tid >> 6] = c;
-  __syncthreads();
-  if (tid == 0) counts[(int64_t)s * kv.H + h] = part[0] + part[1] + part[2] + part[3];
-}
-
-template <int THREADS>
-__global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t* __restrict__ counts) {
-  constexpr int W = THREADS / 64, BINS = 2048;
-  __shared__ uint32_t bins[BINS];
-  __shared__ uint32_t part[W], part2[W];
-  __shared__ uint32_t found[2];
-  const KvView& kv = a.kv;
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = select_tokens(a, s);
-  int least = n;   // present tokens of the head that has fewest
-  for (int i = tid; i < kv.H; i += THREADS) least = min(least, counts[(int64_t)s * kv.H + i]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) least = min(least, __shfl_xor(least, d));
-  if (lane == 0) part[wave] = (uint32_t)least;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < W; ++w) least = min(least, (int)part[w]);
-  __syncthreads();
-  const int K = min(a.budget, least);
-  if (h == 0 && tid == 0) a.n_keep[s] = K;
   Ranks r;
   r.w = a.weights + ((int64_t)s * kv.H + h) * a.w_ld;
   r.ktab = kv.table + ((int64_t)s * 2 * kv.H + h) * kv.nb;
   r.vtab = r.ktab + (int64_t)kv.H * kv.nb;
-  r.n = n;
+  r.n = select_tokens(a, s);
   r.sinks = a.sinks;
   r.late = kv_seq(a.kv, s).end - a.recent;
-  r.all = counts[(int64_t)s * kv.H + h] == n;
-  // the rank of the last token that stays, 11, 11 and 10 bits at a time
-  uint32_t prefix = 0, need = (uint32_t)K;   // of the ranks that begin like prefix, need stay
-  if (K > 0)
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), nb = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < nb; i += THREADS) bins[i] = 0;
-      __syncthreads();
-      for (int j = tid; j < n; j += THREADS) {
-        const uint32_t x = r.of(kv, j, r.w[j]);
-        const bool in = pass == 0 || (pass == 1 ? x >> 21 == prefix >> 21 : x >> 10 == prefix >> 10);
-        if (in) atomicAdd(&bins[(x >> shift) & (uint32_t)(nb - 1)], 1u);
-      }
-      __syncthreads();
-      // bins from the top: thread t has `each` of them
-      const int each = nb / THREADS > 0 ? nb / THREADS : 1;
-      uint32_t own = 0;
-      const int top = nb - 1 - tid * each;
-      if (top >= 0)
-        for (int i = 0; i < each; ++i) own += bins[top - i];
-      uint32_t sum = own;
+  r.all = true;
+  return r;
+}
+__device__ __forceinline__ bool has_pages(const KvView& kv, const Ranks& r, int b) {
+  return (unsigned)r.ktab[b] < (unsigned)kv.n_pages && (unsigned)r.vtab[b] < (unsigned)kv.n_pages;
+}
+// Ranks of a wave's per * 64 tokens from j0 on (per <= PER), 64 at a time; 0: there is none.
+// (Values are selected, not written on a condition: the compiler keeps the array in registers
+// and loses such a write.)
+template <int PER>
+__device__ __forceinline__ void load_weights(const Ranks& r, int j0, int per, float (&w)[PER]) {
+  const int lane = threadIdx.x & 63, last = max(r.n - 1, 0);
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t z = __shfl_up(sum, d);
-        if (lane >= d) sum += z;
-      }
-      if (lane == 63) part[wave] = sum;
-      __syncthreads();
-      for (int w = 0; w < wave; ++w) sum += part[w];
-      if (sum >= need && sum - own < need) {   // one thread
-        uint32_t before = sum - own;
-        int i = 0;
-        while (before + bins[top - i] < need) before += bins[top - i++];
-        found[0] = (uint32_t)(top - i);
-        found[1] = need - before;
-      }
-      __syncthreads();
-      prefix |= found[0] << shift;
-      need = found[1];
-      __syncthreads();
+  for (int i = 0; i < PER; i += 4) {
+    if (i && i >= per) break;
+#pragma unroll
+    for (int k = i; k < i + 4 && k < PER; ++k) w[k] = r.w[min(j0 + k * 64 + lane, last)];   // (w_ld is at least 1)
+  }
+}
+template <int PER>
+__device__ __forceinline__ void to_ranks(const KvView& kv, const Ranks& r, int j0, int per, const float (&w)[PER],
+                                         uint32_t (&x)[PER]) {
+  const int lane = threadIdx.x & 63, last = max(r.n - 1, 0);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = j0 + i * 64 + lane;
+    const uint32_t y = j < r.sinks || j >= r.late ? 0xffffffffu : rank_of(w[i]);
+    x[i] = j < r.n && i < per ? y : 0u;
+  }
+  if (r.all) return;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = (int)kv_div(kv, (uint32_t)min(j0 + i * 64 + lane, last));
+    const bool ok = (unsigned)r.ktab[b] < (unsigned)kv.n_pages & (unsigned)r.vtab[b] < (unsigned)kv.n_pages;
+    x[i] = ok ? x[i] : 0u;
+  }
+}
+template <int PER>
+__device__ __forceinline__ void load_ranks(const KvView& kv, const Ranks& r, int j0, int per, uint32_t (&x)[PER]) {
+  float w[PER];
+  load_weights<PER>(r, j0, per, w);
+  to_ranks<PER>(kv, r, j0, per, w, x);
+}
+
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x = min(x, __shfl_xor(x, d));
+  return x;
+}
+// Tokens of a head that have pages, by a wave.
+__device__ __forceinline__ int count_present(const KvView& kv, const Ranks& r) {
+  int c = 0;
+  for (int b = threadIdx.x & 63; (int64_t)b * kv.T < r.n; b += 64)
+    if (has_pages(kv, r, b)) c += min(kv.T, r.n - b * kv.T);
+  return wave_sum(c);
+}
+
+__device__ __forceinline__ int lanes_below(unsigned long long m) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// Whether the thread, of a block's THREADS, finds a page of the sequence's n tokens missing, of
+// any head.
+template <int THREADS>
+__device__ __forceinline__ bool some_absent(const KvView& kv, int s, int n) {
+  constexpr int U = 8;   // ids on their way at a time
+  const int used = (n + kv.T - 1) / kv.T, ids = 2 * kv.H * kv.nb, step = THREADS % kv.nb;
+  const int32_t* tab = kv.table + (int64_t)s * ids;
+  int column = (int)threadIdx.x % kv.nb;
+  bool bad = false;
+  for (int i0 = threadIdx.x; i0 < ids; i0 += U * THREADS) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = tab[min(i0 + u * THREADS, ids - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bad |= i0 + u * THREADS < ids & column < used & (unsigned)id[u] >= (unsigned)kv.n_pages;
+      column += step;
+      column -= column >= kv.nb ? kv.nb : 0;
     }
-  // the list: every wave an equal run of tokens, those of larger rank and the first of the
-  // equal ones
-  const int each = (n + THREADS - 1) / THREADS * 64, j0 = min(wave * each, n), j1 = min(j0 + each, n);
-  uint32_t more = 0, same = 0;
-  if (K > 0)
-    for (int j = j0; j < j1; j += 64) {
-      const uint32_t x = j + lane < j1 ? r.of(kv, j + lane, r.w[j + lane]) : 0u;
-      more += (uint32_t)__popcll(__ballot(j + lane < j1 && x > prefix));
-      same += (uint32_t)__popcll(__ballot(j + lane < j1 && x == prefix));
+  }
+  return bad;
+}
+
+// What a block finds out in LDS.
+template <int THREADS, int BINS>
+struct SelectShared {
+  uint32_t bins[BINS];
+  uint32_t key[THREADS];   // ranks that begin alike, where they are few, and their tokens
+  int index[THREADS];
+  int part[THREADS / 64], part2[THREADS / 64];
+  uint32_t found[2];
+  int last;
+  uint32_t fill;
+};
+// The last rank that stays: all larger ones do, of the equal ones those of tokens up to `last`.
+struct Border {
+  uint32_t rank;
+  int last;
+};
+// The bin, from the top, in which the need-th of the ranks in sh.bins lies; need becomes what
+// that bin has to give.
+template <int NB, int THREADS, int BINS>
+__device__ __forceinline__ uint32_t find_bin(SelectShared<THREADS, BINS>& sh, uint32_t& need) {
+  constexpr int W = THREADS / 64, EACH = NB > THREADS ? NB / THREADS : 1;
+  static_assert(NB <= BINS && (NB % THREADS == 0 || THREADS % NB == 0), "bins divide over the threads");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int low = NB - (tid + 1) * EACH;   // the thread's bins: low .. low + EACH - 1, the top one first
+  uint32_t bin[EACH], own = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) own += bin[i] = low >= 0 ? sh.bins[low + i] : 0u;
+  uint32_t sum = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t z = __shfl_up(sum, d);
+    if (lane >= d) sum += z;
+  }
+  if (lane == 63) sh.part[wave] = (int)sum;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) sum += w < wave ? (uint32_t)sh.part[w] : 0u;
+  if (sum >= need && sum - own < need) {   // one thread
+    uint32_t before = sum - own, at = low, left = need;
+#pragma unroll
+    for (int i = EACH - 1; i >= 0; --i) {
+      const bool here = before < need && before + bin[i] >= need;
+      at = here ? low + i : at;
+      left = here ? need - before : left;
+      before += bin[i];
     }
-  if (lane == 0) {
-    part[wave] = more;
-    part2[wave] = same;
+    sh.found[0] = at;
+    sh.found[1] = left;
   }
   __syncthreads();
-  uint32_t at = 0, equal = 0;
-  for (int w = 0; w < wave; ++w) {
-    at += part[w];
-    equal += part2[w];
+  need = sh.found[1];
+  return sh.found[0];
+}
+// Of ranks that begin with `prefix` down to bit `shift` the border, `need` of them above or
+// at it: the ranks that each(f) gives f(rank, token) for, in any order.  `count` of them.
+template <int THREADS, int BINS, typename Each>
+__device__ __forceinline__ Border border_of(SelectShared<THREADS, BINS>& sh, uint32_t prefix, int shift, uint32_t need,
+                                            uint32_t count, Each each) {
+  const int tid = threadIdx.x;
+  while (count > THREADS && shift > 0) {
+    // 11 bits at a time, the last ones together with 0s
+    const int next = max(shift - 11, 0), less = 11 - (shift - next);
+    for (int i = tid; i < 2048; i += THREADS) sh.bins[i] = 0;
+    __syncthreads();
+    each([&](uint32_t x, int) {
+      if (((uint64_t)x >> shift) == ((uint64_t)prefix >> shift)) atomicAdd(&sh.bins[(x >> next << less) & 2047u], 1u);
+    });
+    __syncthreads();
+    const uint32_t bin = find_bin<2048>(sh, need);
+    count = sh.bins[bin];
+    prefix |= bin >> less << next;
+    shift = next;
+    __syncthreads();
   }
-  at += min(equal, need);
-  int32_t* out = a.keep + ((int64_t)s * kv.H + h) * a.keep_ld;
-  if (K > 0)
-    for (int j = j0; j < j1; j += 64) {
-      const bool in = j + lane < j1;
-      const uint32_t x = in ? r.of(kv, j + lane, r.w[j + lane]) : 0u;
-      const unsigned long long below = (1ull << lane) - 1, eq = __ballot(in && x == prefix);
-      const bool stay = in && (x > prefix || (x == prefix && equal + (uint32_t)__popcll(eq & below) < need));
-      const unsigned long long st = __ballot(stay);
-      if (stay) out[at + (uint32_t)__popcll(st & below)] = j + lane;
-      at += (uint32_t)__popcll(st);
-      equal += (uint32_t)__popcll(eq);
+  if (count > THREADS) {   // equal ranks: the need-th token of them, bit by bit
+    int last = 0;
+    for (int bit = 30; bit >= 0; --bit) {
+      int c = 0;
+      each([&](uint32_t x, int j) { c += x == prefix && j < (last | 1 << bit); });
+      c = wave_sum(c);
+      if ((tid & 63) == 0) sh.part[tid >> 6] = c;
+      __syncthreads();
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 64; ++w) c += sh.part[w];
+      __syncthreads();
+      if ((uint32_t)c < need) last |= 1 << bit;
     }
+    return Border{prefix, last};   // fewer than `need` lie before it
+  }
+  if (tid == 0) sh.fill = 0;
+  __syncthreads();
+  each([&](uint32_t x, int j) {
+    if (((uint64_t)x >> shift) == ((uint64_t)prefix >> shift)) {
+      const uint32_t at = atomicAdd(&sh.fill, 1u);
+      sh.key[at] = x;
+      sh.index[at] = j;
+    }
+  });
+  __syncthreads();
+  if (tid < (int)count) {
+    const uint32_t x = sh.key[tid];
+    const int j = sh.index[tid];
+    uint32_t before = 0;
+#pragma unroll 4
+    for (uint32_t i = 0; i < count; ++i) before += sh.key[i] > x || (sh.key[i] == x && sh.index[i] < j);
+    if (before == need - 1) {   // one thread
+      sh.found[0] = x;
+      sh.last = j;
+    }
+  }
+  __syncthreads();
+  return Border{sh.found[0], sh.last};
+}
+__device__ __forceinline__ bool stays(const Border& b, uint32_t x, int j) {
+  return x > b.rank || (x == b.rank && j <= b.last);
+}
+// The tokens of a block's waves (per * 64 each, from j0 + wave * per * 64 on) that stay, to out,
+// which has `room` for that many.
+template <int THREADS, int PER, int BINS>
+__device__ __forceinline__ void emit(SelectShared<THREADS, BINS>& sh, const Border& b, int j0, int per,
+                                     const uint32_t (&x)[PER], int32_t* out, int room) {
+  constexpr int W = THREADS / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = j0 + wave * per * 64;
+  unsigned long long stay[PER];
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    stay[i] = __ballot(x[i] && stays(b, x[i], first + i * 64 + lane));
+    count += __popcll(stay[i]);
+  }
+  if (lane == 0) sh.part[wave] = count;
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) at += w < wave ? sh.part[w] : 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int place = at + lanes_below(stay[i]);
+    if (((stay[i] >> lane) & 1) && place < room) out[place] = first + i * 64 + lane;
+    at += __popcll(stay[i]);
+  }
+}
+
+// ---- caches of up to 2048 tokens: a wave for each ---------------------------------
+// The ranks of a (sequence, head) are in one wave's registers, so that nothing waits for
+// another wave but the look at the page ids, which the heads of a block share.
+constexpr int kWaveTokens = 2048, kWavePer = kWaveTokens / 64;
+
+struct WaveShared {
+  uint32_t bins[2048];
+  uint32_t key[64];
+  int index[64];
+};
+// (LDS is in order within a wave; the compiler has to be told)
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t z = __shfl_up(x, d);
+    x += lane >= d ? z : 0u;
+  }
+  return x;
+}
+__device__ __forceinline__ uint32_t wave_bin(const WaveShared& sh, uint32_t& need) {
+  const int lane = threadIdx.x & 63, low = 2048 - (lane + 1) * 32;
+  uint32_t own = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) own += sh.bins[low + ((i + lane) & 31)];   // (every lane another bank)
+  uint32_t sum = wave_scan(own);
+  const int src = __builtin_ctzll(__ballot(sum >= need));
+  const uint32_t before = __shfl(sum - own, src);
+  const int top = 2048 - src * 32 - 1;
+  const uint32_t v = lane < 32 ? sh.bins[top - lane] : 0u;
+  sum = before + wave_scan(v);
+  const int at = __builtin_ctzll(__ballot(sum >= need));
+  need -= __shfl(sum - v, at);
+  return (uint32_t)(top - at);
+}
+__global__ __launch_bounds__(256) void k_select_waves(SelectArgs a, const int32_t* __restrict__ counts) {
+  __shared__ WaveShared shared[4];
+  __shared__ int present[kKvMaxHeads];
+  const KvView& kv = a.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), s = blockIdx.y, h = (int)blockIdx.x * 4 + wave;
+  WaveShared& sh = shared[wave];
+  Ranks r = ranks_of(a, s, min(h, kv.H - 1));
+  const int n = uni(r.n), per = (n + 63) / 64;
+  float w[kWavePer];
+  load_weights<kWavePer>(r, 0, per, w);
+  int least = n;   // tokens that the head with fewest has
+  for (int i = lane; i < 2048 / 4; i += 64) reinterpret_cast<u32x4*>(sh.bins)[i] = u32x4{0, 0, 0, 0};
+  if (!counts) {
+    const bool bad = some_absent<256>(kv, s, n);
+    if (__syncthreads_or(bad)) {
+      for (int o = wave; o < kv.H; o += 4) {
+        const int c = count_present(kv, ranks_of(a, s, o));
+        if (lane == 0) present[o] = c;
+      }
+      __syncthreads();
+      for (int o = lane; o < kv.H; o += 64) least = min(least, present[o]);
+      least = wave_min(least);
+      r.all = present[min(h, kv.H - 1)] == n;
+    }
+  } else {
+    for (int o = lane; o < kv.H; o += 64) least = min(least, counts[(int64_t)s * kv.H + o]);
+    least = wave_min(least);
+    r.all = counts[(int64_t)s * kv.H + min(h, kv.H - 1)] == n;
+  }
+  if (h >= kv.H) return;
+  const int K = min(a.budget, uni(least));
+  if (h == 0 && lane == 0) a.n_keep[s] = K;
+  if (K == 0) return;
+  int32_t* out = a.keep + ((int64_t)s * kv.H + h) * a.keep_ld;
+  if (K == n) {   // all of them
+    for (int j = lane; j < n; j += 64) out[j] = j;
+    return;
+  }
+  uint32_t x[kWavePer];
+  to_ranks<kWavePer>(kv, r, 0, per, w, x);
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < kWavePer; ++i)
+    if (i < per && x[i]) atomicAdd(&sh.bins[x[i] >> 21], 1u);
+  wave_sync();
+  uint32_t need = (uint32_t)K;
+  uint32_t prefix = wave_bin(sh, need), count = sh.bins[prefix];
+  int shift = 21;
+  prefix <<= 21;
+  while (uni((int)count) > 64 && shift > 0) {   // 11 bits more, the last ones together with a 0
+    const int next = max(shift - 11, 0), less = 11 - (shift - next);
+    wave_sync();
+    for (int i = lane; i < 2048 / 4; i += 64) reinterpret_cast<u32x4*>(sh.bins)[i] = u32x4{0, 0, 0, 0};
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < kWavePer; ++i)
+      if (i < per && x[i] && x[i] >> shift == prefix >> shift) atomicAdd(&sh.bins[(x[i] >> next << less) & 2047u], 1u);
+    wave_sync();
+    const uint32_t bin = wave_bin(sh, need);
+    count = sh.bins[bin];
+    prefix |= bin >> less << next;
+    shift = next;
+  }
+  Border b{prefix, 0};
+  if (uni((int)count) > 64) {   // equal ranks: the need-th token of them
+    uint32_t before = 0;
+#pragma unroll
+    for (int i = 0; i < kWavePer; ++i) {
+      const unsigned long long m = __ballot(x[i] == prefix);
+      const unsigned long long hit = __ballot(((m >> lane) & 1) && before + (uint32_t)lanes_below(m) == need - 1);
+      b.last = hit ? i * 64 + __builtin_ctzll(hit) : b.last;
+      before += (uint32_t)__popcll(m);
+    }
+  } else {
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kWavePer; ++i) {
+      if (i < per) {
+        const bool in = x[i] && x[i] >> shift == prefix >> shift;
+        const unsigned long long m = __ballot(in);
+        if (in) {
+          sh.key[at + lanes_below(m)] = x[i];
+          sh.index[at + lanes_below(m)] = i * 64 + lane;
+        }
+        at += __popcll(m);
+      }
+    }
+    wave_sync();
+    const uint32_t mine = lane < at ? sh.key[lane] : 0u;
+    const int j = lane < at ? sh.index[lane] : 0;
+    uint32_t before = 0;
+    for (int i = 0; i < at; ++i) {   // (they lie in their tokens' order)
+      const uint32_t y = (uint32_t)__builtin_amdgcn_readlane((int)mine, i);
+      before += y > mine || (y == mine && i < lane);
+    }
+    const unsigned long long hit = __ballot(lane < at && before == need - 1);
+    const int src = hit ? __builtin_ctzll(hit) : 0;
+    b.rank = (uint32_t)__builtin_amdgcn_readlane((int)mine, src);
+    b.last = __builtin_amdgcn_readlane(j, src);
+  }
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < kWavePer; ++i) {
+    if (i < per) {
+      const bool stay = x[i] && stays(b, x[i], i * 64 + lane);
+      const unsigned long long m = __ballot(stay);
+      const int place = at + lanes_below(m);
+      if (stay && place < K) out[place] = i * 64 + lane;
+      at += __popcll(m);
+    }
+  }
+}
+
+// ---- caches of up to a chunk: a block for each --------------------------------------
+// A block has a (sequence, head) with its ranks in registers: the 11 leading bits of all of
+// them in bins, then the few that share the border's bin compared one with another.  Bound by
+// its rounds through LDS (about a dozen barriers).
+template <int THREADS, int PER>
+__global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t* __restrict__ counts) {
+  constexpr int W = THREADS / 64, BINS = 2048;
+  __shared__ SelectShared<THREADS, BINS> sh;
+  __shared__ int present[kKvMaxHeads];
+  const KvView& kv = a.kv;
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  Ranks r = ranks_of(a, s, h);
+  const int n = uni(r.n), per = (n + THREADS - 1) / THREADS, first = wave * per * 64;
+  int least = n;   // tokens that the head with fewest has
+  uint32_t x[PER];
+  if (!counts) {
+    load_ranks<PER>(kv, r, first, per, x);
+    const bool bad = some_absent<THREADS>(kv, s, n);
+    for (int i = tid; i < BINS; i += THREADS) sh.bins[i] = 0;
+    if (__syncthreads_or(bad)) {
+      for (int o = wave; o < kv.H; o += W) {
+        const int c = count_present(kv, ranks_of(a, s, o));
+        if (lane == 0) present[o] = c;
+      }
+      __syncthreads();
+      for (int o = lane; o < kv.H; o += 64) least = min(least, present[o]);
+      least = wave_min(least);
+      r.all = present[h] == n;
+      if (!r.all) load_ranks<PER>(kv, r, first, per, x);
+    }
+  } else {
+    for (int o = lane; o < kv.H; o += 64) least = min(least, counts[(int64_t)s * kv.H + o]);
+    least = wave_min(least);
+    r.all = counts[(int64_t)s * kv.H + h] == n;
+    load_ranks<PER>(kv, r, first, per, x);
+    for (int i = tid; i < BINS; i += THREADS) sh.bins[i] = 0;
+    __syncthreads();
+  }
+  const int K = min(a.budget, uni(least));
+  if (h == 0 && tid == 0) a.n_keep[s] = K;
+  if (K == 0) return;
+  int32_t* out = a.keep + ((int64_t)s * kv.H + h) * a.keep_ld;
+  if (K == n) {   // all of them
+    for (int j = tid; j < n; j += THREADS) out[j] = j;
+    return;
+  }
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i < per && x[i]) f(x[i], first + i * 64 + lane);
+  };
+  each([&](uint32_t y, int) { atomicAdd(&sh.bins[y >> 21], 1u); });
+  __syncthreads();
+  uint32_t need = (uint32_t)K;
+  const uint32_t bin = find_bin<BINS>(sh, need), count = sh.bins[bin];
+  const Border b = border_of(sh, bin << 21, 21, need, count, each);
+  emit(sh, b, 0, per, x, out, K);
+}
+
+// Tokens of every (sequence, head) that have pages.
+__global__ __launch_bounds__(64) void k_select_count(SelectArgs a, int32_t* __restrict__ counts) {
+  const int h = blockIdx.x, s = blockIdx.y, c = count_present(a.kv, ranks_of(a, s, h));
+  if (threadIdx.x == 0) counts[(int64_t)s * a.kv.H + h] = c;
+}
+
+// ---- long caches: three launches over chunks of them -------------------------------
+// 1: a chunk's ranks in bins (12 bits) and its present tokens; 2: every block adds up the
+// chunks' bins, finds the border's bin and leaves its own ranks of that bin in one list; 3: every
+// block finds the border among these and writes the tokens of its chunk that stay.
+constexpr int kChunk = 8192, kLongThreads = 512, kLongPer = kChunk / kLongThreads, kLongBins = 4096;
+constexpr int kListed = 4096;   // ranks of the border's bin that have a place; with more, all are read again
+
+struct ChunkInfo {
+  int32_t present;   // tokens with pages
+  int32_t above;     // ranks above the border's bin, and in it (from the second launch)
+  int32_t in;
+  int32_t pad;
+};
+// The workspace of a (sequence, head).
+struct LongSpace {
+  ChunkInfo* info;       // [chunks]
+  uint2* list;           // [kListed] rank, token
+  uint16_t* bins;        // [chunks][kLongBins]
+  static __host__ __device__ size_t bytes(int chunks) {
+    return (size_t)chunks * (sizeof(ChunkInfo) + kLongBins * sizeof(uint16_t)) + kListed * sizeof(uint2);
+  }
+  __device__ LongSpace(char* ws, int64_t i, int chunks) {
+    ws += i * bytes(chunks);
+    info = reinterpret_cast<ChunkInfo*>(ws);
+    list = reinterpret_cast<uint2*>(ws + chunks * sizeof(ChunkInfo));
+    bins = reinterpret_cast<uint16_t*>(list + kListed);
+  }
+};
+using LongShared = SelectShared<kLongThreads, kLongBins>;
+
+// Tokens that stay, from the chunks' counts of all heads, and whether the head's are all there.
+__device__ __forceinline__ int long_budget(const SelectArgs& a, int s, int h, int chunks, Ranks& r, int* sh) {
+  const KvView& kv = a.kv;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, used = (r.n + kChunk - 1) / kChunk;
+  int least = r.n;
+  for (int o = wave; o < kv.H; o += kLongThreads / 64) {
+    const LongSpace sp(a.ws, (int64_t)s * kv.H + o, chunks);
+    int c = 0;
+    for (int i = lane; i < used; i += 64) c += sp.info[i].present;
+    c = wave_sum(c);
+    least = min(least, c);
+    if (o == h && lane == 0) sh[kLongThreads / 64] = c;
+  }
+  if (lane == 0) sh[wave] = least;
+  __syncthreads();
+  for (int w = 0; w < kLongThreads / 64; ++w) least = min(least, sh[w]);
+  r.all = sh[kLongThreads / 64] == r.n;
+  return min(a.budget, least);
+}
+
+__global__ __launch_bounds__(kLongThreads) void k_select_bins(SelectArgs a, int chunks) {
+  __shared__ uint32_t bins[kLongBins];
+  __shared__ int part[kLongThreads / 64];
+  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, wave = tid >> 6;
+  Ranks r = ranks_of(a, s, h);
+  const int j0 = ch * kChunk;
+  if (j0 >= r.n) return;
+  uint32_t x[kLongPer];
+  for (int i = tid; i < kLongBins; i += kLongThreads) bins[i] = 0;
+  load_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, x);
+  bool bad = false;
+  for (int b = (int)kv_div(a.kv, (uint32_t)j0) + tid; b * a.kv.T < min(r.n, j0 + kChunk); b += kLongThreads) bad |= !has_pages(a.kv, r, b);
+  if (__syncthreads_or(bad)) {
+    r.all = false;
+    load_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, x);
+  }
+  int c = 0;
+#pragma unroll
+  for (int i = 0; i < kLongPer; ++i)
+    if (x[i]) {
+      atomicAdd(&bins[x[i] >> 20], 1u);
+      ++c;
+    }
+  c = wave_sum(c);
+  if ((tid & 63) == 0) part[wave] = c;
+  __syncthreads();
+  const LongSpace sp(a.ws, (int64_t)s * a.kv.H + h, chunks);
+  for (int i = tid; i < kLongBins / 2; i += kLongThreads)
+    reinterpret_cast<uint32_t*>(sp.bins + (int64_t)ch * kLongBins)[i] = bins[2 * i] | bins[2 * i + 1] << 16;
+  if (tid == 0) {
+    c = 0;
+    for (int w = 0; w < kLongThreads / 64; ++w) c += part[w];
+    sp.info[ch].present = c;
+  }
+}
+
+__global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int chunks) {
+  __shared__ LongShared sh;
+  __shared__ int counts[kLongThreads / 64 + 1];
+  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  Ranks r = ranks_of(a, s, h);
+  const int j0 = ch * kChunk;
+  if (ch == 0 && h == 0 && r.n == 0 && tid == 0) a.n_keep[s] = 0;
+  if (j0 >= r.n) return;
+  float wt[kLongPer];
+  load_weights<kLongPer>(r, j0 + wave * kLongPer * 64, kLongPer, wt);
+  const LongSpace sp(a.ws, (int64_t)s * a.kv.H + h, chunks);
+  const int used = (r.n + kChunk - 1) / kChunk;
+  // thread t adds up the bins 8 t .. 8 t + 7
+  constexpr int PER = kLongBins / kLongThreads;
+  static_assert(PER == 8, "16 bytes a thread");
+  uint32_t sum[PER] = {};
+#pragma unroll 4
+  for (int i = 0; i < used; ++i) {
+    const uint4 v = ld16(sp.bins + (int64_t)i * kLongBins + tid * PER);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < PER; ++j) sum[j] += (w[j / 2] >> (16 * (j & 1))) & 0xffffu;
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) sh.bins[tid * PER + j] = sum[j];
+  const int K = long_budget(a, s, h, chunks, r, counts);   // (a barrier in it)
+  if (ch == 0 && h == 0 && tid == 0) a.n_keep[s] = K;
+  if (K == 0 || K == r.n) return;
+  uint32_t x[kLongPer];
+  to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
+  uint32_t need = (uint32_t)K;
+  const uint32_t bin = find_bin<kLongBins>(sh, need);
+  // the list's places before this chunk's
+  int before = 0;
+  for (int i = lane; i < ch; i += 64) before += sp.bins[(int64_t)i * kLongBins + bin];
+  before = wave_sum(before);
+  int above = 0, in = 0;
+#pragma unroll
+  for (int i = 0; i < kLongPer; ++i) {
+    above += __popcll(__ballot(x[i] >> 20 > bin));
+    in += __popcll(__ballot(x[i] >> 20 == bin && x[i]));
+  }
+  if (lane == 0) {
+    sh.part[wave] = in;
+    sh.part2[wave] = above;
+  }
+  __syncthreads();
+  int at = before;
+  for (int w = 0; w < wave; ++w) at += sh.part[w];
+#pragma unroll
+  for (int i = 0; i < kLongPer; ++i) {
+    const bool mine = x[i] >> 20 == bin && x[i];
+    const unsigned long long m = __ballot(mine);
+    const int place = at + __popcll(m & ((1ull << lane) - 1));
+    if (mine && place < kListed) sp.list[place] = uint2{x[i], (uint32_t)(j0 + (wave * kLongPer + i) * 64 + lane)};
+    at += __popcll(m);
+  }
+  if (tid == 0) {
+    in = above = 0;
+    for (int w = 0; w < kLongThreads / 64; ++w) {
+      in += sh.part[w];
+      above += sh.part2[w];
+    }
+    sp.info[ch].above = above;
+    sp.info[ch].in = in;
+  }
+}
+
+__global__ __launch_bounds__(kLongThreads) void k_select_long(SelectArgs a, int chunks) {
+  __shared__ LongShared sh;
+  __shared__ int counts[kLongThreads / 64 + 1];
+  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  Ranks r = ranks_of(a, s, h);
+  const int j0 = ch * kChunk;
+  if (j0 >= r.n) return;
+  float wt[kLongPer];
+  load_weights<kLongPer>(r, j0 + wave * kLongPer * 64, kLongPer, wt);
+  const int K = long_budget(a, s, h, chunks, r, counts);
+  if (K == 0) return;
+  int32_t* out = a.keep + ((int64_t)s * a.kv.H + h) * a.keep_ld;
+  if (K == r.n) {
+    for (int j = j0 + tid; j < min(r.n, j0 + kChunk); j += kLongThreads) out[j] = j;
+    return;
+  }
+  uint32_t x[kLongPer];
+  to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
+  const LongSpace sp(a.ws, (int64_t)s * a.kv.H + h, chunks);
+  const int used = (r.n + kChunk - 1) / kChunk;
+  int above = 0, in = 0, above_before = 0;
+  for (int i = lane; i < used; i += 64) {
+    const ChunkInfo c = sp.info[i];
+    above += c.above;
+    in += c.in;
+    if (i < ch) above_before += c.above;
+  }
+  above = wave_sum(above);
+  in = wave_sum(in);
+  above_before = wave_sum(above_before);
+  const uint32_t need = (uint32_t)(K - above);
+  Border b;
+  int at = above_before;   // tokens of the chunks before that stay
+  auto with = [&](auto each, uint32_t prefix) {
+    b = border_of(sh, prefix, 20, need, (uint32_t)in, each);
+    int c = 0;
+    each([&](uint32_t y, int j) { c += y >> 20 == prefix >> 20 && j < j0 && stays(b, y, j); });
+    c = wave_sum(c);
+    if (lane == 0) sh.part2[wave] = c;
+    __syncthreads();
+    for (int w = 0; w < kLongThreads / 64; ++w) at += sh.part2[w];
+  };
+  const uint32_t prefix = sp.list[0].x >> 20 << 20;
+  if (in <= kListed) {
+    with([&](auto f) {
+      for (int i = tid; i < in; i += kLongThreads) {
+        const uint2 v = sp.list[i];
+        f(v.x, (int)v.y);
+      }
+    }, prefix);
+  } else {   // (ranks that are nearly all alike)
+    with([&](auto f) {
+      for (int j = tid; j < r.n; j += kLongThreads) {
+        if (!r.all && !has_pages(a.kv, r, (int)kv_div(a.kv, (uint32_t)j))) continue;
+        f(j < r.sinks || j >= r.late ? 0xffffffffu : rank_of(r.w[j]), j);
+      }
+    }, prefix);
+  }
+  emit(sh, b, j0, kLongPer, x, out + at, K - at);
 }
 
 // ---- compact -----------------------------------------------------------------------
@@ -243,11 +788,8 @@ __device__ __forceinline__ Gathered<E> gather_v(const char* pages, const Steps<N
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int64_t f = st.from[1][x0 + e];
-    v[e] = 0;
-    if (f != kNone) {
-      v[e] = *reinterpret_cast<const B*>(pages + f + d * 16);
-      g.have |= 1u << e;
-    }
+    v[e] = *reinterpret_cast<const B*>(pages + (f == kNone ? 0 : f) + d * 16);   // (of page 0 where there is none)
+    g.have |= (uint32_t)(f != kNone) << e;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) g.w[i] = 0;
@@ -288,7 +830,11 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
   for (int u = 0; u < KU; ++u)
     if (st.from[0][x] != kNone) k[u] = ldv(kv.pages + st.from[0][x] + (int64_t)(u * 4 + (tid >> 6)) * kv.T * 16);
 #pragma unroll
-  for (int u = 0; u < VU; ++u) v[u] = gather_v<E>(kv.pages, st, (u * 256 + tid) / D * E, (u * 256 + tid) % D);
+  for (int u = 0; u < VU; ++u) {
+    const int x0 = uni((u * 256 + tid) / D * E);   // the same for a wave
+    v[u].have = 0;
+    if (x0 < p.first + p.n - pos0) v[u] = gather_v<E>(kv.pages, st, x0, (u * 256 + tid) % D);
+  }
   if (E == 16 && tid < 128 && st.from[tid >> 6][x] != kNone)
     sc[0] = kv.scales[scale_at<E, D>(kv, tid >> 6, st.from[tid >> 6][x])];
   float* weights = a.weights ? a.weights + ((int64_t)s * kv.H + h) * a.w_ld : nullptr;
@@ -328,7 +874,7 @@ __global__ __launch_bounds__(256) void k_compact(CompactArgs a, int columns) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             f[u] = x0 + 64 * u < n ? st.from[0][x0 + 64 * u + lane] : kNone;
-            if (f[u] != kNone) v[u] = ldv(kv.pages + f[u] + column);
+            v[u] = ldv(kv.pages + (f[u] == kNone ? 0 : f[u]) + column);   // (of page 0 where there is none)
           }
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -377,14 +923,34 @@ hipError_t compact(const CompactArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t select_workspace(int32_t n_seqs, int32_t H) { return (size_t)n_seqs * H * sizeof(int32_t); }
+// Caches of up to a chunk's tokens, as far as the host can tell, are one launch, or two where
+// one block would have to look at too many page ids of the other heads.
+static int64_t select_most(const KvView& v, int64_t w_ld) { return std::min<int64_t>((int64_t)v.nb * v.T, w_ld); }
+static bool counts_apart(const KvView& v) { return (int64_t)2 * v.H * v.nb > 8192; }
+
+size_t select_workspace(int32_t n_seqs, int32_t H, int64_t tokens) {
+  const size_t pairs = (size_t)n_seqs * H;
+  return std::max(pairs * sizeof(int32_t), tokens > kChunk ? pairs * LongSpace::bytes((int)((tokens + kChunk - 1) / kChunk)) : 0);
+}
 
 hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
-  int32_t* counts = reinterpret_cast<int32_t*>(a.ws);
+  const int64_t most = select_most(a.kv, a.w_ld);
+  if (most > kChunk) {
+    const int chunks = (int)((most + kChunk - 1) / kChunk);
+    const dim3 grid(chunks, a.kv.H, a.kv.n_seqs);
+    hipLaunchKernelGGL(k_select_bins, grid, dim3(kLongThreads), 0, s, a, chunks);
+    hipLaunchKernelGGL(k_select_list, grid, dim3(kLongThreads), 0, s, a, chunks);
+    hipLaunchKernelGGL(k_select_long, grid, dim3(kLongThreads), 0, s, a, chunks);
+    return hipGetLastError();
+  }
   const dim3 grid(a.kv.H, a.kv.n_seqs);
-  hipLaunchKernelGGL(k_select_count, grid, dim3(256), 0, s, a, counts);
-  if ((int64_t)a.kv.nb * a.kv.T <= 8192) hipLaunchKernelGGL((k_select<256>), grid, dim3(256), 0, s, a, counts);
-  else hipLaunchKernelGGL((k_select<1024>), grid, dim3(1024), 0, s, a, counts);
+  int32_t* counts = nullptr;
+  if (counts_apart(a.kv)) {
+    counts = reinterpret_cast<int32_t*>(a.ws);
+    hipLaunchKernelGGL(k_select_count, grid, dim3(64), 0, s, a, counts);
+  }
+  if (most <= kWaveTokens) hipLaunchKernelGGL(k_select_waves, dim3((a.kv.H + 3) / 4, a.kv.n_seqs), dim3(256), 0, s, a, counts);
+  else hipLaunchKernelGGL((k_select<1024, 8>), grid, dim3(1024), 0, s, a, counts);
   return hipGetLastError();
 }
 

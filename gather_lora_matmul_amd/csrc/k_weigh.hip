@@ -19,6 +19,8 @@ namespace {
 #ifndef WR
 #define WR 2
 #define NB8 4
+#define MAXP 8
+#define ROWS 32
 #endif
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -272,20 +274,43 @@ struct WeighShared {
   static __device__ __forceinline__ int row_at(int r) { return r % B * STEP + r / B * (16 * P); }
 };
 
+constexpr int kKeys = 256, kRows = 128;   // keys of a block's tile, rows of a step
+
+// Few tiles are cut by rows, all of them into the same number of parts, which walk the rows
+// in step and find them in their L2; a second launch joins the parts' sums in their order.
+struct WeighTile {
+  int32_t seq, head, tile, parts;   // (parts 1: the tile was not cut)
+};
+constexpr int kMaxParts = MAXP;
+// Units (tiles times parts) of a call of which tiles are cut: at most four a block.
+inline __host__ __device__ int most_units(int G) { return 4 * G; }
+// The parts that make the fewest rounds of G blocks, in tiles' lengths.
+__device__ __forceinline__ int parts_of(int tiles, int G) {
+  int best = 1;
+  for (int p = 2; p <= kMaxParts && tiles * p <= most_units(G); ++p)
+    if ((int64_t)((tiles * p + G - 1) / G) * best < (int64_t)((tiles * best + G - 1) / G) * p) best = p;
+  return best;
+}
+
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_weigh_tiles(WeighArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_weigh_tiles(WeighArgs a, WeighTile* tiles) {
   constexpr bool Q8 = is_quant<KV>();
   using S = WeighShared<D>;
-  constexpr int KT = 256, NQ = D / 16, RT = S::RT, P = S::P, B = S::B;
+  constexpr int KT = kKeys, NQ = D / 16, RT = S::RT, P = S::P, B = S::B;
+  static_assert(RT == kRows, "steps");
   extern __shared__ __align__(16) char smem[];
   S& sh = *reinterpret_cast<S*>(smem);
   const KvView& kv = a.kv;
-  const int units = tile_sums<KT, 256>(a, sh.pre);
+  const int all = tile_sums<KT, 256>(a, sh.pre);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, hi = lane >> 5;
+  const int cut = tiles && all <= most_units((int)gridDim.x) ? parts_of(all, (int)gridDim.x) : 1, units = all * cut;
+  float* const sums = reinterpret_cast<float*>(tiles + most_units((int)gridDim.x));   // [tile][part][KT]
+  if (tiles && all == 0 && blockIdx.x == 0 && tid == 0) tiles[0].parts = 1;
   // an eighth of the units to each XCD: the tiles of one head, which read the same rows, share its L2
   const int per = (units + 7) / 8, x0 = min(((int)blockIdx.x & 7) * per, units), x1 = min(x0 + per, units);
   for (int un = x0 + ((int)blockIdx.x >> 3); un < x1; un += (int)gridDim.x >> 3) {
-    const Unit u = unit_of<KT>(a, sh.pre, un);
+    const int part_no = un / all, tile_no = un - part_no * all;
+    const Unit u = unit_of<KT>(a, sh.pre, tile_no);
     const KvSeq& q = u.q;
     const int32_t* ktab = kv.table + ((int64_t)u.seq * 2 * kv.H + u.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
@@ -317,7 +342,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // of the sequence's rows those of tokens [t0, t1) see something of the block's keys
     const int t0 = max(u.tile - q.base, 0);
     const int t1 = a.window > 0 ? min(q.q_len, u.tile + KT - 1 + a.window - q.base) : q.q_len;
-    const int r0 = t0 * a.group, r1 = t1 * a.group;
+    int r0 = t0 * a.group, r1 = t1 * a.group;
+    if (cut > 1) {   // the part's steps of them
+      const int steps = max(r1 - r0 + RT - 1, 0) / RT;
+      r1 = min(r1, r0 + steps * (part_no + 1) / cut * RT);
+      r0 += steps * part_no / cut * RT;
+    }
     // rows rt .. rt + RT - 1 to a slot, their lse to LDS.  A lane finds the place of a row of
     // each 64, the loads take it from the lanes that have theirs
     auto issue = [&](int rt, int n) {
@@ -428,8 +458,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int here = (n & 1) * S::SLOT, next = S::SLOT - here;
         const float* lse = &sh.lse[n & 3][0];
         step(std::true_type{}, s0, s1, here + HALF32, here + S::HALF, lse + 32, rt);
+        if (rt + 32 >= r1) break;
         step(std::true_type{}, s1, s0, here + S::HALF, here + S::HALF + HALF32, lse + 64, rt + 32);
+        if (rt + 64 >= r1) break;
         step(std::false_type{}, s0, s1, here + S::HALF + HALF32, 0, lse + 96, rt + 64);
+        if (rt + 96 >= r1) break;
         arrived();   // the next tile; this one's slot has been read
         if (rt + 2 * RT < r1) issue(rt + 2 * RT, n + 2);
         begin(next);
@@ -441,9 +474,39 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int c = 0; c < 2; ++c) sum[c] += __shfl_xor(sum[c], 32);
     const int j = k0 + lane;
     const int64_t at = ((int64_t)u.seq * kv.H + u.head) * a.w_ld;
-    if (j < u.n) a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + (hi ? sum[1] : sum[0]) : 0.f;
+    const float got = hi ? sum[1] : sum[0];
+    if (cut > 1) sums[((int64_t)tile_no * cut + part_no) * KT + wave * 64 + lane] = got;
+    else if (j < u.n) a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + got : 0.f;
+    if (tiles && part_no == 0 && tid == 0 && tile_no < most_units((int)gridDim.x))
+      tiles[tile_no] = WeighTile{u.seq, u.head, u.tile, cut};
   }
 }
+
+// The parts of a tile together, a thread a key.
+__global__ __launch_bounds__(kKeys) void k_weigh_join(WeighArgs a, const WeighTile* __restrict__ tiles, int G) {
+  if (tiles[0].parts == 1) return;   // none is cut
+  __shared__ int pre[kKvMaxSeqs + 1];
+  if ((int)blockIdx.x >= tile_sums<kKeys, kKeys>(a, pre)) return;
+  const KvView& kv = a.kv;
+  const WeighTile d = tiles[blockIdx.x];
+  const float* sums = reinterpret_cast<const float*>(tiles + most_units(G)) + (int64_t)blockIdx.x * d.parts * kKeys + threadIdx.x;
+  float sum = 0.f;
+  for (int p = 0; p < d.parts; ++p) sum += sums[p * kKeys];
+  Unit u;
+  u.seq = d.seq;
+  unit_seq(a, u, nullptr);
+  const int j = d.tile + (int)threadIdx.x;
+  if (j >= u.n) return;
+  const int blk = (int)kv_div(kv, (uint32_t)j);
+  const int32_t* ktab = kv.table + ((int64_t)d.seq * 2 * kv.H + d.head) * kv.nb;
+  const bool there = (unsigned)ktab[blk] < (unsigned)kv.n_pages && (unsigned)ktab[(int64_t)kv.H * kv.nb + blk] < (unsigned)kv.n_pages;
+  const int64_t at = ((int64_t)d.seq * kv.H + d.head) * a.w_ld;
+  a.weights[at + j] = there ? old_weight(a, u, at, j) + sum : 0.f;
+}
+
+// Tiles may be cut where a head has more rows than four steps take.
+inline bool may_cut(int32_t group, int32_t max_q_len) { return (int64_t)max_q_len * group > 4 * kRows; }
+inline int blocks_of(int n_cu) { return 2 * n_cu / 8 * 8; }
 
 template <typename A, typename KV, int D>
 hipError_t launch_tiles(const WeighArgs& a, hipStream_t s) {
@@ -457,13 +520,16 @@ hipError_t launch_tiles(const WeighArgs& a, hipStream_t s) {
                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(2 * a.n_cu / 8 * 8), dim3(256), lds, s, a);
+  const int G = blocks_of(a.n_cu);
+  WeighTile* tiles = may_cut(a.group, a.max_q_len) ? reinterpret_cast<WeighTile*>(a.ws) : nullptr;
+  hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a, tiles);
+  if (tiles) hipLaunchKernelGGL(k_weigh_join, dim3(2 * G), dim3(kKeys), 0, s, a, tiles, G);
   return hipGetLastError();
 }
 
 template <typename A, typename KV, int D>
 hipError_t launch(const WeighArgs& a, hipStream_t s) {
-  if ((int64_t)a.max_q_len * a.group <= 16)
+  if ((int64_t)a.max_q_len * a.group <= ROWS)
     hipLaunchKernelGGL((k_weigh_rows<A, KV, D>), dim3(WR * a.n_cu), dim3(256), 0, s, a);
   else
     return launch_tiles<A, KV, D>(a, s);
@@ -476,7 +542,9 @@ hipError_t launch_d(const KvTypes& ty, const WeighArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t weigh_workspace(const KvTypes&, int32_t, int32_t, int32_t) { return 0; }
+size_t weigh_workspace(int32_t n_cu, int32_t group, int32_t max_q_len) {
+  return may_cut(group, max_q_len) ? (size_t)most_units(blocks_of(n_cu)) * (sizeof(WeighTile) + kKeys * sizeof(float)) : 0;
+}
 
 int64_t weigh_units(const KvView& v) { return (int64_t)v.n_seqs * v.H * ((int64_t)v.nb * v.T / 32 + 1); }
 

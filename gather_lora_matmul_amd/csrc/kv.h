@@ -189,7 +189,7 @@ struct WeighArgs {
   char* ws;
   int32_t n_cu;
 };
-size_t weigh_workspace(const KvTypes& ty, int32_t n_cu, int32_t group, int32_t max_q_len);
+size_t weigh_workspace(int32_t n_cu, int32_t group, int32_t max_q_len);
 int64_t weigh_units(const KvView& v);
 hipError_t launch_weigh(const KvTypes& ty, const WeighArgs& a, hipStream_t s);
 
@@ -204,7 +204,7 @@ struct SelectArgs {
   int32_t* n_keep;         // [n_seqs]
   char* ws;
 };
-size_t select_workspace(int32_t n_seqs, int32_t H);
+size_t select_workspace(int32_t n_seqs, int32_t H, int64_t tokens);   // tokens: that a table's row has place for
 hipError_t launch_select(const SelectArgs& a, hipStream_t s);
 
 struct CompactArgs {

@@ -314,7 +314,7 @@ lora_status lora_kv_weigh_workspace_size(const lora_pool* p, const lora_kv_desc*
   LORA_TRY(batch_sizes(b, T));
   if (!bytes) return fail(LORA_E_ARG, "null size");
   LORA_TRY(check_heads(d, n_q_heads, b));
-  *bytes = weigh_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, longest(b));
+  *bytes = weigh_workspace(p->n_cu, n_q_heads / d->n_kv_heads, longest(b));
   return LORA_OK;
 }
 
@@ -338,7 +338,7 @@ lora_status lora_kv_weigh(const lora_pool* p, const lora_kv_desc* d, const lora_
     LORA_TRY(check_rows(q_dev, q_ld, (int64_t)n_q_heads * d->head_dim, "q"));
     if (!lse_dev || ((uintptr_t)lse_dev & 3u)) return fail(LORA_E_ARG, "lse null or not 4-byte aligned");
   }
-  const size_t need = weigh_workspace(ty, p->n_cu, n_q_heads / d->n_kv_heads, longest(b));
+  const size_t need = weigh_workspace(p->n_cu, n_q_heads / d->n_kv_heads, longest(b));
   if (need) LORA_TRY(check_workspace(workspace_dev, ws_bytes, need, "lora_kv_weigh_workspace_size"));
   LORA_TRY(runnable(p));
   a.q = q_dev;
@@ -367,7 +367,7 @@ lora_status lora_kv_select_workspace_size(const lora_pool* p, const lora_kv_desc
   LORA_TRY(geometry(p, d, ty, T));
   LORA_TRY(batch_sizes(b, T));
   if (!bytes) return fail(LORA_E_ARG, "null size");
-  *bytes = select_workspace(b->n_seqs, d->n_kv_heads);
+  *bytes = select_workspace(b->n_seqs, d->n_kv_heads, (int64_t)b->max_blocks * T);
   return LORA_OK;
 }
 
@@ -386,7 +386,7 @@ lora_status lora_kv_select(const lora_pool* p, const lora_kv_desc* d, const lora
   if (keep_ld < budget) return fail(LORA_E_ARG, "keep_ld %lld < budget %d", (long long)keep_ld, budget);
   if ((!keep_dev && budget > 0) || ((uintptr_t)keep_dev & 3u) || !n_keep_dev || ((uintptr_t)n_keep_dev & 3u))
     return fail(LORA_E_ARG, "keep or n_keep null or not 4-byte aligned");
-  LORA_TRY(check_workspace(workspace_dev, ws_bytes, select_workspace(b->n_seqs, d->n_kv_heads),
+  LORA_TRY(check_workspace(workspace_dev, ws_bytes, select_workspace(b->n_seqs, d->n_kv_heads, (int64_t)b->max_blocks * a.kv.T),
                            "lora_kv_select_workspace_size"));
   LORA_TRY(runnable(p));
   a.weights = weights_dev;

@@ -570,3 +570,13 @@ def test_a_step_with_a_tree():
                 at = np.concatenate([np.arange(base[s]), base[s] + path[s, :int(n_out[s])].cpu().numpy()])
                 want = formula(host(one)[s:s + 1], c.kd[s][at], c.vd[s][at], np.ones((1, len(at)), bool), 0.1)
                 agree(host(o2)[s:s + 1], host(l2)[s:s + 1], want, "bf16" if kv == "fp8" else "f16", 2, "f16", len(at), str(s))
+
+
+def test_selection_in_tables_wider_than_the_caches():
+    # the launches follow the tables' width, the work the lengths
+    lens = [0, 5, 300, 9000, 8192, 20]
+    with empty_case(2, lens, seed=102, extra_blocks=300, drop=[(3, 4), (3, 270)]) as c:
+        for kind in ("random", "equal", "near"):
+            w = some_weights(c, 18000, 10, kind)
+            for budget, sinks, recent in ((0, 0, 0), (4, 4, 0), (250, 3, 40), (8999, 0, 0), (9000, 0, 9000)):
+                check_selection(c, w, budget, sinks, recent)
