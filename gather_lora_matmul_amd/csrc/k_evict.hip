@@ -13,8 +13,8 @@ namespace {
 // below all others), the first and the latest tokens above all, absent ones last.
 __device__ __forceinline__ uint32_t rank_of(float w) {
   const uint32_t b = __float_as_uint(w + 0.f);   // -0: 0
-  if ((b & 0x7fffffffu) > 0x7f800000u) return 1u;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t x = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return w != w ? 1u : x;
 }
 __device__ __forceinline__ int select_tokens(const SelectArgs& a, int s) {
   return (int)min((int64_t)kv_seq(a.kv, s).end, a.w_ld);
@@ -47,11 +47,11 @@ __device__ __forceinline__ bool has_pages(const KvView& kv, const Ranks& r, int 
 template <int PER>
 __device__ __forceinline__ void load_weights(const Ranks& r, int j0, int per, float (&w)[PER]) {
   const int lane = threadIdx.x & 63, last = max(r.n - 1, 0);
+  const float* at = r.w + j0 + lane;
 #pragma unroll
-  for (int i = 0; i < PER; i += 4) {
-    if (i && i >= per) break;
-#pragma unroll
-    for (int k = i; k < i + 4 && k < PER; ++k) w[k] = r.w[min(j0 + k * 64 + lane, last)];   // (w_ld is at least 1)
+  for (int i = 0; i < PER; ++i) {
+    if (j0 + i * 64 + 63 < r.n) w[i] = at[i * 64];
+    else if (i == 0 || i < per) w[i] = r.w[min(j0 + i * 64 + lane, last)];   // (w_ld is at least 1)
   }
 }
 template <int PER>
@@ -60,9 +60,14 @@ __device__ __forceinline__ void to_ranks(const KvView& kv, const Ranks& r, int j
   const int lane = threadIdx.x & 63, last = max(r.n - 1, 0);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int j = j0 + i * 64 + lane;
-    const uint32_t y = j < r.sinks || j >= r.late ? 0xffffffffu : rank_of(w[i]);
-    x[i] = j < r.n && i < per ? y : 0u;
+    const int a = j0 + i * 64, j = a + lane;
+    x[i] = 0u;
+    if (i < per) {
+      const uint32_t y = rank_of(w[i]);
+      x[i] = y;
+      // (the first and the latest tokens, and the last ones)
+      if (a < r.sinks || a + 63 >= r.late || a + 63 >= r.n) x[i] = j >= r.n ? 0u : (j < r.sinks || j >= r.late ? 0xffffffffu : y);
+    }
   }
   if (r.all) return;
 #pragma unroll
@@ -315,6 +320,8 @@ __global__ __launch_bounds__(256) void k_select_waves(SelectArgs a, const int32_
   WaveShared& sh = shared[wave];
   Ranks r = ranks_of(a, s, min(h, kv.H - 1));
   const int n = uni(r.n), per = (n + 63) / 64;
+  r.n = n;
+  r.late = uni(r.late);
   float w[kWavePer];
   load_weights<kWavePer>(r, 0, per, w);
   int least = n;   // tokens that the head with fewest has
@@ -433,6 +440,8 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   Ranks r = ranks_of(a, s, h);
   const int n = uni(r.n), per = (n + THREADS - 1) / THREADS, first = wave * per * 64;
+  r.n = n;
+  r.late = uni(r.late);
   int least = n;   // tokens that the head with fewest has
   uint32_t x[PER];
   if (!counts) {
@@ -586,13 +595,22 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
   // thread t adds up the bins 8 t .. 8 t + 7
   constexpr int PER = kLongBins / kLongThreads;
   static_assert(PER == 8, "16 bytes a thread");
-  uint32_t sum[PER] = {};
-#pragma unroll 4
-  for (int i = 0; i < used; ++i) {
-    const uint4 v = ld16(sp.bins + (int64_t)i * kLongBins + tid * PER);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t sum[PER] = {}, earlier[PER] = {};   // of all chunks, of those before this one
+  for (int i0 = 0; i0 < used; i0 += 8) {
+    uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) sum[j] += (w[j / 2] >> (16 * (j & 1))) & 0xffffu;
+    for (int i = 0; i < 8; ++i) v[i] = ld16(sp.bins + (int64_t)min(i0 + i, used - 1) * kLongBins + tid * PER);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      const uint32_t in = i0 + i < used ? 0xffffu : 0u, before = i0 + i < ch ? 0xffffu : 0u;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const uint32_t c = w[j / 2] >> (16 * (j & 1));
+        sum[j] += c & in;
+        earlier[j] += c & before;
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j) sh.bins[tid * PER + j] = sum[j];
@@ -603,10 +621,12 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
   to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
   uint32_t need = (uint32_t)K;
   const uint32_t bin = find_bin<kLongBins>(sh, need);
-  // the list's places before this chunk's
-  int before = 0;
-  for (int i = lane; i < ch; i += 64) before += sp.bins[(int64_t)i * kLongBins + bin];
-  before = wave_sum(before);
+  if (tid == (int)bin / PER) {   // the list's places before this chunk's
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c = j == (int)bin % PER ? earlier[j] : c;
+    sh.last = (int)c;
+  }
   int above = 0, in = 0;
 #pragma unroll
   for (int i = 0; i < kLongPer; ++i) {
@@ -618,7 +638,7 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
     sh.part2[wave] = above;
   }
   __syncthreads();
-  int at = before;
+  int at = sh.last;
   for (int w = 0; w < wave; ++w) at += sh.part[w];
 #pragma unroll
   for (int i = 0; i < kLongPer; ++i) {

@@ -17,6 +17,8 @@
 // and the scan is a second one.  Measured: one sequence of 4 drafted tokens, 32000
 // probabilities, f32, 7.4 us (a launch and three dependent rounds of loads); 128 of
 // none to 7, 131071 probabilities, 108 MB, 25.5 us, 4.2 TB/s.
+#include <algorithm>
+
 #include "kcommon.h"
 #include "kv.h"
 
@@ -453,52 +455,58 @@ __device__ __forceinline__ VerifyRows tree_row(const TreeVerifyArgs& a, const Tr
   return w;
 }
 
-// The token and the outputs of one sequence, from the sums of its last row's regions in LDS.
-template <typename T, int THREADS>
-__device__ __forceinline__ void finish_tree(const TreeVerifyArgs& a, int s, const TreeWalk& r, const VerifyRows& w,
-                                            int regions, uint64_t* sums, const TreeShared& sh, int* out) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  if (tid < 64) {
-    // the refused tokens (each once) leave the sums, and the region that is looked at again
-    auto move = [&](bool back) {
-      for (int i = lane; i < r.refused; i += 64) {
-        const int k = sh.gone[i];
-        unsigned long long* at = reinterpret_cast<unsigned long long*>(sums + sh.token[k] / kRegion);
-        atomicAdd(at, back ? (unsigned long long)sh.w[k] : 0ull - (unsigned long long)sh.w[k]);
-      }
-      __builtin_amdgcn_wave_barrier();
-    };
-    move(false);
-    const float u = a.u_sample[s];
-    int tok = pick_from(u, regions, sums, [&](int region, float* f) {
-      region_rest<T, true>(w, region, a.vocab, f);
-      const int v = region * kRegion + lane * 8;
-      for (int i = 0; i < r.refused; ++i) {
-        const int d = sh.token[sh.gone[i]] - v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = j == d ? 0.f : f[j];
-      }
-    });
-    if (tok == -2) {   // nothing is left: the row as it is
-      move(true);
-      tok = pick_from(u, regions, sums, [&](int region, float* f) { region_rest<T, true>(w, region, a.vocab, f); });
-      if (tok == -2) tok = -1;
+// What the first of two launches leaves for the second, ahead of a sequence's sums: of the
+// refused tokens each once, with the weight it lost.
+struct Gone {
+  uint64_t w;
+  int64_t token;
+};
+struct TreeHead {
+  TreeWalk walk;
+  int32_t pad[3];
+  Gone gone[kTreeTokens];
+};
+static_assert(sizeof(TreeHead) % 16 == 0, "sums follow");
+
+// The token of one sequence, by one wave, from the sums of its last row's regions in LDS.
+template <typename T, typename G>
+__device__ __forceinline__ int tree_token(const TreeVerifyArgs& a, int s, const TreeWalk& r, const VerifyRows& w,
+                                          int regions, uint64_t* sums, G gone) {
+  const int lane = threadIdx.x & 63;
+  // the refused tokens leave the sums, and the region that is looked at again
+  auto move = [&](bool back) {
+    for (int i = lane; i < r.refused; i += 64) {
+      const Gone x = gone(i);
+      atomicAdd(reinterpret_cast<unsigned long long*>(sums + x.token / kRegion),
+                back ? (unsigned long long)x.w : 0ull - (unsigned long long)x.w);
     }
-    if (lane == 0) *out = tok;
-  }
-  __syncthreads();
-  const int tok = *out;
-  for (int i = tid; i < a.path_ld; i += THREADS) {
+    __builtin_amdgcn_wave_barrier();
+  };
+  move(false);
+  const float u = a.u_sample[s];
+  const int tok = pick_from(u, regions, sums, [&](int region, float* f) {
+    region_rest<T, true>(w, region, a.vocab, f);
+    const int v = region * kRegion + lane * 8;
+    for (int i = 0; i < r.refused; ++i) {
+      const int d = (int)gone(i).token - v;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j == d ? 0.f : f[j];
+    }
+  });
+  if (tok != -2) return tok;
+  move(true);   // nothing is left: the row as it is
+  const int plain = pick_from(u, regions, sums, [&](int region, float* f) { region_rest<T, true>(w, region, a.vocab, f); });
+  return plain == -2 ? -1 : plain;
+}
+// The path and its tokens, but for the new one.
+template <int THREADS>
+__device__ __forceinline__ void write_path(const TreeVerifyArgs& a, int s, const TreeWalk& r, const TreeShared& sh) {
+  for (int i = threadIdx.x; i < a.path_ld; i += THREADS) {
     const int64_t at = (int64_t)s * a.path_ld + i;
     a.path[at] = i < r.count ? sh.path[i] : -1;
-    a.tokens[at] = i + 1 < r.count ? sh.token[sh.path[i + 1]] : (i + 1 == r.count ? tok : -1);
+    if (i + 1 != r.count) a.tokens[at] = i + 1 < r.count ? sh.token[sh.path[i + 1]] : -1;
   }
-  if (tid == 0) a.n_out[s] = r.count;
-}
-template <int THREADS>
-__device__ __forceinline__ void idle_tree(const TreeVerifyArgs& a, int s) {
-  for (int i = threadIdx.x; i < a.path_ld; i += THREADS) a.tokens[(int64_t)s * a.path_ld + i] = a.path[(int64_t)s * a.path_ld + i] = -1;
-  if (threadIdx.x == 0) a.n_out[s] = 0;
+  if (threadIdx.x == 0) a.n_out[s] = r.count;
 }
 template <typename T>
 __device__ __forceinline__ void tree_sums(const TreeVerifyArgs& a, const VerifyRows& w, int first, int step, int regions,
@@ -512,46 +520,57 @@ template <typename T>
 __global__ __launch_bounds__(1024) void k_tree_one(TreeVerifyArgs a, int regions) {
   __shared__ uint64_t sums[kMaxRegions];
   __shared__ TreeShared sh;
-  __shared__ int out;
-  const int s = blockIdx.x;
+  const int s = blockIdx.x, tid = threadIdx.x;
   const TreeWalk r = walk_tree<T, 1024>(a, s, sh);
-  if (r.n == 0) return idle_tree<1024>(a, s);
-  const VerifyRows w = tree_row<T>(a, r);
-  tree_sums<T>(a, w, (int)threadIdx.x >> 6, 16, regions, sums);
-  __syncthreads();
-  finish_tree<T, 1024>(a, s, r, w, regions, sums, sh, &out);
-}
-template <typename T>
-__global__ __launch_bounds__(256) void k_tree_sums(TreeVerifyArgs a, uint64_t* __restrict__ ws, int regions) {
-  __shared__ TreeShared sh;
-  const int s = blockIdx.y;
-  const TreeWalk r = walk_tree<T, 256>(a, s, sh);
+  write_path<1024>(a, s, r, sh);
   if (r.n == 0) return;
   const VerifyRows w = tree_row<T>(a, r);
-  tree_sums<T>(a, w, blockIdx.x * 4 + ((int)threadIdx.x >> 6), gridDim.x * 4, regions, ws + (size_t)s * regions);
+  tree_sums<T>(a, w, tid >> 6, 16, regions, sums);
+  __syncthreads();
+  if (tid >= 64) return;
+  const int tok = tree_token<T>(a, s, r, w, regions, sums, [&](int i) { return Gone{sh.w[sh.gone[i]], sh.token[sh.gone[i]]}; });
+  if (tid == 0) a.tokens[(int64_t)s * a.path_ld + r.count - 1] = tok;
+}
+__host__ __device__ inline size_t tree_bytes(int regions) { return sizeof(TreeHead) + ((size_t)regions + 1) / 2 * 16; }
+template <typename T>
+__global__ __launch_bounds__(256) void k_tree_sums(TreeVerifyArgs a, int regions) {
+  __shared__ TreeShared sh;
+  const int s = blockIdx.y, tid = threadIdx.x;
+  TreeHead* head = reinterpret_cast<TreeHead*>(a.ws + s * tree_bytes(regions));
+  const TreeWalk r = walk_tree<T, 256>(a, s, sh);
+  if (blockIdx.x == 0) {
+    write_path<256>(a, s, r, sh);
+    if (tid == 0) head->walk = r;
+    for (int i = tid; i < r.refused; i += 256) head->gone[i] = Gone{sh.w[sh.gone[i]], sh.token[sh.gone[i]]};
+  }
+  if (r.n == 0) return;
+  const VerifyRows w = tree_row<T>(a, r);
+  tree_sums<T>(a, w, blockIdx.x * 4 + (tid >> 6), gridDim.x * 4, regions, reinterpret_cast<uint64_t*>(head + 1));
 }
 template <typename T>
-__global__ __launch_bounds__(512) void k_tree_pick(TreeVerifyArgs a, const uint64_t* __restrict__ ws, int regions) {
+__global__ __launch_bounds__(512) void k_tree_pick(TreeVerifyArgs a, int regions) {
   __shared__ uint64_t sums[kMaxRegions];
-  __shared__ TreeShared sh;
-  __shared__ int out;
   const int s = blockIdx.x, tid = threadIdx.x;
-  const TreeWalk r = walk_tree<T, 512>(a, s, sh);
-  if (r.n == 0) return idle_tree<512>(a, s);
-  if (tid < regions) sums[tid] = ws[(size_t)s * regions + tid];
+  const TreeHead* head = reinterpret_cast<const TreeHead*>(a.ws + s * tree_bytes(regions));
+  const TreeWalk r = head->walk;
+  if (tid < regions) sums[tid] = reinterpret_cast<const uint64_t*>(head + 1)[tid];
   __syncthreads();
-  finish_tree<T, 512>(a, s, r, tree_row<T>(a, r), regions, sums, sh, &out);
+  if (r.n == 0 || tid >= 64) return;
+  const int tok = tree_token<T>(a, s, r, tree_row<T>(a, r), regions, sums, [&](int i) { return head->gone[i]; });
+  if (tid == 0) a.tokens[(int64_t)s * a.path_ld + r.count - 1] = tok;
 }
+
+// As for chains.
+bool one_tree_launch(int32_t n_seqs, int32_t vocab) { return vocab <= 32768 || n_seqs >= 192; }
 
 template <typename T>
 hipError_t launch_tree(const TreeVerifyArgs& a, hipStream_t s) {
   const int regions = (a.vocab + kRegion - 1) / kRegion;
-  if (a.vocab <= 32768 || a.n_seqs >= 192) {
+  if (one_tree_launch(a.n_seqs, a.vocab)) {
     hipLaunchKernelGGL((k_tree_one<T>), dim3(a.n_seqs), dim3(1024), 0, s, a, regions);
   } else {
-    uint64_t* ws = reinterpret_cast<uint64_t*>(a.ws);
-    hipLaunchKernelGGL((k_tree_sums<T>), dim3((regions + 7) / 8, a.n_seqs), dim3(256), 0, s, a, ws, regions);
-    hipLaunchKernelGGL((k_tree_pick<T>), dim3(a.n_seqs), dim3(512), 0, s, a, ws, regions);
+    hipLaunchKernelGGL((k_tree_sums<T>), dim3((regions + 7) / 8, a.n_seqs), dim3(256), 0, s, a, regions);
+    hipLaunchKernelGGL((k_tree_pick<T>), dim3(a.n_seqs), dim3(512), 0, s, a, regions);
   }
   return hipGetLastError();
 }
@@ -559,7 +578,7 @@ hipError_t launch_tree(const TreeVerifyArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t tree_verify_workspace(int32_t n_seqs, int32_t vocab) {
-  return (size_t)n_seqs * ((vocab + kRegion - 1) / kRegion) * sizeof(uint64_t);
+  return one_tree_launch(n_seqs, vocab) ? 16 : std::max<size_t>(16, n_seqs * tree_bytes((vocab + kRegion - 1) / kRegion));
 }
 
 hipError_t launch_tree_verify(const TreeVerifyArgs& a, hipStream_t s) {
