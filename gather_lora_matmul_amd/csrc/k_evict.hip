@@ -133,8 +133,8 @@ __device__ __forceinline__ bool some_absent(const KvView& kv, int s, int n) {
 template <int THREADS, int BINS>
 struct SelectShared {
   uint32_t bins[BINS];
-  uint32_t key[THREADS];   // ranks that begin alike, where they are few, and their tokens
-  int index[THREADS];
+  alignas(16) uint32_t key[THREADS];   // ranks that begin alike, where they are few, and their tokens
+  alignas(16) int index[THREADS];
   int part[THREADS / 64], part2[THREADS / 64];
   uint32_t found[2];
   int last;
@@ -220,6 +220,7 @@ __device__ __forceinline__ Border border_of(SelectShared<THREADS, BINS>& sh, uin
     return Border{prefix, last};   // fewer than `need` lie before it
   }
   if (tid == 0) sh.fill = 0;
+  if (tid >= (int)count && tid < (int)((count + 3) & ~3u)) sh.key[tid] = 0;
   __syncthreads();
   each([&](uint32_t x, int j) {
     if (((uint64_t)x >> shift) == ((uint64_t)prefix >> shift)) {
@@ -233,8 +234,12 @@ __device__ __forceinline__ Border border_of(SelectShared<THREADS, BINS>& sh, uin
     const uint32_t x = sh.key[tid];
     const int j = sh.index[tid];
     uint32_t before = 0;
-#pragma unroll 4
-    for (uint32_t i = 0; i < count; ++i) before += sh.key[i] > x || (sh.key[i] == x && sh.index[i] < j);
+#pragma unroll 2
+    for (uint32_t i = 0; i < count; i += 4) {
+      const u32x4 y = *reinterpret_cast<const u32x4*>(sh.key + i), k = *reinterpret_cast<const u32x4*>(sh.index + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) before += y[e] > x || (y[e] == x && (int)k[e] < j);
+    }
     if (before == need - 1) {   // one thread
       sh.found[0] = x;
       sh.last = j;
@@ -273,164 +278,13 @@ __device__ __forceinline__ void emit(SelectShared<THREADS, BINS>& sh, const Bord
   }
 }
 
-// ---- caches of up to 2048 tokens: a wave for each ---------------------------------
-// The ranks of a (sequence, head) are in one wave's registers, so that nothing waits for
-// another wave but the look at the page ids, which the heads of a block share.
-constexpr int kWaveTokens = 2048, kWavePer = kWaveTokens / 64;
-
-struct WaveShared {
-  uint32_t bins[2048];
-  uint32_t key[64];
-  int index[64];
-};
-// (LDS is in order within a wave; the compiler has to be told)
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t z = __shfl_up(x, d);
-    x += lane >= d ? z : 0u;
-  }
-  return x;
-}
-__device__ __forceinline__ uint32_t wave_bin(const WaveShared& sh, uint32_t& need) {
-  const int lane = threadIdx.x & 63, low = 2048 - (lane + 1) * 32;
-  uint32_t own = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) own += sh.bins[low + ((i + lane) & 31)];   // (every lane another bank)
-  uint32_t sum = wave_scan(own);
-  const int src = __builtin_ctzll(__ballot(sum >= need));
-  const uint32_t before = __shfl(sum - own, src);
-  const int top = 2048 - src * 32 - 1;
-  const uint32_t v = lane < 32 ? sh.bins[top - lane] : 0u;
-  sum = before + wave_scan(v);
-  const int at = __builtin_ctzll(__ballot(sum >= need));
-  need -= __shfl(sum - v, at);
-  return (uint32_t)(top - at);
-}
-__global__ __launch_bounds__(256) void k_select_waves(SelectArgs a, const int32_t* __restrict__ counts) {
-  __shared__ WaveShared shared[4];
-  __shared__ int present[kKvMaxHeads];
-  const KvView& kv = a.kv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), s = blockIdx.y, h = (int)blockIdx.x * 4 + wave;
-  WaveShared& sh = shared[wave];
-  Ranks r = ranks_of(a, s, min(h, kv.H - 1));
-  const int n = uni(r.n), per = (n + 63) / 64;
-  r.n = n;
-  r.late = uni(r.late);
-  float w[kWavePer];
-  load_weights<kWavePer>(r, 0, per, w);
-  int least = n;   // tokens that the head with fewest has
-  for (int i = lane; i < 2048 / 4; i += 64) reinterpret_cast<u32x4*>(sh.bins)[i] = u32x4{0, 0, 0, 0};
-  if (!counts) {
-    const bool bad = some_absent<256>(kv, s, n);
-    if (__syncthreads_or(bad)) {
-      for (int o = wave; o < kv.H; o += 4) {
-        const int c = count_present(kv, ranks_of(a, s, o));
-        if (lane == 0) present[o] = c;
-      }
-      __syncthreads();
-      for (int o = lane; o < kv.H; o += 64) least = min(least, present[o]);
-      least = wave_min(least);
-      r.all = present[min(h, kv.H - 1)] == n;
-    }
-  } else {
-    for (int o = lane; o < kv.H; o += 64) least = min(least, counts[(int64_t)s * kv.H + o]);
-    least = wave_min(least);
-    r.all = counts[(int64_t)s * kv.H + min(h, kv.H - 1)] == n;
-  }
-  if (h >= kv.H) return;
-  const int K = min(a.budget, uni(least));
-  if (h == 0 && lane == 0) a.n_keep[s] = K;
-  if (K == 0) return;
-  int32_t* out = a.keep + ((int64_t)s * kv.H + h) * a.keep_ld;
-  if (K == n) {   // all of them
-    for (int j = lane; j < n; j += 64) out[j] = j;
-    return;
-  }
-  uint32_t x[kWavePer];
-  to_ranks<kWavePer>(kv, r, 0, per, w, x);
-  wave_sync();
-#pragma unroll
-  for (int i = 0; i < kWavePer; ++i)
-    if (i < per && x[i]) atomicAdd(&sh.bins[x[i] >> 21], 1u);
-  wave_sync();
-  uint32_t need = (uint32_t)K;
-  uint32_t prefix = wave_bin(sh, need), count = sh.bins[prefix];
-  int shift = 21;
-  prefix <<= 21;
-  while (uni((int)count) > 64 && shift > 0) {   // 11 bits more, the last ones together with a 0
-    const int next = max(shift - 11, 0), less = 11 - (shift - next);
-    wave_sync();
-    for (int i = lane; i < 2048 / 4; i += 64) reinterpret_cast<u32x4*>(sh.bins)[i] = u32x4{0, 0, 0, 0};
-    wave_sync();
-#pragma unroll
-    for (int i = 0; i < kWavePer; ++i)
-      if (i < per && x[i] && x[i] >> shift == prefix >> shift) atomicAdd(&sh.bins[(x[i] >> next << less) & 2047u], 1u);
-    wave_sync();
-    const uint32_t bin = wave_bin(sh, need);
-    count = sh.bins[bin];
-    prefix |= bin >> less << next;
-    shift = next;
-  }
-  Border b{prefix, 0};
-  if (uni((int)count) > 64) {   // equal ranks: the need-th token of them
-    uint32_t before = 0;
-#pragma unroll
-    for (int i = 0; i < kWavePer; ++i) {
-      const unsigned long long m = __ballot(x[i] == prefix);
-      const unsigned long long hit = __ballot(((m >> lane) & 1) && before + (uint32_t)lanes_below(m) == need - 1);
-      b.last = hit ? i * 64 + __builtin_ctzll(hit) : b.last;
-      before += (uint32_t)__popcll(m);
-    }
-  } else {
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kWavePer; ++i) {
-      if (i < per) {
-        const bool in = x[i] && x[i] >> shift == prefix >> shift;
-        const unsigned long long m = __ballot(in);
-        if (in) {
-          sh.key[at + lanes_below(m)] = x[i];
-          sh.index[at + lanes_below(m)] = i * 64 + lane;
-        }
-        at += __popcll(m);
-      }
-    }
-    wave_sync();
-    const uint32_t mine = lane < at ? sh.key[lane] : 0u;
-    const int j = lane < at ? sh.index[lane] : 0;
-    uint32_t before = 0;
-    for (int i = 0; i < at; ++i) {   // (they lie in their tokens' order)
-      const uint32_t y = (uint32_t)__builtin_amdgcn_readlane((int)mine, i);
-      before += y > mine || (y == mine && i < lane);
-    }
-    const unsigned long long hit = __ballot(lane < at && before == need - 1);
-    const int src = hit ? __builtin_ctzll(hit) : 0;
-    b.rank = (uint32_t)__builtin_amdgcn_readlane((int)mine, src);
-    b.last = __builtin_amdgcn_readlane(j, src);
-  }
-  int at = 0;
-#pragma unroll
-  for (int i = 0; i < kWavePer; ++i) {
-    if (i < per) {
-      const bool stay = x[i] && stays(b, x[i], i * 64 + lane);
-      const unsigned long long m = __ballot(stay);
-      const int place = at + lanes_below(m);
-      if (stay && place < K) out[place] = i * 64 + lane;
-      at += __popcll(m);
-    }
-  }
-}
-
 // ---- caches of up to a chunk: a block for each --------------------------------------
 // A block has a (sequence, head) with its ranks in registers: the 11 leading bits of all of
 // them in bins, then the few that share the border's bin compared one with another.  Bound by
-// its rounds through LDS (about a dozen barriers).
+// its rounds through LDS (about a dozen barriers): the fewest waves that hold the ranks wait
+// the least for one another.  2048 heads of up to 2048 tokens take 15.7 us with 256 threads
+// (with 128 17.8, 512 20.3, 1024 26; a wave by itself for each head 17.6), half of it for the weights and the
+// look for missing pages.
 template <int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t* __restrict__ counts) {
   constexpr int W = THREADS / 64, BINS = 2048;
@@ -969,7 +823,7 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
     counts = reinterpret_cast<int32_t*>(a.ws);
     hipLaunchKernelGGL(k_select_count, grid, dim3(64), 0, s, a, counts);
   }
-  if (most <= kWaveTokens) hipLaunchKernelGGL(k_select_waves, dim3((a.kv.H + 3) / 4, a.kv.n_seqs), dim3(256), 0, s, a, counts);
+  if (most <= 2048) hipLaunchKernelGGL((k_select<256, 8>), grid, dim3(256), 0, s, a, counts);
   else hipLaunchKernelGGL((k_select<1024, 8>), grid, dim3(1024), 0, s, a, counts);
   return hipGetLastError();
 }

@@ -16,12 +16,6 @@ namespace lora {
 
 namespace {
 
-#ifndef WR
-#define WR 2
-#define NB8 4
-#define MAXP 8
-#define ROWS 32
-#endif
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Tiles of KT cached tokens of a (sequence, head), in that order of sequences.
@@ -103,14 +97,20 @@ __device__ __forceinline__ float old_weight(const WeighArgs& a, const Unit& u, i
   return a.before && a.decay > 0.f && j < u.q.base ? a.decay * a.before[at + j] : 0.f;
 }
 
-// ---- up to 16 rows ---------------------------------------------------------------
+// ---- up to 32 rows a head and sequence ---------------------------------------------
 // A wave for itself: KT keys straight to registers, the rows in tiles of 16.  Bound by the
 // reads of K: a wave's units are neighbours, the next one's keys are on their way while it
-// works on one, its page ids while it loads one.
+// works on one, its page ids while it loads one.  64 sequences of 20 to 2048 tokens, 32 heads on
+// 32, in FP8 (268 MB of keys) take 74 us, 3.6 TB/s; with 48 keys in three waves a SIMD 75, with 32 in four 74.5.
+// A key's exponentials are 16 a row tile whether its rows are there or not, and every tile
+// of rows is read again for each unit: above 32 rows the tiles below are faster.  us of rows /
+// tiles: 16-bit 32 heads on 32, 17 rows over 500 tokens 5.0 / 11.9; 24 rows over 30000 20 / 30; 32 rows
+// over 5000 16 / 25; 48 rows, 4 sequences over 2500, 79 / 62; 64 rows 93 / 58, in FP8 57 / 48.
+constexpr int kFewRows = 32, kRowsBlocks = 2;   // rows; blocks a CU
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WR, WR))) void k_weigh_rows(WeighArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kRowsBlocks, kRowsBlocks))) void k_weigh_rows(WeighArgs a) {
   constexpr bool Q8 = is_quant<KV>();
-  constexpr int E = ET<KV>::E, NB = Q8 ? NB8 : 2, KT = 16 * NB, NC = D / (4 * E), NQ = D / 32;
+  constexpr int E = ET<KV>::E, NB = Q8 ? 4 : 2, KT = 16 * NB, NC = D / (4 * E), NQ = D / 32;
   __shared__ int pre[kKvMaxSeqs + 1];
   __shared__ KvSeq seqs[kKvMaxSeqs];
   const KvView& kv = a.kv;
@@ -259,7 +259,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WR, WR))) v
 
 // ---- more rows -------------------------------------------------------------------
 // A block's four waves have 64 keys each, in registers for all of the rows, which go
-// through LDS in tiles of 64 (two slots, one barrier a tile).
+// through LDS in steps of 128 (two slots, one barrier a step).  32 products of 32x32x16 and 32
+// exponentials of a wave cost about the same, so they are woven: the last 2048 of 16384
+// tokens, 64 heads on 8 in bf16, take 600 us, 860 TFLOP/s, at the 1.9 to 2.2 GHz that the
+// card holds under them.  (Products of one step, then its exponentials: 640.)
 // Rows in LDS, 64 of them in B blocks of 1 KB, each what one load brings: row r is number r / B
 // of block r % B, and a block begins 16 bytes further in the banks than the one before.  The
 // loads cover whole rows, a product's lanes read all banks alike, and all operands of a lane
@@ -277,11 +280,15 @@ struct WeighShared {
 constexpr int kKeys = 256, kRows = 128;   // keys of a block's tile, rows of a step
 
 // Few tiles are cut by rows, all of them into the same number of parts, which walk the rows
-// in step and find them in their L2; a second launch joins the parts' sums in their order.
+// in step and find them in their L2; a second launch joins the parts' sums in their order.  us
+// uncut / cut: 4096 tokens over 4096, 8 heads on 1, 741 / 170; 1000 over 30000, 216 / 124; 512 over 4096,
+// 64 heads on 8, 162 / 86; 2048 over 2048 in FP8 401 / 152; 4 sequences of 128 over 2000 66 / 49.  (Equal
+// shares of all rows, cut wherever they end, were slower where there are many tiles: 736 for
+// 599, their rows come from HBM instead of L2.)
 struct WeighTile {
   int32_t seq, head, tile, parts;   // (parts 1: the tile was not cut)
 };
-constexpr int kMaxParts = MAXP;
+constexpr int kMaxParts = 8;
 // Units (tiles times parts) of a call of which tiles are cut: at most four a block.
 inline __host__ __device__ int most_units(int G) { return 4 * G; }
 // The parts that make the fewest rounds of G blocks, in tiles' lengths.
@@ -529,8 +536,8 @@ hipError_t launch_tiles(const WeighArgs& a, hipStream_t s) {
 
 template <typename A, typename KV, int D>
 hipError_t launch(const WeighArgs& a, hipStream_t s) {
-  if ((int64_t)a.max_q_len * a.group <= ROWS)
-    hipLaunchKernelGGL((k_weigh_rows<A, KV, D>), dim3(WR * a.n_cu), dim3(256), 0, s, a);
+  if ((int64_t)a.max_q_len * a.group <= kFewRows)
+    hipLaunchKernelGGL((k_weigh_rows<A, KV, D>), dim3(kRowsBlocks * a.n_cu), dim3(256), 0, s, a);
   else
     return launch_tiles<A, KV, D>(a, s);
   return hipGetLastError();
