@@ -401,7 +401,7 @@ __device__ __forceinline__ int long_budget(const SelectArgs& a, int s, int h, in
 __global__ __launch_bounds__(kLongThreads) void k_select_bins(SelectArgs a, int chunks) {
   __shared__ uint32_t bins[kLongBins];
   __shared__ int part[kLongThreads / 64];
-  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, wave = tid >> 6;
+  const int h = blockIdx.x, ch = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, wave = tid >> 6;
   Ranks r = ranks_of(a, s, h);
   const int j0 = ch * kChunk;
   if (j0 >= r.n) return;
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(kLongThreads) void k_select_bins(SelectArgs a, int 
 __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int chunks) {
   __shared__ LongShared sh;
   __shared__ int counts[kLongThreads / 64 + 1];
-  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x, ch = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Ranks r = ranks_of(a, s, h);
   const int j0 = ch * kChunk;
   if (ch == 0 && h == 0 && r.n == 0 && tid == 0) a.n_keep[s] = 0;
@@ -449,13 +449,21 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
   // thread t adds up the bins 8 t .. 8 t + 7
   constexpr int PER = kLongBins / kLongThreads;
   static_assert(PER == 8, "16 bytes a thread");
+  constexpr int AHEAD = 8;
+  uint4 v[AHEAD];
+  auto bins_from = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = ld16(sp.bins + (int64_t)min(i0 + i, used - 1) * kLongBins + tid * PER);
+  };
+  bins_from(0);
+  const int K = long_budget(a, s, h, chunks, r, counts);
+  if (ch == 0 && h == 0 && tid == 0) a.n_keep[s] = K;
+  if (K == 0 || K == r.n) return;
   uint32_t sum[PER] = {}, earlier[PER] = {};   // of all chunks, of those before this one
-  for (int i0 = 0; i0 < used; i0 += 8) {
-    uint4 v[8];
+  for (int i0 = 0; i0 < used; i0 += AHEAD) {
+    if (i0 > 0) bins_from(i0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ld16(sp.bins + (int64_t)min(i0 + i, used - 1) * kLongBins + tid * PER);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       const uint32_t in = i0 + i < used ? 0xffffu : 0u, before = i0 + i < ch ? 0xffffu : 0u;
 #pragma unroll
@@ -468,9 +476,7 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j) sh.bins[tid * PER + j] = sum[j];
-  const int K = long_budget(a, s, h, chunks, r, counts);   // (a barrier in it)
-  if (ch == 0 && h == 0 && tid == 0) a.n_keep[s] = K;
-  if (K == 0 || K == r.n) return;
+  __syncthreads();
   uint32_t x[kLongPer];
   to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
   uint32_t need = (uint32_t)K;
@@ -516,12 +522,25 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
 __global__ __launch_bounds__(kLongThreads) void k_select_long(SelectArgs a, int chunks) {
   __shared__ LongShared sh;
   __shared__ int counts[kLongThreads / 64 + 1];
-  const int ch = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x, ch = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Ranks r = ranks_of(a, s, h);
   const int j0 = ch * kChunk;
   if (j0 >= r.n) return;
+  const LongSpace sp(a.ws, (int64_t)s * a.kv.H + h, chunks);
+  const int used = (r.n + kChunk - 1) / kChunk;
   float wt[kLongPer];
   load_weights<kLongPer>(r, j0 + wave * kLongPer * 64, kLongPer, wt);
+  constexpr int LISTED = kListed / kLongThreads;
+  uint2 listed[LISTED];   // (asked for ahead of how many there are)
+#pragma unroll
+  for (int i = 0; i < LISTED; ++i) listed[i] = sp.list[i * kLongThreads + tid];
+  int above = 0, in = 0, above_before = 0;
+  for (int i = lane; i < used; i += 64) {
+    const ChunkInfo c = sp.info[i];
+    above += c.above;
+    in += c.in;
+    if (i < ch) above_before += c.above;
+  }
   const int K = long_budget(a, s, h, chunks, r, counts);
   if (K == 0) return;
   int32_t* out = a.keep + ((int64_t)s * a.kv.H + h) * a.keep_ld;
@@ -531,15 +550,6 @@ __global__ __launch_bounds__(kLongThreads) void k_select_long(SelectArgs a, int 
   }
   uint32_t x[kLongPer];
   to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
-  const LongSpace sp(a.ws, (int64_t)s * a.kv.H + h, chunks);
-  const int used = (r.n + kChunk - 1) / kChunk;
-  int above = 0, in = 0, above_before = 0;
-  for (int i = lane; i < used; i += 64) {
-    const ChunkInfo c = sp.info[i];
-    above += c.above;
-    in += c.in;
-    if (i < ch) above_before += c.above;
-  }
   above = wave_sum(above);
   in = wave_sum(in);
   above_before = wave_sum(above_before);
@@ -558,10 +568,9 @@ __global__ __launch_bounds__(kLongThreads) void k_select_long(SelectArgs a, int 
   const uint32_t prefix = sp.list[0].x >> 20 << 20;
   if (in <= kListed) {
     with([&](auto f) {
-      for (int i = tid; i < in; i += kLongThreads) {
-        const uint2 v = sp.list[i];
-        f(v.x, (int)v.y);
-      }
+#pragma unroll
+      for (int i = 0; i < LISTED; ++i)
+        if (i * kLongThreads + tid < in) f(listed[i].x, (int)listed[i].y);
     }, prefix);
   } else {   // (ranks that are nearly all alike)
     with([&](auto f) {
@@ -811,7 +820,7 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
   const int64_t most = select_most(a.kv, a.w_ld);
   if (most > kChunk) {
     const int chunks = (int)((most + kChunk - 1) / kChunk);
-    const dim3 grid(chunks, a.kv.H, a.kv.n_seqs);
+    const dim3 grid(a.kv.H, chunks, a.kv.n_seqs);
     hipLaunchKernelGGL(k_select_bins, grid, dim3(kLongThreads), 0, s, a, chunks);
     hipLaunchKernelGGL(k_select_list, grid, dim3(kLongThreads), 0, s, a, chunks);
     hipLaunchKernelGGL(k_select_long, grid, dim3(kLongThreads), 0, s, a, chunks);
