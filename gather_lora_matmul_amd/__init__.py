@@ -693,7 +693,7 @@ class KvBatch:
     [n_seqs + 1], kv_len [n_seqs] and table [n_seqs][2][n_kv_heads][max_blocks],
     read by the calls that use it (kept alive here).  Their contents may change
     between calls; n_tokens and max_q_len are bounds.  two_terms: lora_kv_attend
-    takes the weights in two 16-bit terms in long work too."""
+    and lora_kv_attend_tree take the weights in two 16-bit terms in long work too."""
 
     def __init__(self, q_start, kv_len, table, n_tokens: int, max_q_len: int, two_terms: bool = False):
         import torch

@@ -578,18 +578,19 @@ typedef struct {
 /* Rows of a lora_kv_tree from the parents: every token sees itself and its
  * ancestors, with window > 0 those less than window above it.  seen [n_tokens]
  * [words] and depth [n_tokens] are written; tokens from 64 * words on get empty
- * rows and depth 0, rows that belong to no sequence are left.  The time grows with the
- * depth (a chain of 1024 tokens takes 43 us).  Stream-ordered,
- * no allocation.  n_seqs 0..1024, n_tokens 0..2^24. */
+ * rows and depth 0, rows that belong to no sequence are left.  Stream-ordered, no
+ * wait, no allocation.  n_seqs 0..1024, n_tokens 0..2^24. */
 lora_status lora_kv_tree_build(int32_t n_seqs, int32_t n_tokens, const int32_t* q_start_dev,
                                const int32_t* parent_dev, int32_t words, int32_t window,
                                uint64_t* seen_dev, int32_t* depth_dev, void* stream);
 /* lora_kv_attend for tokens of trees: a token of depth d sees the present tokens j <
  * kv_len - q_len that were cached before the new ones (if window > 0, those with j >
  * kv_len - q_len + d - window), and the new tokens that its row of seen has, in
- * any order, itself only if its bit is there.  A chain's rows give what
- * lora_kv_attend gives.  Depths below 0 count as 0.  Everything else, the
- * workspace and its size (lora_kv_attend_workspace_size) too, is as there. */
+ * any order, itself only if its bit is there.  Depths below 0 count as 0.  p goes in
+ * one 16-bit term (two_terms: in two) from 160 rows a head and sequence on average
+ * and 24 tiles a compute unit.  Everything else, the workspace and its size
+ * (lora_kv_attend_workspace_size) too, is as in lora_kv_attend, which a chain's rows
+ * agree with within both calls' roundings. */
 lora_status lora_kv_attend_tree(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                                 const lora_kv_tree* tree, const void* q_dev, int64_t q_ld,
                                 int32_t n_q_heads, float scale, int32_t window, void* out_dev,
@@ -627,15 +628,15 @@ lora_status lora_spec_verify_tree_workspace_size(int32_t n_seqs, int32_t vocab, 
 /* From token 0 on, the children of the token reached are tried in their order.  With
  * the weights w_v = floor(2^44 p_v) of its row (p clamped to [0, 1], NaN: 0), child c
  * with token id d is accepted if floor(L floor(2^31 u_c) / 2^31) < w_d, L being 2^44
- * less the weights of the ones refused before it (at least 0); a refused one's id loses its weight, so
- * that children of one id are refused with the first of them, as are ids outside [0,
- * vocab).  The walk goes on from an accepted child.  Where none is accepted (or
- * there are none, or path_ld is reached), the next token is drawn with the weights that are left: the
- * smallest v with w_0 + .. + w_v > floor(total floor(2^31 u_sample) / 2^31); if none
- * is left, with those of the row as it is; all 0: -1.  For rows that sum to 1 the
- * tokens given out are distributed as the target's, for drafted tokens that were
- * chosen without chance (the likeliest ones).  Whole-number sums: the result depends on no
- * order or split.  Stream-ordered, no wait, no allocation; workspace_dev 16-byte
+ * less the weights of the ones refused before it (at least 0); a refused one's id
+ * loses its weight, so that children of one id are refused with the first of them, as
+ * are ids outside [0, vocab).  The walk goes on from an accepted child.  Where none
+ * is accepted (or there are none, or path_ld is reached), the next token is drawn with
+ * the weights that are left: the smallest v with w_0 + .. + w_v > floor(total floor(2^31 u_sample) / 2^31);
+ * if none is left, with those of the row as it is; all 0: -1.  For rows that sum to 1
+ * the tokens given out are distributed as the target's, for drafted tokens that were
+ * chosen without chance (the likeliest ones).  Whole-number sums: the result depends
+ * on no order or split.  Stream-ordered, no wait, no allocation; workspace_dev 16-byte
  * aligned, no initial contents, not shared by calls that overlap. */
 lora_status lora_spec_verify_tree(const lora_tree_verify_desc* desc, void* workspace_dev, size_t ws_bytes,
                                   void* stream);
@@ -650,13 +651,15 @@ lora_status lora_spec_verify_tree(const lora_tree_verify_desc* desc, void* works
  *   weights_j = decay before_j + sum_i exp(scale q_i . k_j - lse_i)
  * over the rows i (new tokens and query heads of the kv head) that see j as in
  * lora_kv_attend, whose lse of the same q, scale and window is given
- * [n_tokens][n_q_heads].  New tokens and calls with before_dev == NULL have nothing from before (nor is before read for
- * decay 0); absent tokens get 0.  before has the layout of weights and may be weights itself.  Scores,
- * exponentials (of lse's own accuracy) and sums are fp32; keys that a row does not
- * see do not touch its terms, whatever they hold.  Entries from kv_len on are left.
- * Runs of one batch give the same bits.  decay in [0, 1].  LORA_E_UNSUPPORTED for calls
- * that could need 2^31 tiles of 32 tokens.  Stream-ordered, no wait, no allocation; workspace as
- * for lora_kv_attend (size 0: none is needed). */
+ * [n_tokens][n_q_heads].  decay in [0, 1].  before has the layout of weights and may be
+ * weights itself; new tokens and calls with before_dev == NULL have nothing from before
+ * (nor is before read for decay 0), absent tokens get 0.  Scores, exponentials (of lse's
+ * own accuracy) and sums are fp32; keys that a row does not see do not touch its terms,
+ * whatever they hold.  Entries from kv_len on are left.  Runs of one batch give the same
+ * bits.  LORA_E_UNSUPPORTED for calls that could need 2^31 tiles of 32 tokens.
+ * Stream-ordered, no wait, no allocation; workspace_dev: 256-byte aligned, at least
+ * lora_kv_weigh_workspace_size bytes (0: it may be NULL), no initial contents; calls that
+ * share one must not overlap. */
 lora_status lora_kv_weigh_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
                                          const lora_kv_batch* batch, int32_t n_q_heads, size_t* bytes);
 lora_status lora_kv_weigh(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
@@ -666,10 +669,12 @@ lora_status lora_kv_weigh(const lora_pool* pool, const lora_kv_desc* kv, const l
                           void* stream);
 /* The tokens of every sequence and kv head that stay: the first `sinks`, the last
  * `recent` (sinks + recent <= budget), then those of largest weight, of equal ones the
- * first (NaN: below all others); absent tokens and those from w_ld on are never among them.  n_keep [n_seqs] =
- * min(budget, the fewest present tokens of a head), keep [n_seqs][n_kv_heads][keep_ld]
- * (keep_ld >= budget): their positions, ascending; entries from n_keep on are left.
- * q_start and the batch's tokens play no part.  The same workspace rules as above. */
+ * first (NaN: below all others); absent tokens and those from w_ld on are never among
+ * them.  n_keep [n_seqs] = min(budget, the fewest present tokens of a head), keep [n_seqs]
+ * [n_kv_heads][keep_ld] (keep_ld >= budget): their positions, ascending; entries from
+ * n_keep on are left.  q_start and the batch's tokens play no part.  Stream-ordered, no
+ * wait, no allocation; workspace_dev as for lora_kv_weigh, of
+ * lora_kv_select_workspace_size bytes. */
 lora_status lora_kv_select_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
                                           const lora_kv_batch* batch, size_t* bytes);
 lora_status lora_kv_select(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
@@ -677,15 +682,15 @@ lora_status lora_kv_select(const lora_pool* pool, const lora_kv_desc* kv, const 
                            int32_t recent, int32_t* keep_dev, int64_t keep_ld, int32_t* n_keep_dev,
                            void* workspace_dev, size_t ws_bytes, void* stream);
 /* In every sequence and head, place first + i gets the token first + keep[i], i < n_keep
- * [n_seqs] (and < keep_ld): K, V, FP8 scales and, if weights_dev is not NULL, weights.  first is
- * 0, or with from_new the first new token's position (kv_len - q_len); keep [n_seqs]
- * [keep_heads][keep_ld], keep_heads 1 (one list for all heads, e.g. the path of
- * lora_spec_verify_tree) or n_kv_heads (lora_kv_select).  A list ascends strictly; of one that
- * does not it is undefined which tokens its places get.  Moves happen in place, so no page
- * may be shared by two places of the call.  A place keeps what it has where the number names no
- * cached token or one of the two has no page; nothing else is touched, the places behind
- * included.  kv_len is not changed: the caller's next one is first + n_keep.  Stream-ordered,
- * no wait, no allocation. */
+ * [n_seqs] (and < keep_ld): K, V, FP8 scales and, if weights_dev is not NULL, weights.
+ * first is 0, or with from_new the first new token's position (kv_len - q_len); keep
+ * [n_seqs][keep_heads][keep_ld], keep_heads 1 (one list for all heads, e.g. the path of
+ * lora_spec_verify_tree) or n_kv_heads (lora_kv_select).  A list ascends strictly; of one
+ * that does not it is undefined which tokens its places get.  Moves happen in place, so no
+ * page may be shared by two places of the call.  A place keeps what it has where the number
+ * names no cached token or one of the two has no page; nothing else is touched, the places
+ * behind included.  kv_len is not changed: the caller's next one is first + n_keep.
+ * Stream-ordered, no wait, no allocation. */
 lora_status lora_kv_compact(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                             const int32_t* keep_dev, int32_t keep_heads, int64_t keep_ld,
                             const int32_t* n_keep_dev, int32_t from_new, float* weights_dev,
