@@ -966,7 +966,12 @@ def _attend_args(cache: KvCache, batch: KvBatch, q, out, scale, window, lse, wor
 
 
 def _window(window) -> int:
-    return max(-1, min(int(window), 2 ** 31 - 1))
+    return _whole(window)
+
+
+def _whole(n) -> int:
+    """n, or the end of 32 bits that it lies beyond (below 0: -1)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
 
 
 def prepare_kv_attend(cache: KvCache, batch: KvBatch, q, out, scale: float, window: int = 0, lse=None,
@@ -1051,8 +1056,8 @@ def prepare_kv_select(cache: KvCache, batch: KvBatch, weights, budget: int, keep
                                                                   cache.desc.n_kv_heads))
     wp, wb = _ws(workspace)
     return PreparedCall(_lib.lora_kv_select,
-                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), wt, w_ld, int(budget),
-                         int(sinks), int(recent), _dev_ptr(keep), int(keep.shape[2]), _dev_ptr(n_keep), wp, wb),
+                        (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), wt, w_ld, _whole(budget),
+                         _whole(sinks), _whole(recent), _dev_ptr(keep), int(keep.shape[2]), _dev_ptr(n_keep), wp, wb),
                         "lora_kv_select", (cache, batch, weights, keep, n_keep, workspace))
 
 

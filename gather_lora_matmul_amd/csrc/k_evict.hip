@@ -643,7 +643,7 @@ __device__ __forceinline__ bool resolve(const CompactArgs& a, const Places& p, i
     const int src = k >= 0 && k < p.end - p.first ? p.first + k : -1;
     const bool move = src >= 0 && src != pos && pos >= 0;
     moves |= move;
-    st.w[x] = move && src < a.w_ld ? src : -1;
+    st.w[x] = move && src < a.w_ld && pos < a.w_ld ? src : -1;   // (of lists that do not ascend src may be below)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const int64_t f = src >= 0 ? token_at<E, D>(a.kv, p, which, src) : kNone;

@@ -347,8 +347,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if (Q8) f[c] *= __uint_as_float((uint32_t)kv.scales[(int64_t)pg * kv.T + sl] << 23);
     }
     // of the sequence's rows those of tokens [t0, t1) see something of the block's keys
-    const int t0 = max(u.tile - q.base, 0);
-    const int t1 = a.window > 0 ? min(q.q_len, u.tile + KT - 1 + a.window - q.base) : q.q_len;
+    // (none of either where positions lie far from the keys: both stay within the sequence)
+    const int t0 = min(max(u.tile - q.base, 0), q.q_len);
+    const int t1 = a.window > 0 ? max(min(q.q_len, u.tile + KT - 1 + a.window - q.base), 0) : q.q_len;
     int r0 = t0 * a.group, r1 = t1 * a.group;
     if (cut > 1) {   // the part's steps of them
       const int steps = max(r1 - r0 + RT - 1, 0) / RT;

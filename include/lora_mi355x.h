@@ -688,8 +688,9 @@ lora_status lora_kv_select(const lora_pool* pool, const lora_kv_desc* kv, const 
  * lora_spec_verify_tree) or n_kv_heads (lora_kv_select).  A list ascends strictly; of one
  * that does not it is undefined which tokens its places get.  Moves happen in place, so no
  * page may be shared by two places of the call.  A place keeps what it has where the number
- * names no cached token or one of the two has no page; nothing else is touched, the places
- * behind included.  kv_len is not changed: the caller's next one is first + n_keep.
+ * names no cached token, its K (V) also where one of the two has no page for it, its weight
+ * where one of the two is not below w_ld; nothing else is touched, the places behind
+ * included.  kv_len is not changed: the caller's next one is first + n_keep.
  * Stream-ordered, no wait, no allocation. */
 lora_status lora_kv_compact(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                             const int32_t* keep_dev, int32_t keep_heads, int64_t keep_ld,

@@ -214,6 +214,31 @@ def test_a_wrong_longest_length_changes_the_rounding_only(max_q):
         assert torch.allclose(a, b, rtol=480 * 2.0 ** -23 + 2.0 ** -18, atol=0)
 
 
+@pytest.mark.parametrize("kv,G", [("bf16", 6), ("fp8", 6), ("bf16", 64), ("bf16", 1)])
+def test_weights_of_lengths_and_rows_far_from_each_other(kv, G):
+    # positions past the table and rows before the first token: rows that see nothing leave what was before
+    with Case("bf16", kv, 4096, 2, 128, [70, 9], [300, 130], seed=89, extra_blocks=0) as c:
+        c.fill()
+        q = queries(c, 2 * G)
+        lse = torch.zeros((c.n, 2 * G), device="cuda")
+        cap = c.table_host.shape[3] * c.T
+        for lens, starts, window, had in ((2 ** 31 - 1, None, 20, True), (2 ** 30, None, 2 ** 28, True),
+                                          (100, [0, 2 ** 31 - 1, 2 ** 31 - 1], 0, False),
+                                          (100, [0, 2 ** 31 - 1, 2 ** 31 - 1], 5, False), (-5, None, 7, None)):
+            log("[case] weigh far %s G %d kv_len %d starts %s window %d" % (kv, G, lens, starts, window))
+            c.kvl.fill_(lens)
+            c.q_start.copy_(torch.tensor([0, 70, 79] if starts is None else starts, dtype=torch.int32))
+            before = torch.rand((2, 2, cap + 4), device="cuda", generator=c.gen)
+            weights = torch.full_like(before, 7.0)
+            weigh(c, q, lse, weights, 0.1, window, 0.5, before)
+            torch.cuda.synchronize()
+            end = min(max(lens, 0), cap)
+            first = (weights[0], before[0])
+            assert (weights[:, :, end:] == 7.0).all()
+            if had is not None:
+                assert torch.equal(first[0][:, :end], first[1][:, :end] * 0.5 if had else torch.zeros_like(first[1][:, :end]))
+
+
 # ---------------------------------------------------------------------------------------------
 # selection
 # ---------------------------------------------------------------------------------------------
@@ -316,6 +341,15 @@ def test_selection_of_absent_and_unweighed_tokens():
         for bad in ([100000, 2 ** 31 - 1, -1, -2 ** 31],):
             c.kvl.copy_(torch.tensor(bad, dtype=torch.int32))
             check_selection(c, some_weights(c, 500, 8, "random"), 60, 3, 9, lens=bad)
+
+
+def test_counts_past_32_bits_are_refused():
+    with empty_case(1, [20], seed=90) as c:
+        w = torch.rand((1, 1, 20), device="cuda")
+        for kw in (dict(budget=2 ** 32 + 5), dict(budget=8, sinks=2 ** 32), dict(budget=8, recent=2 ** 32 + 1),
+                   dict(budget=8, sinks=2 ** 31 - 1, recent=2 ** 31 - 1), dict(budget=-2 ** 32 + 8)):
+            with pytest.raises(Exception, match="budget|keep_ld"):
+                select(c, w, ld=11, **kw)
 
 
 def test_many_heads_and_sequences():
@@ -442,6 +476,28 @@ def test_numbers_and_pages_that_are_not_there():
                 check_moves(c, keep, [12, 7, 2 ** 31 - 1, -4], from_new=from_new)
                 c.kvl.copy_(torch.tensor([4, 2 ** 31 - 1, 0, 5], dtype=torch.int32))   # fewer tokens than rows; past the table
                 check_moves(c, keep, [12, 12, 12, 12], from_new=from_new)
+
+
+def test_lists_that_do_not_ascend_stay_within_the_weights():
+    # which tokens the places get is open; nothing behind the rows of weights or in pages of others is touched
+    for most in (12, 200):
+        with Case("bf16", "bf16", 4096, 2, 128, [0, 0], [260, 90], seed=99) as c:
+            c.fill()
+            n = 7
+            flat = torch.rand((2 * 2 * n + 500,), device="cuda", generator=c.gen)
+            mark = flat.clone()
+            weights = flat[:2 * 2 * n].view(2, 2, n)
+            keep = np.zeros((2, 2, most), np.int64)
+            keep[:, :, ::2] = 5
+            keep[:, 1] = np.arange(most)[::-1]
+            pages = c.pages.clone()
+            used = set(int(x) for x in c.table_host.ravel())
+            L.lora_kv_compact(c.cache, c.batch(), i32(keep), i32([most, most]), weights=weights)
+            torch.cuda.synchronize()
+            assert torch.equal(flat[2 * 2 * n:], mark[2 * 2 * n:])
+            assert all(torch.isin(weights[s, h], mark[:2 * 2 * n].view(2, 2, n)[s, h]).all() for s in (0, 1) for h in (0, 1))
+            others = [p for p in range(c.n_pages) if p not in used]
+            assert torch.equal(c.pages[others], pages[others])
 
 
 # ---------------------------------------------------------------------------------------------
