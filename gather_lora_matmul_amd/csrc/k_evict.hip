@@ -282,9 +282,9 @@ __device__ __forceinline__ void emit(SelectShared<THREADS, BINS>& sh, const Bord
 // A block has a (sequence, head) with its ranks in registers: the 11 leading bits of all of
 // them in bins, then the few that share the border's bin compared one with another.  Bound by
 // its rounds through LDS (about a dozen barriers): the fewest waves that hold the ranks wait
-// the least for one another.  2048 heads of up to 2048 tokens take 15.7 us with 256 threads
-// (with 128 17.8, 512 20.3, 1024 26; a wave by itself for each head 17.6), half of it for the
-// weights and the look for missing pages.
+// the least for one another.  2048 heads of up to 2048 tokens take 15.1 us with 256 threads
+// (with 128 17.8, 512 20.3, 1024 26; a wave by itself for each head 17.6; ranks that wait for
+// the page ids 15.7), half of it for the weights and the look for missing pages.
 template <int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t* __restrict__ counts) {
   constexpr int W = THREADS / 64, BINS = 2048;
@@ -298,10 +298,24 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
   r.late = uni(r.late);
   int least = n;   // tokens that the head with fewest has
   uint32_t x[PER];
-  if (!counts) {
-    load_ranks<PER>(kv, r, first, per, x);
-    const bool bad = some_absent<THREADS>(kv, s, n);
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i < per && x[i]) f(x[i], first + i * 64 + lane);
+  };
+  auto clear = [&] {
     for (int i = tid; i < BINS; i += THREADS) sh.bins[i] = 0;
+    __syncthreads();
+  };
+  auto to_bins = [&] { each([&](uint32_t y, int) { atomicAdd(&sh.bins[y >> 21], 1u); }); };
+  float w[PER];
+  load_weights<PER>(r, first, per, w);
+  if (!counts) {
+    // the ranks go to their bins as if all pages were there, while the ids are on their way
+    const bool bad = some_absent<THREADS>(kv, s, n);
+    clear();
+    to_ranks<PER>(kv, r, first, per, w, x);
+    if (n > a.budget) to_bins();
     if (__syncthreads_or(bad)) {
       for (int o = wave; o < kv.H; o += W) {
         const int c = count_present(kv, ranks_of(a, s, o));
@@ -311,15 +325,12 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
       for (int o = lane; o < kv.H; o += 64) least = min(least, present[o]);
       least = wave_min(least);
       r.all = present[h] == n;
-      if (!r.all) load_ranks<PER>(kv, r, first, per, x);
     }
   } else {
     for (int o = lane; o < kv.H; o += 64) least = min(least, counts[(int64_t)s * kv.H + o]);
     least = wave_min(least);
     r.all = counts[(int64_t)s * kv.H + h] == n;
-    load_ranks<PER>(kv, r, first, per, x);
-    for (int i = tid; i < BINS; i += THREADS) sh.bins[i] = 0;
-    __syncthreads();
+    to_ranks<PER>(kv, r, first, per, w, x);
   }
   const int K = min(a.budget, uni(least));
   if (h == 0 && tid == 0) a.n_keep[s] = K;
@@ -329,13 +340,13 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
     for (int j = tid; j < n; j += THREADS) out[j] = j;
     return;
   }
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i < per && x[i]) f(x[i], first + i * 64 + lane);
-  };
-  each([&](uint32_t y, int) { atomicAdd(&sh.bins[y >> 21], 1u); });
-  __syncthreads();
+  if (counts || !r.all || n <= a.budget) {   // there are no bins yet, or not of these ranks
+    if (!r.all) to_ranks<PER>(kv, r, first, per, w, x);
+    __syncthreads();
+    clear();
+    to_bins();
+    __syncthreads();
+  }
   uint32_t need = (uint32_t)K;
   const uint32_t bin = find_bin<BINS>(sh, need), count = sh.bins[bin];
   const Border b = border_of(sh, bin << 21, 21, need, count, each);
