@@ -273,34 +273,130 @@ struct WeighShared {
   static constexpr int RT = 128, SLOT = RT / 64 * HALF;
   __align__(16) char q[2 * SLOT];
   float lse[4][RT];        // of the tile before, this one and the two after
-  int pre[kKvMaxSeqs + 1];
+  int pre[kKvMaxSeqs + 1];   // units of the sequences before
+  int slot[kKvMaxSeqs];      // of the first sums of a sequence whose tiles are cut
   static __device__ __forceinline__ int row_at(int r) { return r % B * STEP + r / B * (16 * P); }
 };
 
 constexpr int kKeys = 256, kRows = 128;   // keys of a block's tile, rows of a step
 
-// Few tiles are cut by rows, all of them into the same number of parts, which walk the rows
-// in step and find them in their L2; a second launch joins the parts' sums in their order.  us
-// uncut / cut: 4096 tokens over 4096, 8 heads on 1, 741 / 170; 1000 over 30000, 216 / 124; 512 over 4096,
-// 64 heads on 8, 162 / 86; 2048 over 2048 in FP8 401 / 152; 4 sequences of 128 over 2000 66 / 49.  (Equal
-// shares of all rows, cut wherever they end, were slower where there are many tiles: 736 for
-// 599, their rows come from HBM instead of L2.)
+// A unit is a tile, or where a call's tiles are few or differ a part of its rows; the parts'
+// sums are joined by a second launch in their order.  Units are ordered by sequence, head, part
+// and tile, so that neighbours read the same rows, and an eighth of the work (not of
+// the units) goes to each XCD, whose blocks take its units in turn and find their rows in
+// its L2.
+// us with whole tiles, in equal numbers / so: 4096 tokens over 4096, 8 heads on 1, 741 / 78; 1000 over
+// 30000 216 / 105; 512 over 4096, 64 heads on 8, 162 / 68; 2048 over 2048 in FP8 401 / 101; 2 x 2048 over 5000
+// 427 / 335; one of 2048 over 4096 among 63 of 1 over 2000 1187 / 348; 32 sequences of 1 to 1024 over 1024 to 4096 1025 / 865, 64 of 1 to 512, 32 heads on 32, 472 / 394.
+// (One more part for each block: 10 of 1 to 1672 over 1672 198 / 190, but 2 x 2048 over 5000 335 / 359. Equal shares
+// of all rows, cut wherever they end, were slower: the last 2048 of 16384 736 for 600, with rows
+// from HBM instead of L2.)
 struct WeighTile {
-  int32_t seq, head, tile, parts;   // (parts 1: the tile was not cut)
+  int32_t seq, head, tile;
+  int32_t parts;   // 0: not the first part of its tile
 };
-constexpr int kMaxParts = 8;
-// Units (tiles times parts) of a call of which tiles are cut: at most four a block.
-inline __host__ __device__ int most_units(int G) { return 4 * G; }
-// The parts that make the fewest rounds of G blocks, in tiles' lengths.
-__device__ __forceinline__ int parts_of(int tiles, int G) {
-  int best = 1;
-  for (int p = 2; p <= kMaxParts && tiles * p <= most_units(G); ++p)
-    if ((int64_t)((tiles * p + G - 1) / G) * best < (int64_t)((tiles * best + G - 1) / G) * p) best = p;
-  return best;
+struct WeighCut {
+  int32_t slots;   // sums that the second launch finds
+  int32_t pad[63];
+};
+constexpr int kCuts = 2, kMaxParts = 32;
+inline __host__ __device__ int most_slots(int G) { return 4 * kCuts * G; }
+struct Plan {
+  int x0, x1;    // units of the block's XCD
+  int quantum;   // steps of a part
+};
+// Steps of rows that a tile of the sequence has at most.
+__device__ __forceinline__ int steps_of(const WeighArgs& a, const KvSeq& q) {
+  const int tokens = a.window > 0 ? min(q.q_len, a.window + kKeys) : q.q_len;
+  return (tokens * a.group + kRows - 1) / kRows;
+}
+__device__ __forceinline__ int parts_of(int steps, int quantum) { return min((steps + quantum - 1) / quantum, kMaxParts); }
+
+// Sums over a wave's lanes up to each.
+template <typename T>
+__device__ __forceinline__ T lanes_up_to(T x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const T z = __shfl_up(x, d);
+    x += lane >= d ? z : 0;
+  }
+  return x;
+}
+// The block's part of the call, by each of its waves.  A unit's work is its steps and two more
+// for its keys.  A cut tile has more steps than the quantum, and all tiles' steps are twice the work
+// at most, 2 kCuts G quanta: so cut tiles are 2 kCuts G and their parts 4 kCuts G at most.
+template <class S>
+__device__ __forceinline__ Plan plan_work(const WeighArgs& a, S& sh, WeighCut* cut) {
+  using I64 = long long;
+  const int n = a.kv.n_seqs, lane = threadIdx.x & 63, G = (int)gridDim.x, xcd = (int)blockIdx.x & 7;
+  struct Work {
+    int tiles, steps;
+    I64 all;   // in half steps; a tile of new tokens has half of the steps, about
+  };
+  auto of = [&](int s) {
+    if (s >= n) return Work{0, 0, 0};
+    const KvSeq q = kv_seq(a.kv, s);
+    const int tiles = (tokens_of(a, q) + kKeys - 1) / kKeys, steps = steps_of(a, q);
+    return Work{tiles * a.kv.H, steps, a.kv.H * ((I64)(2 * tiles - min(q.q_len / kKeys, tiles)) * steps + 4 * tiles)};
+  };
+  const Work mine = of(lane);
+  I64 total = mine.all;
+  int whole = mine.tiles, longest = mine.tiles ? mine.steps + 2 : 0;
+  for (int s = lane + 64; s < n; s += 64) {
+    const Work w = of(s);
+    total += w.all;
+    whole += w.tiles;
+    longest = max(longest, w.tiles ? w.steps + 2 : 0);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    total += __shfl_xor(total, d);
+    whole += __shfl_xor(whole, d);
+    longest = max(longest, __shfl_xor(longest, d));
+  }
+  Plan p;
+  // (whole tiles where their rounds are within a tenth of the work)
+  p.quantum = cut && (I64)((whole + G - 1) / G) * longest > total / 2 / G * 11 / 10
+                  ? (int)min(max((total / 2 + kCuts * G) / (kCuts * G), (I64)4), (I64)1 << 30)
+                  : 1 << 30;
+  const I64 v[2] = {total * xcd / 8, total * (xcd + 1) / 8};
+  int bound[2] = {0, 0}, units = 0, slots = 0;
+  I64 before = 0;
+  for (int s0 = 0; s0 < n; s0 += 64) {
+    const int s = s0 + lane;
+    const Work w = s0 ? of(s) : mine;
+    const int parts = max(parts_of(w.steps, p.quantum), 1), own = w.tiles * parts, in_slots = parts > 1 ? own : 0;
+    const int u = lanes_up_to(own), t = lanes_up_to(in_slots);
+    const I64 c = lanes_up_to(w.all);
+    if (s < n) {   // (every wave writes the same)
+      sh.pre[s] = units + u - own;
+      sh.slot[s] = slots + t - in_slots;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const I64 in = v[i] - (before + c - w.all);
+      const unsigned long long hit = __ballot(in >= 0 && in < w.all);
+      const int at = units + u - own + min((int)((double)in / (double)w.all * (double)own), own);
+      if (hit) bound[i] = __builtin_amdgcn_readlane(at, __builtin_ctzll(hit));
+    }
+    units += __builtin_amdgcn_readlane(u, 63);
+    slots += __builtin_amdgcn_readlane(t, 63);
+    before += __shfl(c, 63);
+  }
+  if (threadIdx.x == 0) {
+    sh.pre[n] = units;
+    if (cut && blockIdx.x == 0) cut->slots = slots;
+  }
+  __syncthreads();
+  p.quantum = uni(p.quantum);
+  p.x0 = uni(bound[0]);
+  p.x1 = uni(xcd == 7 ? units : bound[1]);
+  return p;
 }
 
 template <typename A, typename KV, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_weigh_tiles(WeighArgs a, WeighTile* tiles) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_weigh_tiles(WeighArgs a, WeighCut* cut) {
   constexpr bool Q8 = is_quant<KV>();
   using S = WeighShared<D>;
   constexpr int KT = kKeys, NQ = D / 16, RT = S::RT, P = S::P, B = S::B;
@@ -308,16 +404,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   extern __shared__ __align__(16) char smem[];
   S& sh = *reinterpret_cast<S*>(smem);
   const KvView& kv = a.kv;
-  const int all = tile_sums<KT, 256>(a, sh.pre);
+  const Plan plan = plan_work(a, sh, cut);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, hi = lane >> 5;
-  const int cut = tiles && all <= most_units((int)gridDim.x) ? parts_of(all, (int)gridDim.x) : 1, units = all * cut;
-  float* const sums = reinterpret_cast<float*>(tiles + most_units((int)gridDim.x));   // [tile][part][KT]
-  if (tiles && all == 0 && blockIdx.x == 0 && tid == 0) tiles[0].parts = 1;
-  // an eighth of the units to each XCD: the tiles of one head, which read the same rows, share its L2
-  const int per = (units + 7) / 8, x0 = min(((int)blockIdx.x & 7) * per, units), x1 = min(x0 + per, units);
-  for (int un = x0 + ((int)blockIdx.x >> 3); un < x1; un += (int)gridDim.x >> 3) {
-    const int part_no = un / all, tile_no = un - part_no * all;
-    const Unit u = unit_of<KT>(a, sh.pre, tile_no);
+  WeighTile* const tiles = reinterpret_cast<WeighTile*>(cut + 1);   // of each slot
+  float* const sums = reinterpret_cast<float*>(tiles + most_slots((int)gridDim.x));
+  for (int un = plan.x0 + ((int)blockIdx.x >> 3); un < plan.x1; un += (int)gridDim.x >> 3) {
+    Unit u;
+    u.seq = uni(seq_of(sh.pre, kv.n_seqs, un));
+    unit_seq(a, u, nullptr);
+    const int n_tiles = (u.n + KT - 1) / KT, parts = max(parts_of(steps_of(a, u.q), plan.quantum), 1);
+    const int rem = un - uni(sh.pre[u.seq]);
+    u.head = rem / (parts * n_tiles);
+    const int part_no = (rem - u.head * parts * n_tiles) / n_tiles, tile_no = rem - (u.head * parts + part_no) * n_tiles;
+    u.tile = tile_no * KT;
     const KvSeq& q = u.q;
     const int32_t* ktab = kv.table + ((int64_t)u.seq * 2 * kv.H + u.head) * kv.nb;
     const int32_t* vtab = ktab + (int64_t)kv.H * kv.nb;
@@ -351,10 +450,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int t0 = min(max(u.tile - q.base, 0), q.q_len);
     const int t1 = a.window > 0 ? max(min(q.q_len, u.tile + KT - 1 + a.window - q.base), 0) : q.q_len;
     int r0 = t0 * a.group, r1 = t1 * a.group;
-    if (cut > 1) {   // the part's steps of them
+    if (parts > 1) {   // the part's steps of them
       const int steps = max(r1 - r0 + RT - 1, 0) / RT;
-      r1 = min(r1, r0 + steps * (part_no + 1) / cut * RT);
-      r0 += steps * part_no / cut * RT;
+      r1 = min(r1, r0 + steps * (part_no + 1) / parts * RT);
+      r0 += steps * part_no / parts * RT;
     }
     // rows rt .. rt + RT - 1 to a slot, their lse to LDS.  A lane finds the place of a row of
     // each 64, the loads take it from the lanes that have theirs
@@ -483,33 +582,38 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int j = k0 + lane;
     const int64_t at = ((int64_t)u.seq * kv.H + u.head) * a.w_ld;
     const float got = hi ? sum[1] : sum[0];
-    if (cut > 1) sums[((int64_t)tile_no * cut + part_no) * KT + wave * 64 + lane] = got;
-    else if (j < u.n) a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + got : 0.f;
-    if (tiles && part_no == 0 && tid == 0 && tile_no < most_units((int)gridDim.x))
-      tiles[tile_no] = WeighTile{u.seq, u.head, u.tile, cut};
+    if (parts > 1) {
+      const int slot = uni(sh.slot[u.seq]) + (u.head * n_tiles + tile_no) * parts + part_no;
+      sums[(int64_t)slot * KT + wave * 64 + lane] = got;
+      if (tid == 0) tiles[slot] = WeighTile{u.seq, u.head, u.tile, part_no ? 0 : parts};
+    } else if (j < u.n) {
+      a.weights[at + j] = (hi ? there[1] : there[0]) ? old_weight(a, u, at, j) + got : 0.f;
+    }
   }
 }
 
 // The parts of a tile together, a thread a key.
-__global__ __launch_bounds__(kKeys) void k_weigh_join(WeighArgs a, const WeighTile* __restrict__ tiles, int G) {
-  if (tiles[0].parts == 1) return;   // none is cut
-  __shared__ int pre[kKvMaxSeqs + 1];
-  if ((int)blockIdx.x >= tile_sums<kKeys, kKeys>(a, pre)) return;
+__global__ __launch_bounds__(kKeys) void k_weigh_join(WeighArgs a, const WeighCut* __restrict__ cut, int G) {
   const KvView& kv = a.kv;
-  const WeighTile d = tiles[blockIdx.x];
-  const float* sums = reinterpret_cast<const float*>(tiles + most_units(G)) + (int64_t)blockIdx.x * d.parts * kKeys + threadIdx.x;
-  float sum = 0.f;
-  for (int p = 0; p < d.parts; ++p) sum += sums[p * kKeys];
-  Unit u;
-  u.seq = d.seq;
-  unit_seq(a, u, nullptr);
-  const int j = d.tile + (int)threadIdx.x;
-  if (j >= u.n) return;
-  const int blk = (int)kv_div(kv, (uint32_t)j);
-  const int32_t* ktab = kv.table + ((int64_t)d.seq * 2 * kv.H + d.head) * kv.nb;
-  const bool there = (unsigned)ktab[blk] < (unsigned)kv.n_pages && (unsigned)ktab[(int64_t)kv.H * kv.nb + blk] < (unsigned)kv.n_pages;
-  const int64_t at = ((int64_t)d.seq * kv.H + d.head) * a.w_ld;
-  a.weights[at + j] = there ? old_weight(a, u, at, j) + sum : 0.f;
+  const WeighTile* tiles = reinterpret_cast<const WeighTile*>(cut + 1);
+  const float* sums = reinterpret_cast<const float*>(tiles + most_slots(G)) + threadIdx.x;
+  const int slots = cut->slots;
+  for (int i = blockIdx.x; i < slots; i += gridDim.x) {
+    const WeighTile d = tiles[i];
+    if (d.parts == 0) continue;
+    float sum = 0.f;
+    for (int p = 0; p < d.parts; ++p) sum += sums[(int64_t)(i + p) * kKeys];
+    Unit u;
+    u.seq = d.seq;
+    unit_seq(a, u, nullptr);
+    const int j = d.tile + (int)threadIdx.x;
+    if (j >= u.n) continue;
+    const int blk = (int)kv_div(kv, (uint32_t)j);
+    const int32_t* ktab = kv.table + ((int64_t)d.seq * 2 * kv.H + d.head) * kv.nb;
+    const bool there = (unsigned)ktab[blk] < (unsigned)kv.n_pages && (unsigned)ktab[(int64_t)kv.H * kv.nb + blk] < (unsigned)kv.n_pages;
+    const int64_t at = ((int64_t)d.seq * kv.H + d.head) * a.w_ld;
+    a.weights[at + j] = there ? old_weight(a, u, at, j) + sum : 0.f;
+  }
 }
 
 // Tiles may be cut where a head has more rows than four steps take.
@@ -529,9 +633,9 @@ hipError_t launch_tiles(const WeighArgs& a, hipStream_t s) {
     });
   if (e != hipSuccess) return e;
   const int G = blocks_of(a.n_cu);
-  WeighTile* tiles = may_cut(a.group, a.max_q_len) ? reinterpret_cast<WeighTile*>(a.ws) : nullptr;
-  hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a, tiles);
-  if (tiles) hipLaunchKernelGGL(k_weigh_join, dim3(2 * G), dim3(kKeys), 0, s, a, tiles, G);
+  WeighCut* cut = may_cut(a.group, a.max_q_len) ? reinterpret_cast<WeighCut*>(a.ws) : nullptr;
+  hipLaunchKernelGGL((k_weigh_tiles<A, KV, D>), dim3(G), dim3(256), lds, s, a, cut);
+  if (cut) hipLaunchKernelGGL(k_weigh_join, dim3(2 * G), dim3(kKeys), 0, s, a, cut, G);
   return hipGetLastError();
 }
 
@@ -551,7 +655,8 @@ hipError_t launch_d(const KvTypes& ty, const WeighArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t weigh_workspace(int32_t n_cu, int32_t group, int32_t max_q_len) {
-  return may_cut(group, max_q_len) ? (size_t)most_units(blocks_of(n_cu)) * (sizeof(WeighTile) + kKeys * sizeof(float)) : 0;
+  if (!may_cut(group, max_q_len)) return 0;
+  return sizeof(WeighCut) + (size_t)most_slots(blocks_of(n_cu)) * (sizeof(WeighTile) + kKeys * sizeof(float));
 }
 
 int64_t weigh_units(const KvView& v) { return (int64_t)v.n_seqs * v.H * ((int64_t)v.nb * v.T / 32 + 1); }

@@ -201,6 +201,27 @@ def test_many_rows_and_long_sums():
         check_weights(c, queries(c, 2), 0.125, 250, 0.5)
 
 
+@pytest.mark.parametrize("act,kv,G", [("bf16", "bf16", 8), ("f16", "fp8", 5)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_long_rows_among_many_short_ones(act, kv, G, window):
+    # tiles cut into several parts, into two, and not at all; sequences of nothing; more of them than a wave has lanes
+    rng = np.random.default_rng(G)
+    q_len, kv_len = [1] * 150, [int(x) for x in rng.integers(1, 60, 150)]
+    for s, (a, m) in {0: (0, 0), 3: (300, 700), 63: (0, 300), 64: (90, 500), 70: (2, 5), 100: (130, 130), 149: (250, 251)}.items():
+        q_len[s], kv_len[s] = a, m
+    with Case(act, kv, 2048, 1, 64, q_len, kv_len, seed=88) as c:
+        c.fill()
+        check_weights(c, queries(c, G), 0.11, window, 0.9)
+
+
+def test_one_long_sequence_in_parts_on_few_tiles():
+    # 32 parts of one tile, and a batch whose blocks all get whole tiles
+    for H, G, q_len, kv_len in ((1, 8, [600], [200 + 600]), (1, 16, [520, 1], [520, 9]), (8, 6, [90] * 9, [90] * 9)):
+        with Case("bf16", "bf16", 4096, H, 128, q_len, kv_len, seed=91) as c:
+            c.fill()
+            check_weights(c, queries(c, H * G), 0.08, 0, 1.0)
+
+
 @pytest.mark.parametrize("max_q", [0, 1, 60])
 def test_a_wrong_longest_length_changes_the_rounding_only(max_q):
     with Case("bf16", "bf16", 4096, 1, 128, [60, 3], [200, 90], seed=87) as c:
