@@ -620,13 +620,10 @@ __device__ __forceinline__ Places places_of(const CompactArgs& a, int s, int h) 
   p.tab = kv.table + ((int64_t)s * 2 * kv.H + h) * kv.nb;
   return p;
 }
-// Bytes of a token's K (which 0) or V rows in the pool's pages: of K its 16 bytes of piece
+// Bytes of the K (which 0) or V of a token in page `page` of the pool: of K its 16 bytes of piece
 // 0, of V its element 0.  kNone: it has no page.
 template <int E, int D>
-__device__ __forceinline__ int64_t token_at(const KvView& kv, const Places& p, int which, int pos) {
-  if (pos < 0 || pos >= p.end) return kNone;
-  const int b = (int)kv_div(kv, (uint32_t)pos), slot = pos - b * kv.T;
-  const int page = p.tab[(which ? (int64_t)kv.H * kv.nb : 0) + b];
+__device__ __forceinline__ int64_t token_at(const KvView& kv, int which, int slot, int page) {
   if ((unsigned)page >= (unsigned)kv.n_pages) return kNone;
   return (int64_t)page * kv.page_bytes + (which ? slot / E * (D * 16) + slot % E * (16 / E) : slot * 16);
 }
@@ -645,25 +642,45 @@ struct Steps {
   int64_t from[2][N], to[2][N];   // of K and V; from kNone: the place keeps what it has
   int32_t w[N];                   // position that the weight comes from, -1: none
 };
-template <int E, int D, int N, int THREADS>
-__device__ __forceinline__ bool resolve(const CompactArgs& a, const Places& p, int pos0, Steps<N>& st) {
-  bool moves = false;
-  for (int x = threadIdx.x; x < N; x += THREADS) {
-    const int pos = pos0 + x, i = pos - p.first;
-    const int k = i >= 0 && i < p.n ? p.keep[i] : -1;
-    const int src = k >= 0 && k < p.end - p.first ? p.first + k : -1;
-    const bool move = src >= 0 && src != pos && pos >= 0;
-    moves |= move;
-    st.w[x] = move && src < a.w_ld && pos < a.w_ld ? src : -1;   // (of lists that do not ascend src may be below)
+// One place of the list on its way: the token's number, then the page ids of both, then what
+// the block's waves go by.
+__device__ __forceinline__ int number_of(const Places& p, int pos) {
+  const int i = pos - p.first, k = p.keep[max(min(i, p.n - 1), 0)];   // (p.n is at least 1)
+  return i >= 0 && i < p.n ? k : -1;
+}
+struct Entry {
+  int src, pos;   // from which position to which; src -1: none
+  int from[2], to[2];   // page ids
+};
+__device__ __forceinline__ Entry entry_of(const KvView& kv, const Places& p, int pos, int k) {
+  Entry e;
+  e.src = k >= 0 && k < p.end - p.first ? p.first + k : -1;
+  e.src = e.src >= 0 && pos >= 0 && pos < p.end ? e.src : -1;
+  e.pos = pos;
+  const int a = (int)kv_div(kv, (uint32_t)max(e.src, 0)), b = (int)kv_div(kv, (uint32_t)(e.src >= 0 ? pos : 0));
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const int64_t f = src >= 0 ? token_at<E, D>(a.kv, p, which, src) : kNone;
-      const int64_t t = src >= 0 ? token_at<E, D>(a.kv, p, which, pos) : kNone;
-      st.from[which][x] = t == kNone ? kNone : f;
-      st.to[which][x] = t;
-    }
+  for (int which = 0; which < 2; ++which) {
+    const int32_t* tab = p.tab + (which ? (int64_t)kv.H * kv.nb : 0);
+    e.from[which] = tab[a];
+    e.to[which] = tab[b];
   }
-  return __syncthreads_or(moves) != 0;
+  return e;
+}
+// Returns whether something moves.
+template <int E, int D, int N>
+__device__ __forceinline__ bool put(const CompactArgs& a, const Entry& e, int x, Steps<N>& st) {
+  const KvView& kv = a.kv;
+  const bool move = e.src >= 0 && e.src != e.pos;
+  st.w[x] = move && e.src < a.w_ld && e.pos < a.w_ld ? e.src : -1;   // (of lists that do not ascend src may be below)
+  const int fs = e.src - (int)kv_div(kv, (uint32_t)max(e.src, 0)) * kv.T, ts = e.pos - (int)kv_div(kv, (uint32_t)max(e.pos, 0)) * kv.T;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int64_t f = token_at<E, D>(kv, which, fs, e.from[which]), t = token_at<E, D>(kv, which, ts, e.to[which]);
+    const bool ok = e.src >= 0 && t != kNone;
+    st.from[which][x] = ok ? f : kNone;
+    st.to[which][x] = ok ? t : kNone;
+  }
+  return move;
 }
 
 // E tokens' values of an element of V, gathered and in their places: what is in registers
@@ -718,7 +735,10 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   const Places p = places_of(a, s, h);
   const int pos0 = max(p.first, 0) / E * E;
-  if (p.n <= 0 || !resolve<E, D, N, 256>(a, p, pos0, st)) return;
+  if (p.n <= 0) return;
+  bool moves = false;
+  if (tid < N) moves = put<E, D>(a, entry_of(kv, p, pos0 + tid, number_of(p, pos0 + tid)), tid, st);
+  if (!__syncthreads_or(moves)) return;
   const int x = tid & 63;
   u32x4 k[KU];
   Gathered<E> v[VU > 0 ? VU : 1];
@@ -751,21 +771,34 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
 // Lists of any length.  A wave owns a column (a 16-byte piece of K, 8 elements of V, the
 // scale bytes or the weights) of one (sequence, head) and goes through the list in order: what
 // it reads for a step lies at or behind what this step writes, and before that only earlier
-// steps have written.  The block's waves share the look-up of 512 places.  Bound by HBM's
-// lines: 16 sequences of 4001 to 16000 tokens, 8 heads in bf16, down to 2048 with their weights
-// take 153 us (places looked up by each wave 675, by the block 327, 8 elements of V a wave
-// instead of 64 222, reads that wait for no condition 153).
+// steps have written.  The block's waves share the look-up of 256 places, whose numbers and page
+// ids are on their way one step ahead.  Bound by HBM's lines: 16 sequences of 4001 to 16000
+// tokens, 8 heads in bf16, down to 2048 with their weights take 153 us (places looked up by
+// each wave 675, by the block 327, 8 elements of V a wave instead of 64 222, reads that wait
+// for no condition 153); where heads are few by the steps, 3 us each: 30000 tokens of 8 heads to
+// 4096 63 us (looked up when their step comes, 512 at a time, 72), of one head to 15000 177 (203).
+// Tokens read a step ahead of their writes too made these 67 and 199: one loop for all kinds of
+// columns waits for all that is on its way.
 template <int E, int D>
 __global__ __launch_bounds__(256) void k_compact(CompactArgs a, int columns) {
-  constexpr int N = 512, KC = D / E, VC = D / 8, U = 4, UV = 16 / E;
-  __shared__ Steps<N> st;
+  constexpr int N = 256, KC = D / E, VC = D / 8, U = 4, UV = 16 / E;
+  __shared__ Steps<N> steps[2];
   const KvView& kv = a.kv;
   const int lane = threadIdx.x & 63, c = blockIdx.x * 4 + uni((int)threadIdx.x >> 6), h = blockIdx.y, s = blockIdx.z;
   const Places p = places_of(a, s, h);
   float* weights = a.weights ? a.weights + ((int64_t)s * kv.H + h) * a.w_ld : nullptr;
-  const int end = p.first + p.n;
-  for (int pos0 = max(p.first, 0) / E * E; pos0 < end; pos0 += N) {
-    if (resolve<E, D, N, 256>(a, p, pos0, st)) {
+  if (p.n <= 0) return;
+  const int end = p.first + p.n, tid = threadIdx.x;
+  // while a step's tokens move, the next one's page ids and the numbers of the one behind are on their way
+  int pos0 = max(p.first, 0) / E * E;
+  Entry entry = entry_of(kv, p, pos0 + tid, number_of(p, pos0 + tid));
+  int number = number_of(p, pos0 + N + tid);
+  for (int i = 0; pos0 < end; pos0 += N, i ^= 1) {
+    Steps<N>& st = steps[i];
+    const bool moves = put<E, D>(a, entry, tid, st);
+    entry = entry_of(kv, p, pos0 + N + tid, number);
+    number = number_of(p, pos0 + 2 * N + tid);
+    if (__syncthreads_or(moves)) {   // (the other half of `steps` has been read by all when a wave writes there)
       const int n = min(N, end - pos0);
       if (c < KC) {
         const int64_t column = (int64_t)c * kv.T * 16;
@@ -807,7 +840,6 @@ __global__ __launch_bounds__(256) void k_compact(CompactArgs a, int columns) {
         }
       }
     }
-    __syncthreads();   // the step's places have been read
   }
 }
 
