@@ -269,7 +269,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kRowsBlocks
 // are at constant distances from one address.
 template <int D>
 struct WeighShared {
-  static constexpr int P = D / 8, B = P, STEP = 1024 + 16, HALF = B * STEP;   // (64 rows of P pieces in 1 KB blocks: B = P)
+  // (64 rows of P pieces in 1 KB blocks: B = P)
+  static constexpr int P = D / 8, B = P, STEP = 1024 + 16, HALF = B * STEP;
   static constexpr int RT = 128, SLOT = RT / 64 * HALF;
   __align__(16) char q[2 * SLOT];
   float lse[4][RT];        // of the tile before, this one and the two after
@@ -282,15 +283,15 @@ constexpr int kKeys = 256, kRows = 128;   // keys of a block's tile, rows of a s
 
 // A unit is a tile, or where a call's tiles are few or differ a part of its rows; the parts'
 // sums are joined by a second launch in their order.  Units are ordered by sequence, head, part
-// and tile, so that neighbours read the same rows, and an eighth of the work (not of
-// the units) goes to each XCD, whose blocks take its units in turn and find their rows in
-// its L2.
-// us with whole tiles, in equal numbers / so: 4096 tokens over 4096, 8 heads on 1, 741 / 78; 1000 over
-// 30000 216 / 105; 512 over 4096, 64 heads on 8, 162 / 68; 2048 over 2048 in FP8 401 / 101; 2 x 2048 over 5000
-// 427 / 335; one of 2048 over 4096 among 63 of 1 over 2000 1187 / 348; 32 sequences of 1 to 1024 over 1024 to 4096 1025 / 865, 64 of 1 to 512, 32 heads on 32, 472 / 394.
-// (One more part for each block: 10 of 1 to 1672 over 1672 198 / 190, but 2 x 2048 over 5000 335 / 359. Equal shares
-// of all rows, cut wherever they end, were slower: the last 2048 of 16384 736 for 600, with rows
-// from HBM instead of L2.)
+// and tile, so that neighbours read the same rows, and an eighth of the work (not of the
+// units) goes to each XCD, whose blocks take its units in turn and find their rows in its
+// L2.  us with whole tiles, in equal numbers / so: 4096 tokens over 4096, 8 heads on 1, 741 / 78;
+// 1000 over 30000 216 / 105; 512 over 4096, 64 heads on 8, 162 / 68; 2048 over 2048 in FP8 401 /
+// 101; 2 x 2048 over 5000 427 / 335; one of 2048 over 4096 among 63 of 1 over 2000 1187 / 348; 32
+// sequences of 1 to 1024 over 1024 to 4096 1025 / 865; 64 of 1 to 512, 32 heads on 32, 472 / 394.
+// (One more part for each block: 10 of 1 to 1672 over 1672 198 / 190, but 2 x 2048 over 5000
+// 335 / 359.  Equal shares of all rows, cut wherever they end, were slower: the last 2048 of
+// 16384 736 for 600, with rows from HBM instead of L2.)
 struct WeighTile {
   int32_t seq, head, tile;
   int32_t parts;   // 0: not the first part of its tile
