@@ -167,6 +167,10 @@ struct PartDesc {        // a tile whose last of several parts a block has
 // their own tree (TreeArgs): each is a kernel of its own.
 template <class AA>
 constexpr bool is_tree = std::is_same<AA, TreeArgs>::value;
+// A piece as the loop over its tiles has it: of trees a copy.  (The compiler would leave a piece
+// that their masks refer to in scratch memory, whose reads wait for the keys on their way.)
+template <class AA>
+using Held = typename std::conditional<is_tree<AA>, Piece, Piece&>::type;
 
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
 // row's window, down to a multiple of KU, to the last row's own position or the
@@ -812,10 +816,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const Parts<TR, D> parts(a.ws, workers);
   PartDesc* desc = parts.desc + (SOLO ? (int)blockIdx.x * 4 + wave : (int)blockIdx.x);
   const bool speaker = SOLO ? lane == 0 : tid == 0;
-  Piece p;
+  Piece piece;
   int n_piece = 0;
   if (c.pos >= c.end && speaker) describe(desc, c, nullptr);
-  while (next_piece<KU, TR>(a, pre, c, p)) {
+  while (next_piece<KU, TR>(a, pre, c, piece)) {
+    const Held<AA> p = piece;
     // ---- queries: operand B of the first product, column = row of the tile
     const int row = p.row0 + min(col, p.rows - 1);
     const int tq = token_of(a, row);
@@ -1083,7 +1088,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (g == 0) parts.ml[at] = float2{m, l};
         }
       }
-      if (n_piece == 0 && speaker) describe(desc, c, &p);
+      if (n_piece == 0 && speaker) describe(desc, c, &piece);
       ++n_piece;
       continue;
     }
@@ -1126,7 +1131,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (d == 0) parts.ml[at] = float2{M, sum};
       }
     }
-    if (n_piece == 0 && speaker) describe(desc, c, &p);
+    if (n_piece == 0 && speaker) describe(desc, c, &piece);
     ++n_piece;
     __syncthreads();
   }
@@ -1271,7 +1276,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   Cut c;
   cut_work<KU, TR, NW * 64>(a, sh.pre, c, (int)gridDim.x, (int)blockIdx.x >> 3, sh.preT);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
-  Piece p;
+  Piece piece;
   int n_piece = 0;
   auto tell = [&](const Piece* q) {
     PartDesc* d = parts.desc + blockIdx.x;
@@ -1291,7 +1296,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   // those of tokens hi * 8 .. + 7 and 16 + hi * 8 .. + 7
   const int ktok = (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
   const float sl = DOWN ? a.scale_log2 * 2.f : a.scale_log2;
-  while (next_piece<KU, TR>(a, sh.pre, c, p, sh.preT)) {
+  while (next_piece<KU, TR>(a, sh.pre, c, piece, sh.preT)) {
+    const Held<AA> p = piece;
     const int wrow0 = p.row0 + wave * 32;
     const int wrows = min(32, p.rows - wave * 32);   // <= 0: no rows of its own
     const int base = p.q.base;
@@ -1729,7 +1735,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
       }
     }
     if (p.first >= 0) {
-      if (n_piece == 0 && tid == 0) tell(&p);
+      if (n_piece == 0 && tid == 0) tell(&piece);
       ++n_piece;
     }
     __syncthreads();  // the slots of this piece have been read
