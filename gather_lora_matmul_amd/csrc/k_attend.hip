@@ -1770,17 +1770,18 @@ inline bool solo_waves(int32_t n_seqs, int32_t H, int n_cu) { return (int64_t)n_
 // 255 / 198, 1000 over 30000 of 8 on 1 205 / 151; and below the line 4 x 128 over 2000 81 /
 // 72, 512 over 512 50 / 57, 1000 over 1000 of 32 on 32 54 / 55, 4096 over 4096 of 8 on 1 119 /
 // 131, 32 x 5 over 4096 115 / 117 (112 / 130), 16 x 300 over 300 of 32 on 32 69 / 80.
-// Trees, whose rows are few and whose keys are many, from 160 rows: 32 x n tokens over 2500, n =
-// 16 120 / 128, 20 164 / 142, 24 178 / 153, 32 197 / 168 (206 / 172), 40 230 / 192, 48 275 / 246;
-// 2 x 32 over 30000 147 / 124.
+// Trees, whose rows are few beside their keys, from 80 rows and seven units a block: 32 x n
+// tokens over 2500, n = 6 81 / 84, 8 84 / 84 (95 / 98), 10 90 / 86, 12 92 / 87 (101 / 100), 16 102 / 89
+// (108 / 103), 20 128 / 97, 32 152 / 118 (167 / 120), 48 232 / 179; 32 x 20 over 500 38 / 32; 8 x 64 over
+// 1000 54 / 47; 4 x 16 over 8000 62 / 59; 32 heads on 8, 32 x 20 over 2000, f16, 78 / 72.
 template <class AA>
-constexpr int wide_rows() { return is_tree<AA> ? 160 : 512; }
-inline bool wide_tiles(const AttendArgs& a, int blocks, int least) {
+inline bool wide_tiles(const AA& a, int blocks) {
   const int64_t rows = (int64_t)a.kv.n_tokens * a.group;
-  if (a.two_terms || rows < least * (int64_t)a.kv.n_seqs) return false;
+  if (a.two_terms || rows < (is_tree<AA> ? 80 : 512) * (int64_t)a.kv.n_seqs) return false;
   int64_t keys = (int64_t)a.kv.nb * a.kv.T - a.max_q_len / 2;
   if (a.window > 0) keys = std::min<int64_t>(keys, a.window);
-  return rows / 256 * a.kv.H * (keys / 64) >= 24 * (int64_t)blocks;
+  const int64_t tiles = is_tree<AA> ? std::max<int64_t>(rows / 256, a.kv.n_seqs) : rows / 256;
+  return tiles * a.kv.H * (keys / 64) >= (is_tree<AA> ? 7 : 24) * (int64_t)blocks;
 }
 
 template <typename A, typename KV, int D, int NW, class AA>
@@ -1798,8 +1799,8 @@ hipError_t launch_tiles(const AA& a, int G, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_attend_tiles<A, KV, D, NW, AA>), dim3(G), dim3(NW * 64), lds, s, a);
   // tiles of which none has many parts: four blocks each, of trees, most of whose tiles
-  // are cut, 16 (32 x 17 to 64 tokens over 900 to 4100, 64 heads on 8: 4 blocks 230 us, 8 223, 16
-  // 223, 32 224; 32 x 2 over 2500 115 with 4, 110 with 16); else the list.  Measured
+  // are cut, 16 (32 x 17 to 64 tokens over 900 to 4100, 64 heads on 8: 209 us with 4 blocks, 205
+  // with 16; 8 and 32 are within a us of 16); else the list.  Measured
   // (us of a call, list / this): 32 sequences of 5 x 8 rows over 2500 tokens 78.4 / 76.1,
   // 2 of 256 x 8 rows over 4096 130 / 126, 64 x 4 rows of 8 heads over 2000 33.6 / 83.6,
   // 100 x 8 rows of one head over 30000 49.5 / 123
@@ -1829,7 +1830,7 @@ hipError_t launch(const AA& a, hipStream_t s) {
   } else {
     // FP8 of 64 elements has too few loads in a tile for eight waves
     constexpr bool wide = D / ET<KV>::E % 8 == 0;
-    if (wide && wide_tiles(a, G / 16 * 8, wide_rows<AA>()))
+    if (wide && wide_tiles(a, G / 16 * 8))
       return launch_tiles<A, KV, D, wide ? 8 : 4, AA>(a, G / 16 * 8, s);
     return launch_tiles<A, KV, D, 4, AA>(a, G, s);
   }

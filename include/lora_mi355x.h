@@ -587,8 +587,8 @@ lora_status lora_kv_tree_build(int32_t n_seqs, int32_t n_tokens, const int32_t* 
  * kv_len - q_len that were cached before the new ones (if window > 0, those with j >
  * kv_len - q_len + d - window), and the new tokens that its row of seen has, in
  * any order, itself only if its bit is there.  Depths below 0 count as 0.  p goes in
- * one 16-bit term (two_terms: in two) from 160 rows a head and sequence on average
- * and 24 tiles a compute unit.  Everything else, the workspace and its size
+ * one 16-bit term (two_terms: in two) from 80 rows a head and sequence on average and
+ * seven tiles a compute unit.  Everything else, the workspace and its size
  * (lora_kv_attend_workspace_size) too, is as in lora_kv_attend, which a chain's rows
  * agree with within both calls' roundings. */
 lora_status lora_kv_attend_tree(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
