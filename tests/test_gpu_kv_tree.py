@@ -190,6 +190,25 @@ def test_attention_of_wide_tiles(act, kv, H, G, q_len, kv_len, window):
         check(c, queries(c, H * G), trees_for(c, 5, 2, window), 0.09, window, wide=True)
 
 
+@pytest.mark.parametrize("act,kv", [("f16", "f16"), ("bf16", "bf16"), ("f16", "fp8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("H,G,q_len,kv_len", [(1, 8, [9, 14, 10, 30, 2], [20, 300, 10, 64, 700]), (2, 5, [20, 17, 16], [400, 17, 90])])
+def test_attention_of_wide_tiles_with_few_rows(act, kv, H, G, q_len, kv_len):
+    log("[case] tree attention, wide, few rows, %s/%s %s" % (act, kv, q_len))
+    with wide_case(act, kv, 4096, 128, H, G, q_len, kv_len, seed=74) as c:
+        c.fill()
+        check(c, queries(c, H * G), trees_for(c, 15, 1), 0.09, wide=True)
+
+
+@pytest.mark.parametrize("act,kv", [("bf16", "bf16"), ("f16", "fp8")])
+def test_attention_of_wide_tiles_in_a_window(act, kv):
+    S, rng = 100, np.random.default_rng(16)
+    kv_len = [int(x) for x in rng.integers(12, 500, S)]
+    log("[case] tree attention, wide, window, %s/%s" % (act, kv))
+    with Case(act, kv, 4096, 8, 128, [12] * S, kv_len, seed=75, extra_blocks=0) as c:
+        c.fill()
+        check(c, queries(c, 64), trees_for(c, 17, 1, 192), 0.09, 192, wide=True, rows=[0, 5, 11])
+
+
 @pytest.mark.parametrize("G,n", [(1, 7), (8, 30)])
 def test_rows_of_any_bits(G, n):
     # not trees: rows that see nothing, not themselves, later tokens, tokens that the sequence has not
