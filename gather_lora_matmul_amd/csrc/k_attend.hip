@@ -167,10 +167,6 @@ struct PartDesc {        // a tile whose last of several parts a block has
 // their own tree (TreeArgs): each is a kernel of its own.
 template <class AA>
 constexpr bool is_tree = std::is_same<AA, TreeArgs>::value;
-// A piece as the loop over its tiles has it: of trees a copy.  (The compiler would leave a piece
-// that their masks refer to in scratch memory, whose reads wait for the keys on their way.)
-template <class AA>
-using Held = typename std::conditional<is_tree<AA>, Piece, Piece&>::type;
 
 // Keys that the rows [row0, row0 + rows) of a sequence visit: from the first
 // row's window, down to a multiple of KU, to the last row's own position or the
@@ -816,15 +812,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const Parts<TR, D> parts(a.ws, workers);
   PartDesc* desc = parts.desc + (SOLO ? (int)blockIdx.x * 4 + wave : (int)blockIdx.x);
   const bool speaker = SOLO ? lane == 0 : tid == 0;
-  Piece piece;
+  Piece p;
   int n_piece = 0;
   if (c.pos >= c.end && speaker) describe(desc, c, nullptr);
-  while (next_piece<KU, TR>(a, pre, c, piece)) {
-    const Held<AA> p = piece;
+  while (next_piece<KU, TR>(a, pre, c, p)) {
     // ---- queries: operand B of the first product, column = row of the tile
     const int row = p.row0 + min(col, p.rows - 1);
     const int tq = token_of(a, row);
     const int pos = p.q.base + tq;
+    const KvSeq sq = p.q;   // (as in k_attend_tiles)
     // (rows of a tree: all see the token before the new ones, and none is past the last new one)
     const int posmin = is_tree<AA> ? p.q.base - 1 : p.q.base + token_of(a, p.row0);
     const int posmax = is_tree<AA> ? p.q.base + p.q.q_len - 1 : p.q.base + token_of(a, p.row0 + p.rows - 1);
@@ -919,7 +915,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         // values that are not finite go to the rows that see them, then they leave V
         uint32_t live;
         if constexpr (is_tree<AA>) {
-          seen = gone ? 0u : tree_sees_few<E>(a, p.q, tq, k0);
+          seen = gone ? 0u : tree_sees_few<E>(a, sq, tq, k0);
           live = seen;
 #pragma unroll
           for (int x = 1; x < 16; x <<= 1) live |= (uint32_t)__shfl_xor((int)live, x);
@@ -1060,8 +1056,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if (__builtin_expect(__ballot(mine) != 0, 0)) {
         const auto dim = [&](int bit) { return (bit >> 2) * 16 + 4 * g + (bit & 3); };
         if constexpr (is_tree<AA>)
-          settle<A, D>(kv, ktab, vtab, max(tree_from(a, p.q, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
-                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, p.q, tq, t); });
+          settle<A, D>(kv, ktab, vtab, max(tree_from(a, sq, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, sq, tq, t); });
         else
           settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
                        min(posmin, p.key1 - 1), mine, o, dim, [](int) { return 0xffu; });
@@ -1088,7 +1084,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (g == 0) parts.ml[at] = float2{m, l};
         }
       }
-      if (n_piece == 0 && speaker) describe(desc, c, &piece);
+      if (n_piece == 0 && speaker) describe(desc, c, &p);
       ++n_piece;
       continue;
     }
@@ -1131,7 +1127,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (d == 0) parts.ml[at] = float2{M, sum};
       }
     }
-    if (n_piece == 0 && speaker) describe(desc, c, &piece);
+    if (n_piece == 0 && speaker) describe(desc, c, &p);
     ++n_piece;
     __syncthreads();
   }
@@ -1276,7 +1272,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   Cut c;
   cut_work<KU, TR, NW * 64>(a, sh.pre, c, (int)gridDim.x, (int)blockIdx.x >> 3, sh.preT);
   const Parts<TR, D> parts(a.ws, (int)gridDim.x);
-  Piece piece;
+  Piece p;
   int n_piece = 0;
   auto tell = [&](const Piece* q) {
     PartDesc* d = parts.desc + blockIdx.x;
@@ -1296,14 +1292,16 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
   // those of tokens hi * 8 .. + 7 and 16 + hi * 8 .. + 7
   const int ktok = (col >> 4) * 16 + ((col >> 2) & 1) * 8 + ((col >> 3) & 1) * 4 + (col & 3);
   const float sl = DOWN ? a.scale_log2 * 2.f : a.scale_log2;
-  while (next_piece<KU, TR>(a, sh.pre, c, piece, sh.preT)) {
-    const Held<AA> p = piece;
+  while (next_piece<KU, TR>(a, sh.pre, c, p, sh.preT)) {
     const int wrow0 = p.row0 + wave * 32;
     const int wrows = min(32, p.rows - wave * 32);   // <= 0: no rows of its own
     const int base = p.q.base;
     const int row = min(wrow0 + col, p.row0 + p.rows - 1);
     const int tq = token_of(a, row);
     const int pos = base + tq;
+    // (a copy: the compiler would leave a piece that trees' masks refer to in scratch memory, whose
+    // reads in the loop wait for the keys on their way)
+    const KvSeq sq = p.q;
     const int win = a.window > 0 ? a.window : 0x40000000;
     // (rows of a tree: all see the token before the new ones, and none is past the last new one)
     const int posmin = is_tree<AA> ? base - 1 : base + token_of(a, wrow0);
@@ -1458,7 +1456,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
           for (int q = 0; q < 4; ++q) {
             const int k0 = (q >> 1) * 32 + (q & 1) * 16 + hi * 8;
             uint32_t see;
-            if constexpr (is_tree<AA>) see = (uint32_t)(tree_sees(a, p.q, tq, tile) >> k0) & 0xffu;
+            if constexpr (is_tree<AA>) see = (uint32_t)(tree_sees(a, sq, tq, tile) >> k0) & 0xffu;
             else see = run_bits<8>(k0, pos - win + 1 - tile, pos - tile);
             const u32x4 vis = ones8<A>(see & ~(uint32_t)(bad >> k0));
 #pragma unroll
@@ -1482,7 +1480,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
     };
     auto mask = [&](f32x16(&s)[2], int tile, unsigned long long bad) __attribute__((always_inline)) {
       uint64_t row = 0;
-      if constexpr (is_tree<AA>) row = tree_sees(a, p.q, tq, tile) & ~(uint64_t)bad;
+      if constexpr (is_tree<AA>) row = tree_sees(a, sq, tq, tile) & ~(uint64_t)bad;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int k0 = (h >> 1) * 32 + (h & 1) * 16 + hi * 8;
@@ -1698,8 +1696,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
       if (__builtin_expect(__ballot(mine) != 0, 0)) {
         const auto dim = [&](int bit) { return (bit >> 4) * 32 + (bit >> 2 & 3) * 8 + hi * 4 + (bit & 3); };
         if constexpr (is_tree<AA>)
-          settle<A, D>(kv, ktab, vtab, max(tree_from(a, p.q, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
-                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, p.q, tq, t); });
+          settle<A, D>(kv, ktab, vtab, max(tree_from(a, sq, tq), p.key0), min(posmax, p.key1 - 1), max(deep - win + 1, p.key0),
+                       min(posmin, p.key1 - 1), mine, o, dim, [&](int t) { return tree_sees_few<8>(a, sq, tq, t); });
         else
           settle<A, D>(kv, ktab, vtab, max(pos - win + 1, p.key0), min(pos, p.key1 - 1), max(posmax - win + 1, p.key0),
                        min(posmin, p.key1 - 1), mine, o, dim, [](int) { return 0xffu; });
@@ -1735,7 +1733,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
       }
     }
     if (p.first >= 0) {
-      if (n_piece == 0 && tid == 0) tell(&piece);
+      if (n_piece == 0 && tid == 0) tell(&p);
       ++n_piece;
     }
     __syncthreads();  // the slots of this piece have been read
