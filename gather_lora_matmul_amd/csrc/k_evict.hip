@@ -278,13 +278,15 @@ __device__ __forceinline__ void emit(SelectShared<THREADS, BINS>& sh, const Bord
   }
 }
 
-// ---- caches of up to a chunk: a block for each --------------------------------------
+// ---- caches of up to 16384 tokens: a block for each ---------------------------------
 // A block has a (sequence, head) with its ranks in registers: the 11 leading bits of all of
 // them in bins, then the few that share the border's bin compared one with another.  Bound by
 // its rounds through LDS (about a dozen barriers): the fewest waves that hold the ranks wait
 // the least for one another.  2048 heads of up to 2048 tokens take 15.1 us with 256 threads
 // (with 128 17.8, 512 20.3, 1024 26; a wave by itself for each head 17.6; ranks that wait for
 // the page ids 15.7), half of it for the weights and the look for missing pages.
+constexpr int kBlockTokens = 16384;
+
 template <int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t* __restrict__ counts) {
   constexpr int W = THREADS / 64, BINS = 2048;
@@ -856,19 +858,22 @@ hipError_t compact(const CompactArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Caches of up to a chunk's tokens, as far as the host can tell, are one launch, or two where
-// one block would have to look at too many page ids of the other heads.
+// Caches of up to 16384 tokens, as far as the host can tell, are one launch, or two where
+// one block would have to look at too many page ids of the other heads.  Many heads go to blocks
+// of fewer threads, of which a CU has more at a time: us with 512 / 1024 threads, 2048 heads of 2000 to
+// 4000 tokens 33 / 77, of 4100 to 8100 49 / 87, 512 heads of 8200 to 16000 36 / 44; 4 heads of 3000 6.3 /
+// 7.3, of 8000 9.2 / 8.4, of 10845 13.7 / 12.0 (in chunks 21).
 static int64_t select_most(const KvView& v, int64_t w_ld) { return std::min<int64_t>((int64_t)v.nb * v.T, w_ld); }
 static bool counts_apart(const KvView& v) { return (int64_t)2 * v.H * v.nb > 8192; }
 
 size_t select_workspace(int32_t n_seqs, int32_t H, int64_t tokens) {
   const size_t pairs = (size_t)n_seqs * H;
-  return std::max(pairs * sizeof(int32_t), tokens > kChunk ? pairs * LongSpace::bytes((int)((tokens + kChunk - 1) / kChunk)) : 0);
+  return std::max(pairs * sizeof(int32_t), tokens > kBlockTokens ? pairs * LongSpace::bytes((int)((tokens + kChunk - 1) / kChunk)) : 0);
 }
 
 hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
   const int64_t most = select_most(a.kv, a.w_ld);
-  if (most > kChunk) {
+  if (most > kBlockTokens) {
     const int chunks = (int)((most + kChunk - 1) / kChunk);
     const dim3 grid(a.kv.H, chunks, a.kv.n_seqs);
     hipLaunchKernelGGL(k_select_bins, grid, dim3(kLongThreads), 0, s, a, chunks);
@@ -882,8 +887,12 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
     counts = reinterpret_cast<int32_t*>(a.ws);
     hipLaunchKernelGGL(k_select_count, grid, dim3(64), 0, s, a, counts);
   }
-  if (most <= 2048) hipLaunchKernelGGL((k_select<256, 8>), grid, dim3(256), 0, s, a, counts);
-  else hipLaunchKernelGGL((k_select<1024, 8>), grid, dim3(1024), 0, s, a, counts);
+  const bool few = (int64_t)a.kv.H * a.kv.n_seqs <= 256;   // a block a CU
+  const auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, a, counts); };
+  if (most <= 2048) run(k_select<256, 8>, 256);
+  else if (most <= 4096) run(k_select<512, 8>, 512);
+  else if (most <= 8192) few ? run(k_select<1024, 8>, 1024) : run(k_select<512, 16>, 512);
+  else few ? run(k_select<1024, 16>, 1024) : run(k_select<512, 32>, 512);
   return hipGetLastError();
 }
 

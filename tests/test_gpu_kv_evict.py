@@ -364,6 +364,15 @@ def test_selection_of_absent_and_unweighed_tokens():
             check_selection(c, some_weights(c, 500, 8, "random"), 60, 3, 9, lens=bad)
 
 
+@pytest.mark.parametrize("lens", [(4097, 8192, 5000), (8193, 16384, 3)])
+def test_selection_of_many_heads_of_long_caches(lens):
+    # more heads than the device has compute units
+    lens = [lens[i % 3] if i % 9 < 3 else 30 for i in range(36)]
+    with empty_case(8, lens, seed=103, page=16384) as c:
+        check_selection(c, some_weights(c, max(lens), 7, "ties"), 700, 4, 100)
+        check_selection(c, some_weights(c, max(lens), 8, "random"), 2500)
+
+
 def test_counts_past_32_bits_are_refused():
     with empty_case(1, [20], seed=90) as c:
         w = torch.rand((1, 1, 20), device="cuda")
