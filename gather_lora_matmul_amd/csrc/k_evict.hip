@@ -136,7 +136,7 @@ struct SelectShared {
   alignas(16) uint32_t key[THREADS];   // ranks that begin alike, where they are few, and their tokens
   alignas(16) int index[THREADS];
   int part[THREADS / 64], part2[THREADS / 64];
-  uint32_t found[2];
+  uint32_t found[3];
   int last;
   uint32_t fill;
 };
@@ -146,9 +146,10 @@ struct Border {
   int last;
 };
 // The bin, from the top, in which the need-th of the ranks in sh.bins lies; need becomes what
-// that bin has to give.
+// that bin has to give, `count` what it has.  No wave reads sh.bins after the last barrier here:
+// another one may be clearing them by then.
 template <int NB, int THREADS, int BINS>
-__device__ __forceinline__ uint32_t find_bin(SelectShared<THREADS, BINS>& sh, uint32_t& need) {
+__device__ __forceinline__ uint32_t find_bin(SelectShared<THREADS, BINS>& sh, uint32_t& need, uint32_t& count) {
   constexpr int W = THREADS / 64, EACH = NB > THREADS ? NB / THREADS : 1;
   static_assert(NB <= BINS && (NB % THREADS == 0 || THREADS % NB == 0), "bins divide over the threads");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -167,23 +168,27 @@ __device__ __forceinline__ uint32_t find_bin(SelectShared<THREADS, BINS>& sh, ui
 #pragma unroll
   for (int w = 0; w < W; ++w) sum += w < wave ? (uint32_t)sh.part[w] : 0u;
   if (sum >= need && sum - own < need) {   // one thread
-    uint32_t before = sum - own, at = low, left = need;
+    uint32_t before = sum - own, at = low, left = need, has = own;
 #pragma unroll
     for (int i = EACH - 1; i >= 0; --i) {
       const bool here = before < need && before + bin[i] >= need;
       at = here ? low + i : at;
       left = here ? need - before : left;
+      has = here ? bin[i] : has;
       before += bin[i];
     }
     sh.found[0] = at;
     sh.found[1] = left;
+    sh.found[2] = has;
   }
   __syncthreads();
   need = sh.found[1];
+  count = sh.found[2];
   return sh.found[0];
 }
 // Of ranks that begin with `prefix` down to bit `shift` the border, `need` of them above or
-// at it: the ranks that each(f) gives f(rank, token) for, in any order.  `count` of them.
+// at it: the ranks that each(f) gives f(rank, token) for, in any order.  `count` of them.  What
+// sh.bins had may be gone from the call on.
 template <int THREADS, int BINS, typename Each>
 __device__ __forceinline__ Border border_of(SelectShared<THREADS, BINS>& sh, uint32_t prefix, int shift, uint32_t need,
                                             uint32_t count, Each each) {
@@ -197,11 +202,8 @@ __device__ __forceinline__ Border border_of(SelectShared<THREADS, BINS>& sh, uin
       if (((uint64_t)x >> shift) == ((uint64_t)prefix >> shift)) atomicAdd(&sh.bins[(x >> next << less) & 2047u], 1u);
     });
     __syncthreads();
-    const uint32_t bin = find_bin<2048>(sh, need);
-    count = sh.bins[bin];
-    prefix |= bin >> less << next;
+    prefix |= find_bin<2048>(sh, need, count) >> less << next;
     shift = next;
-    __syncthreads();
   }
   if (count > THREADS) {   // equal ranks: the need-th token of them, bit by bit
     int last = 0;
@@ -349,8 +351,8 @@ __global__ __launch_bounds__(THREADS) void k_select(SelectArgs a, const int32_t*
     to_bins();
     __syncthreads();
   }
-  uint32_t need = (uint32_t)K;
-  const uint32_t bin = find_bin<BINS>(sh, need), count = sh.bins[bin];
+  uint32_t need = (uint32_t)K, count;
+  const uint32_t bin = find_bin<BINS>(sh, need, count);
   const Border b = border_of(sh, bin << 21, 21, need, count, each);
   emit(sh, b, 0, per, x, out, K);
 }
@@ -494,8 +496,8 @@ __global__ __launch_bounds__(kLongThreads) void k_select_list(SelectArgs a, int 
   __syncthreads();
   uint32_t x[kLongPer];
   to_ranks<kLongPer>(a.kv, r, j0 + wave * kLongPer * 64, kLongPer, wt, x);
-  uint32_t need = (uint32_t)K;
-  const uint32_t bin = find_bin<kLongBins>(sh, need);
+  uint32_t need = (uint32_t)K, count;
+  const uint32_t bin = find_bin<kLongBins>(sh, need, count);
   if (tid == (int)bin / PER) {   // the list's places before this chunk's
     uint32_t c = 0;
 #pragma unroll
