@@ -962,11 +962,7 @@ def _attend_args(cache: KvCache, batch: KvBatch, q, out, scale, window, lse, wor
     if lse is not None:
         _check_tensor(lse, "lse", 0, batch.desc.n_tokens * heads)
     wp, wb = _ws(workspace)
-    return (qp, q_ld, heads, float(scale), _window(window), op, out_ld, _dev_ptr(lse), wp, wb)
-
-
-def _window(window) -> int:
-    return _whole(window)
+    return (qp, q_ld, heads, float(scale), _whole(window), op, out_ld, _dev_ptr(lse), wp, wb)
 
 
 def _whole(n) -> int:
@@ -1008,7 +1004,7 @@ def prepare_kv_tree_build(q_start, parent, seen, depth, window: int = 0) -> Prep
         raise ValueError("seen: %d rows for %d tokens" % (seen.shape[0], n))
     return PreparedCall(_lib.lora_kv_tree_build,
                         (int(q_start.numel()) - 1, n, _dev_ptr(q_start), _dev_ptr(parent), tree.desc.words,
-                         _window(window), tree.desc.seen_dev, tree.desc.depth_dev),
+                         _whole(window), tree.desc.seen_dev, tree.desc.depth_dev),
                         "lora_kv_tree_build", (q_start, parent, seen, depth))
 
 
@@ -1041,7 +1037,7 @@ def prepare_kv_weigh(cache: KvCache, batch: KvBatch, q, lse, weights, scale: flo
     wp, wb = _ws(workspace)
     return PreparedCall(_lib.lora_kv_weigh,
                         (cache.pool, ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, q_ld, heads, float(scale),
-                         _window(window), _dev_ptr(lse), float(decay), old, wt, w_ld, wp, wb),
+                         _whole(window), _dev_ptr(lse), float(decay), old, wt, w_ld, wp, wb),
                         "lora_kv_weigh", (cache, batch, q, lse, weights, before, workspace))
 
 
