@@ -746,7 +746,7 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
   const int x = tid & 63;
   u32x4 k[KU];
   Gathered<E> v[VU > 0 ? VU : 1];
-  uint8_t sc[2] = {0, 0};
+  uint8_t sc = 0;
   float w = 0.f;
 #pragma unroll
   for (int u = 0; u < KU; ++u)
@@ -758,7 +758,7 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
     if (x0 < p.first + p.n - pos0) v[u] = gather_v<E>(kv.pages, st, x0, (u * 256 + tid) % D);
   }
   if (E == 16 && tid < 128 && st.from[tid >> 6][x] != kNone)
-    sc[0] = kv.scales[scale_at<E, D>(kv, tid >> 6, st.from[tid >> 6][x])];
+    sc = kv.scales[scale_at<E, D>(kv, tid >> 6, st.from[tid >> 6][x])];
   float* weights = a.weights ? a.weights + ((int64_t)s * kv.H + h) * a.w_ld : nullptr;
   if (weights && tid < N && st.w[tid] >= 0) w = weights[st.w[tid]];
   __syncthreads();
@@ -768,7 +768,7 @@ __global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
 #pragma unroll
   for (int u = 0; u < VU; ++u) place_v<E>(kv.pages, st, (u * 256 + tid) / D * E, (u * 256 + tid) % D, v[u]);
   if (E == 16 && tid < 128 && st.from[tid >> 6][x] != kNone)
-    kv.scales[scale_at<E, D>(kv, tid >> 6, st.to[tid >> 6][x])] = sc[0];
+    kv.scales[scale_at<E, D>(kv, tid >> 6, st.to[tid >> 6][x])] = sc;
   if (weights && tid < N && st.w[tid] >= 0) weights[pos0 + tid] = w;
 }
 
