@@ -370,7 +370,13 @@ __global__ __launch_bounds__(64) void k_select_count(SelectArgs a, int32_t* __re
 // of 100001 and 131071 tokens, 8 heads, to 16384 take 26 us (one block a head 161; chunks of
 // 4096 30): 7, 9 and 10 of the launches, none of which moves more than 13 MB.
 constexpr int kChunk = 8192, kLongThreads = 512, kLongPer = kChunk / kLongThreads, kLongBins = 4096;
-constexpr int kListed = 4096;   // ranks of the border's bin that have a place; with more, all are read again
+// Ranks of the border's bin (an eighth of an octave) that have a place in the list.  With more,
+// every block of the third launch reads its whole head again for each pass: a second one and a third
+// for ranks that lie close, a pass for each bit of a token's number too where they are equal.  4096 holds
+// the bins of 131071 log-normal weights with a sigma of 2 (1700 to 3100).  8 heads of them to 65536
+// take 26 us with sigma 2, 193 with 1 or 0.5; to 16384 25 to 26 with each, but 2.04 ms if all
+// weights are equal or most are 0.
+constexpr int kListed = 4096;
 
 struct ChunkInfo {
   int32_t present;   // tokens with pages

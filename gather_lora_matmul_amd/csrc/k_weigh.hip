@@ -98,14 +98,19 @@ __device__ __forceinline__ float old_weight(const WeighArgs& a, const Unit& u, i
 }
 
 // ---- up to 32 rows a head and sequence ---------------------------------------------
-// A wave for itself: KT keys straight to registers, the rows in tiles of 16.  Bound by the
-// reads of K: a wave's units are neighbours, the next one's keys are on their way while it
-// works on one, its page ids while it loads one.  64 sequences of 20 to 2048 tokens, 32 heads on
-// 32, in FP8 (268 MB of keys) take 74 us, 3.6 TB/s; with 48 keys in three waves a SIMD 75, with 32 in four 74.5.
+// A wave for itself: KT keys straight to registers, the rows in tiles of 16.  A wave's units are
+// neighbours; the next one's keys are asked for ahead of this one's products, the page ids of the
+// one after behind them.  Bound by the reads of K, which do not overlap the products in full: what a token
+// had before is faded, and in FP8 a scale byte widened, as soon as it is there, and these are the
+// last of a unit's loads, so that a wave waits for all of them before it multiplies.  64 sequences
+// of 20 to 2048 tokens, 32 heads on 32, in FP8 (268 MB of keys) take 74 us, 3.6 TB/s (with nothing
+// from before 69; with 48 keys in three waves a SIMD 75, with 32 in four 74.5), in bf16 128, 4.2 TB/s (123).
 // A key's exponentials are 16 a row tile whether its rows are there or not, and every tile
-// of rows is read again for each unit: above 32 rows the tiles below are faster.  us of rows /
-// tiles: 16-bit 32 heads on 32, 17 rows over 500 tokens 5.0 / 11.9; 24 rows over 30000 20 / 30; 32 rows
-// over 5000 16 / 25; 48 rows, 4 sequences over 2500, 79 / 62; 64 rows 93 / 58, in FP8 57 / 48.
+// of rows is read again for each unit: from about 32 rows on the tiles below are faster.  us of rows /
+// tiles: bf16, 32 heads on 32, 17 rows over 500 tokens 5.0 / 7.8; 24 over 5000 15.9 / 17.0, 32 16.2 /
+// 15.1; four sequences over 2500, 24 rows 25.5 / 23.9 (FP8 19.0 / 21.8), 32 27.1 / 21.4 (20.1 / 19.9),
+// 48 34.4 / 26.4 (23.9 / 25.4), 64 41.5 / 23.5 (28.0 / 22.5); 64 heads on 8, 24 rows over 30000 20.0 /
+// 19.3, 40 24.8 / 20.9, 64 30.9 / 19.7.
 constexpr int kFewRows = 32, kRowsBlocks = 2;   // rows; blocks a CU
 template <typename A, typename KV, int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kRowsBlocks, kRowsBlocks))) void k_weigh_rows(WeighArgs a) {
@@ -261,8 +266,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kRowsBlocks
 // A block's four waves have 64 keys each, in registers for all of the rows, which go
 // through LDS in steps of 128 (two slots, one barrier a step).  32 products of 32x32x16 and 32
 // exponentials of a wave cost about the same, so they are woven: the last 2048 of 16384
-// tokens, 64 heads on 8 in bf16, take 600 us, 860 TFLOP/s, at the 1.9 to 2.2 GHz that the
-// card holds under them.  (Products of one step, then its exponentials: 640.)
+// tokens, 64 heads on 8 in bf16, take 600 to 620 us, 830 to 860 TFLOP/s, at 2.0 to 2.1 GHz
+// (its cycles by its time).  (Products of one step, then its exponentials: 640.)
 // Rows in LDS, 64 of them in B blocks of 1 KB, each what one load brings: row r is number r / B
 // of block r % B, and a block begins 16 bytes further in the banks than the one before.  The
 // loads cover whole rows, a product's lanes read all banks alike, and all operands of a lane

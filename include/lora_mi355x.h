@@ -452,8 +452,8 @@ typedef struct {
   const int32_t* q_start_dev;  /* [n_seqs + 1], ascending                        */
   const int32_t* kv_len_dev;   /* [n_seqs]                                       */
   const int32_t* table_dev;
-  int32_t two_terms;       /* lora_kv_attend: not 0 takes the weights in two terms in
-                              long work too                                      */
+  int32_t two_terms;       /* lora_kv_attend, lora_kv_attend_tree: not 0 takes the
+                              weights in two terms in long work too              */
 } lora_kv_batch;
 
 /* Tokens of a page (T), pages of one block of T tokens (2 n_kv_heads) and bytes
@@ -587,8 +587,10 @@ lora_status lora_kv_tree_build(int32_t n_seqs, int32_t n_tokens, const int32_t* 
  * kv_len - q_len that were cached before the new ones (if window > 0, those with j >
  * kv_len - q_len + d - window), and the new tokens that its row of seen has, in
  * any order, itself only if its bit is there.  Depths below 0 count as 0.  p goes in
- * one 16-bit term (two_terms: in two) from 80 rows a head and sequence on average and
- * seven tiles a compute unit.  Everything else, the workspace and its size
+ * one 16-bit term (two_terms: in two, for up to half as much time again) from 80 rows a
+ * head and sequence on average where full tables (or the window) would give every compute
+ * unit seven tiles of 256 rows and 64 keys: as in lora_kv_attend the tables' width decides,
+ * not the lengths.  Everything else, the workspace and its size
  * (lora_kv_attend_workspace_size) too, is as in lora_kv_attend, which a chain's rows
  * agree with within both calls' roundings. */
 lora_status lora_kv_attend_tree(const lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
@@ -672,8 +674,13 @@ lora_status lora_kv_weigh(const lora_pool* pool, const lora_kv_desc* kv, const l
  * first (NaN: below all others); absent tokens and those from w_ld on are never among
  * them.  n_keep [n_seqs] = min(budget, the fewest present tokens of a head), keep [n_seqs]
  * [n_kv_heads][keep_ld] (keep_ld >= budget): their positions, ascending; entries from
- * n_keep on are left.  q_start and the batch's tokens play no part.  Stream-ordered, no
- * wait, no allocation; workspace_dev as for lora_kv_weigh, of
+ * n_keep on are left.  Where n_keep is below the present ones of a head's first and latest
+ * tokens (pages are missing in another head), the lowest positions of them stay and the newest
+ * tokens are left out.  q_start and the batch's tokens play no part.  Launches and workspace
+ * follow the tables' width, not the lengths: one launch for up to 16384 tokens (or w_ld of no
+ * more; two where a sequence has over 8192 page ids), three for more; 4 bytes a (sequence,
+ * head) for tables of up to 16384 tokens, for wider ones 32 KB and 8 KB more for every 8192
+ * tokens.  Stream-ordered, no wait, no allocation; workspace_dev as for lora_kv_weigh, of
  * lora_kv_select_workspace_size bytes. */
 lora_status lora_kv_select_workspace_size(const lora_pool* pool, const lora_kv_desc* kv,
                                           const lora_kv_batch* batch, size_t* bytes);
@@ -690,7 +697,9 @@ lora_status lora_kv_select(const lora_pool* pool, const lora_kv_desc* kv, const 
  * page may be shared by two places of the call.  A place keeps what it has where the number
  * names no cached token, its K (V) also where one of the two has no page for it, its weight
  * where one of the two is not below w_ld; nothing else is touched, the places behind
- * included.  kv_len is not changed: the caller's next one is first + n_keep.
+ * included.  kv_len is not changed: the caller's next one is first + n_keep.  Later calls
+ * go by the places: after an eviction a token's place is no longer its position in the text
+ * (rotary embeddings are the caller's, and keys keep theirs), and a window counts places.
  * Stream-ordered, no wait, no allocation. */
 lora_status lora_kv_compact(lora_pool* pool, const lora_kv_desc* kv, const lora_kv_batch* batch,
                             const int32_t* keep_dev, int32_t keep_heads, int64_t keep_ld,
