@@ -666,3 +666,15 @@ def test_selection_in_tables_wider_than_the_caches():
             w = some_weights(c, 18000, 10, kind)
             for budget, sinks, recent in ((0, 0, 0), (4, 4, 0), (250, 3, 40), (8999, 0, 0), (9000, 0, 9000)):
                 check_selection(c, w, budget, sinks, recent)
+
+
+@pytest.mark.parametrize("kind", ["equal", "near", "zeros"])
+@pytest.mark.parametrize("lens", [(2048, 300), (4096, 2049), (8192, 5000), (16384, 8193), (30000, 16385)])
+def test_selection_whose_border_has_more_ranks_than_a_block_has_threads(lens, kind):
+    with empty_case(2, list(lens), seed=104, page=16384) as c:
+        w = some_weights(c, max(lens), 11, "random" if kind == "zeros" else kind)
+        if kind == "zeros":
+            w[torch.rand(w.shape, device="cuda", generator=c.gen) < 0.98] = 0.0
+        for budget, sinks, recent in ((max(lens) // 3, 4, 100), (max(lens) // 2, 0, 0)):
+            log("[case] select crowded %s %s budget %d" % (kind, lens, budget))
+            check_selection(c, w, budget, sinks, recent)
